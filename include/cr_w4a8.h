@@ -550,6 +550,63 @@ cr_status cr_gemm_s8(const int8_t *xq, const float *xs, const int8_t *w8, const 
                      int32_t *acc_out, cr_stream_t stream);
 
 /*
+ * (19) RMS norm with the residual's addition, rotated and quantised: what
+ * stands between two layers, in one kernel.
+ *
+ * The pages leave the norm to the model; its output here is exactly what (1)
+ * hands the contractions (ai-toolkit convrot_w4a8_quant.py, prepare_act).
+ *   h[m, k]  = bf16( x[m, k] + residual[m, k] )         (h = x without a residual)
+ *   rs[m]    = fp32( 1 / sqrt( sum_k h^2 / K + eps ) )  (sum, quotient and root in fp64)
+ *   v[m, k]  = (h * rs) * gamma[k]                      (two fp32 operations)
+ *   xq, xs   = (1) applied to v: the same rotation order, scale and rounding
+ *   rows M <= m < MP:  xq = 0, xs = 1
+ *
+ * x, residual [M, K] bf16 bits; residual may be NULL.  gamma [K] bf16 or fp32
+ * per gamma_dtype.  h [M, K] bf16 is written when a residual is given (and
+ * required then); it may be x or residual itself, but not overlap them
+ * otherwise; without a residual it is not written and may be NULL.
+ * xq [MP, K] int8, xs [MP] fp32, written.  rs [M] fp32 or NULL: what (20) needs.
+ * eps in [1e-30, 1e30] (CR_ERR_INVALID_ARG otherwise); v must meet the bound
+ * on activations.  MP, act_qmax as in (1).
+ */
+cr_status cr_rmsnorm_quant_act(const uint16_t *x, const uint16_t *residual, const void *gamma,
+                               cr_out_dtype gamma_dtype, double eps, int64_t M, int64_t K, int64_t MP, int act_qmax,
+                               uint16_t *h, int8_t *xq, float *xs, float *rs, cr_stream_t stream);
+
+/*
+ * (20) The gradient of (19), straight through the quantiser.
+ *
+ * dr [M, K] bf16 is the gradient of the layer's rotated input, as (13), (22)
+ * and (23) return it (added up by the caller where several layers read it).
+ *   dv = dr rotated (the rotation is its own inverse and transpose), fp32
+ *   xh = h * rs;  g = dv * gamma;  c = sum_k(g * xh) / K
+ *   dx[m, k]  = bf16( rs * (g - xh * c) [+ dres[m, k]] )
+ *   dgamma[k] = sum_m dv * xh
+ * in fp32.  dx is the gradient of h: of x and of the residual alike.
+ *
+ * h [M, K] bf16 and rs [M] fp32 from (19) (h = x without a residual); gamma as
+ * there.  dres [M, K] bf16 or NULL: the gradient that reaches h by the residual
+ * path, added in.  dx may be dr or dres itself, but not overlap them otherwise,
+ * nor h.  dgamma [K] fp32, or NULL when it is not wanted; when given, work
+ * holds cr_rmsnorm_backward_work_bytes(M, K) bytes (16-byte aligned;
+ * CR_ERR_INVALID_ARG when smaller), else it is not used.  dgamma is the same
+ * from run to run (no atomics).  M == 0 writes dgamma = 0.
+ */
+int64_t cr_rmsnorm_backward_work_bytes(int64_t M, int64_t K);
+cr_status cr_rmsnorm_backward(const uint16_t *dr, const uint16_t *h, const void *gamma, cr_out_dtype gamma_dtype,
+                              const float *rs, const uint16_t *dres, int64_t M, int64_t K, uint16_t *dx,
+                              float *dgamma, void *work, int64_t work_bytes, cr_stream_t stream);
+
+/*
+ * (21) The block rotation alone: out = bf16( x rotated ), in the fp32 order of
+ * (1) (h3-rs src/weights.rs, rotate_activation).  The rotation is its own
+ * inverse and transpose, so this is also the rotation's backward: it takes the
+ * gradient that (13) returns for a layer back to the layer's unrotated input.
+ * x, out [M, K] bf16 bits; out may be x itself, but not overlap it otherwise.
+ */
+cr_status cr_rotate(const uint16_t *x, int64_t M, int64_t K, uint16_t *out, cr_stream_t stream);
+
+/*
  * (15) Self-test of the failure path: launches one CTA whose thread waits,
  * with the library's bounded wait, on an mbarrier that nothing completes.
  * After limit_ns (1 ms .. 1 s, CR_ERR_INVALID_ARG otherwise) the wait gives

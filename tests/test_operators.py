@@ -1,0 +1,118 @@
+"""The operators around the layer without a GPU: argument checks of the C ABI
+(nothing is launched on these paths), and the restatements the GPU tests use
+against each other and against the oracle."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import oracle
+import w4a8_codebook_quantized_b200 as cr
+from w4a8_codebook_quantized_b200 import build, inputs
+
+from operator_refs import hadamard, norm_backward, norm_quant, rotate32, rotate64
+
+A, B, C = 0x10000, 0x4000000, 0x8000000  # aligned stand-in addresses far apart; never dereferenced
+MIS = 0x10008
+OK, INVALID, UNSUPPORTED, ALIGNMENT = (cr.CR_OK, cr.CR_ERR_INVALID_ARG, cr.CR_ERR_UNSUPPORTED, cr.CR_ERR_ALIGNMENT)
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return cr.lib()
+
+
+def test_norm_quant_validation(L):
+    def call(x=A, res=None, gamma=A, gdt=1, eps=1e-6, M=4, K=256, MP=4, qmax=127, h=None, xq=B, xs=A, rs=A):
+        return L.cr_rmsnorm_quant_act(x, res, gamma, gdt, eps, M, K, MP, qmax, h, xq, xs, rs, None)
+
+    assert call(M=-1) == INVALID and call(MP=3) == INVALID and call(qmax=0) == INVALID and call(qmax=128) == INVALID
+    assert call(gdt=2) == INVALID
+    for eps in (0.0, -1.0, 1e-31, 1e31, float("nan"), float("inf")):
+        assert call(eps=eps) == INVALID
+    assert call(K=384) == UNSUPPORTED and call(K=0) == UNSUPPORTED and call(K=131072 + 256) == UNSUPPORTED
+    assert call(M=1, MP=2 ** 31) == UNSUPPORTED
+    assert call(x=None) == INVALID and call(gamma=None) == INVALID and call(xq=None) == INVALID
+    assert call(res=C) == INVALID                       # a residual needs h
+    assert call(res=C, h=A + 512) == INVALID            # h overlaps x without being x
+    assert call(res=C, h=C + 512) == INVALID
+    for name in ("x", "gamma", "xq", "xs", "rs"):
+        assert call(**{name: MIS}) == ALIGNMENT
+    assert call(res=MIS, h=B) == ALIGNMENT and call(res=C, h=MIS) == ALIGNMENT
+    assert call(M=0, MP=0, x=None, gamma=None, xq=None, xs=None, rs=None) == OK
+
+
+def test_norm_backward_validation(L):
+    need = L.cr_rmsnorm_backward_work_bytes(4, 256)
+    assert need == 4 * 256 * 4
+    assert L.cr_rmsnorm_backward_work_bytes(0, 256) == 0 and L.cr_rmsnorm_backward_work_bytes(4, 300) == 0
+
+    def call(dr=A, h=B, gamma=A, gdt=0, rs=A, dres=None, M=4, K=256, dx=C, dg=A, work=A, wb=need):
+        return L.cr_rmsnorm_backward(dr, h, gamma, gdt, rs, dres, M, K, dx, dg, work, wb, None)
+
+    assert call(M=-1) == INVALID and call(gdt=5) == INVALID and call(K=300) == UNSUPPORTED
+    assert call(M=2 ** 31) == UNSUPPORTED
+    for name in ("dr", "h", "gamma", "rs", "dx"):
+        assert call(**{name: None}) == INVALID
+        assert call(**{name: MIS}) == ALIGNMENT
+    assert call(dres=MIS) == ALIGNMENT and call(dg=MIS) == ALIGNMENT and call(work=MIS) == ALIGNMENT
+    assert call(wb=need - 1) == INVALID and call(work=None) == INVALID
+    assert call(dx=B) == INVALID and call(dx=A + 512) == INVALID
+    assert call(M=0, dr=None, h=None, gamma=None, rs=None, dx=None, dg=None, work=None, wb=0) == OK
+
+
+def test_rotate_validation(L):
+    f = L.cr_rotate
+    assert f(A, -1, 256, B, None) == INVALID and f(A, 2, 384, B, None) == UNSUPPORTED
+    assert f(None, 2, 256, B, None) == INVALID and f(A, 2, 256, None, None) == INVALID
+    assert f(MIS, 2, 256, B, None) == ALIGNMENT and f(A, 2, 256, MIS, None) == ALIGNMENT
+    assert f(A, 2, 256, A + 512, None) == INVALID
+    assert f(A, 2 ** 31, 256, B, None) == UNSUPPORTED
+    assert f(None, 0, 256, None, None) == OK
+
+
+def test_rotation_restatements_agree():
+    """H is symmetric and its own inverse; the fp32 order against the matrix
+    (8 additions and as many roundings, each at most the block's sum of
+    magnitudes over 16)."""
+    H = hadamard()
+    assert np.array_equal(H, H.T) and np.allclose(H @ H, np.eye(256), atol=1e-12)
+    v = np.random.default_rng(0).standard_normal((3, 512))
+    v32 = v.astype(np.float32).astype(np.float64)
+    bound = 12 * 2.0 ** -24 * np.abs(v32).reshape(3, 2, 256).sum(2).repeat(256, 1) / 16
+    assert (np.abs(rotate32(v32) - rotate64(v32)) <= bound).all()
+    assert np.allclose(rotate64(rotate64(v)), v, atol=1e-12)
+
+
+def test_norm_restatement_quantises_as_the_oracle():
+    """With a unit weight and rows of mean square 1 the norm changes nothing,
+    and its int8 activations are the oracle's of the same rows."""
+    rng = np.random.default_rng(1)
+    x = rng.choice([-1.0, 1.0], size=(5, 512))
+    bits = (x.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    xq, xs, h, rs = norm_quant(x, np.ones(512, np.float32), 2.0 ** -60, mp=8)
+    q_ref, s_ref = oracle.rotate_quant_act(bits, 8, 127)
+    assert (rs == 1).all() and np.array_equal(h, x)
+    assert np.array_equal(xq, q_ref) and np.array_equal(xs, s_ref)
+
+
+def test_norm_gradient_formula_against_differences():
+    rng = np.random.default_rng(2)
+    M, K, eps = 3, 512, 1e-5
+    h, dr, gamma = rng.standard_normal((M, K)), rng.standard_normal((M, K)), 1 + 0.1 * rng.standard_normal(K)
+
+    def loss(hh, gg):
+        return (dr * rotate64(hh / np.sqrt((hh ** 2).mean(1, keepdims=True) + eps) * gg)).sum()
+
+    rs = 1 / np.sqrt((h ** 2).mean(1) + eps)
+    dx, dg, _, _ = norm_backward(dr, h, gamma, rs)
+    step = 1e-6
+    for m, k in ((0, 0), (1, 300), (2, 511)):
+        e = np.zeros_like(h)
+        e[m, k] = step
+        assert abs((loss(h + e, gamma) - loss(h - e, gamma)) / (2 * step) - dx[m, k]) < 1e-6
+    for k in (0, 200, 511):
+        e = np.zeros(K)
+        e[k] = step
+        assert abs((loss(h, gamma + e) - loss(h, gamma - e)) / (2 * step) - dg[k]) < 1e-6

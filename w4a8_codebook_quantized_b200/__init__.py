@@ -31,6 +31,7 @@ __all__ = [
     "interleave_gate_up", "cr_w4a8_quantize_rotated", "cr_w4a8_assign_codes",
     "cr_w4a8_ste_backward", "cr_w4a8_dequant_t_bf16", "cr_selftest_wait_timeout", "cr_gemm_s8",
     "cr_w4a8_gemm_ws", "cr_w4a8_linear_ws", "cr_w4a8_ste_backward_ws", "cr_mma_i8_peak",
+    "cr_rmsnorm_quant_act", "cr_rmsnorm_backward", "cr_rotate",
     "cr_status_string", "cr_version",
     "gemv_rows",
 ]
@@ -109,6 +110,12 @@ def lib() -> ctypes.CDLL:
             L.cr_mma_i8_peak.argtypes = [i64, ctypes.POINTER(ctypes.c_double), P]
             L.cr_w4a8_linear_ws.argtypes = [P, P, P, P, P, P, i64, i64, i64, i32, i32, P, P, P, P, P]
             L.cr_w4a8_ste_backward_ws.argtypes = [P, P, P, P, P, i64, i64, i64, P, P, P]
+            f64 = ctypes.c_double
+            L.cr_rmsnorm_quant_act.argtypes = [P, P, P, i32, f64, i64, i64, i64, i32, P, P, P, P, P]
+            L.cr_rmsnorm_backward_work_bytes.argtypes = [i64, i64]
+            L.cr_rmsnorm_backward_work_bytes.restype = i64
+            L.cr_rmsnorm_backward.argtypes = [P, P, P, i32, P, P, i64, i64, P, P, P, i64, P]
+            L.cr_rotate.argtypes = [P, i64, i64, P, P]
             LP = ctypes.POINTER(CrLayer)
             L.cr_w4a8_gemv_grouped.argtypes = [P, P, P, i64, i64, LP, i32, i32, P]
             L.cr_w4a8_linear_grouped.argtypes = [P, P, i64, i64, LP, i32, i32, i32, P, P, P]
@@ -224,6 +231,30 @@ def _out_code(dtype) -> int:
     if dtype == torch.float32:
         return CR_OUT_F32
     raise TypeError(f"out dtype must be bfloat16 or float32, got {dtype}")
+
+
+def _on_stream(fn):
+    """_on_device, and with `stream` (a torch Stream or a raw handle) made the
+    current stream for the call, so that the outputs and work buffers the call
+    allocates belong to the stream that uses them: the caching allocator may
+    hand a freed buffer to later work of the stream it was allocated on only."""
+    import functools
+    body = _on_device(fn)
+
+    @functools.wraps(fn)
+    def wrapper(*args, stream=None, **kwargs):
+        if stream is None:
+            return body(*args, **kwargs)
+        torch = _torch()
+        dev = _cuda_device_of(args, kwargs)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        elif dev is not None and stream.device != dev:
+            raise ValueError(f"stream of {stream.device}, the tensors are on {dev}")
+        with torch.cuda.stream(stream):
+            return body(*args, **kwargs)
+
+    return wrapper
 
 
 def gemv_rows(m: int) -> int:
@@ -949,6 +980,114 @@ def cr_w4a8_dequant_t_bf16(qdata, srel, codebook, s_channel, wt=None, stream=Non
     _check(lib().cr_w4a8_dequant_t_bf16(_ptr(qdata), _ptr(srel), _ptr(codebook), _ptr(s_channel), N, K, _ptr(wt),
                                         _stream(stream)), "cr_w4a8_dequant_t_bf16")
     return wt
+
+
+# ---------------------------------------------------------------- between the layers
+
+def _gamma(gamma, K):
+    torch = _torch()
+    _need(gamma, "gamma", (torch.bfloat16, torch.float32), shape=(K,))
+    return CR_OUT_BF16 if gamma.dtype == torch.bfloat16 else CR_OUT_F32
+
+
+@_on_stream
+def cr_rmsnorm_quant_act(x, gamma, eps: float = 1e-6, residual=None, mp: Optional[int] = None, act_qmax: int = 127,
+                         h=None, xq=None, xs=None, rs=None):
+    """RMS norm of x (+ residual), rotated and quantised for the next layer:
+    x [M, K] bf16, gamma [K] bf16 or fp32 -> (xq int8 [MP, K], xs fp32 [MP],
+    h bf16 [M, K], rs fp32 [M]).  h = x + residual is the new residual stream
+    (x itself without a residual; pass h=x or h=residual to update in place);
+    h and rs are what cr_rmsnorm_backward needs.  Rows >= M of xq / xs are 0 / 1."""
+    torch = _torch()
+    _need(x, "x", (torch.bfloat16,), 2)
+    M, K = x.shape
+    code = _gamma(gamma, K)
+    MP = M if mp is None else int(mp)
+    if residual is not None:
+        _need(residual, "residual", (torch.bfloat16,), shape=(M, K))
+        if h is None:
+            h = torch.empty_like(x)
+        _need(h, "h", (torch.bfloat16,), shape=(M, K))
+    elif h is not None and h is not x:
+        raise ValueError("h is an output of the residual's addition: without a residual it is x")
+    if xq is None:
+        xq = torch.empty(MP, K, dtype=torch.int8, device=x.device)
+    else:
+        _need(xq, "xq", (torch.int8,), shape=(MP, K))
+    if xs is None:
+        xs = torch.empty(MP, dtype=torch.float32, device=x.device)
+    else:
+        _need(xs, "xs", (torch.float32,), shape=(MP,))
+    if rs is None:
+        rs = torch.empty(M, dtype=torch.float32, device=x.device)
+    else:
+        _need(rs, "rs", (torch.float32,), shape=(M,))
+    _check(lib().cr_rmsnorm_quant_act(_ptr(x), _ptr(residual), _ptr(gamma), code, float(eps), M, K, MP, int(act_qmax),
+                                      _ptr(h) if residual is not None else None, _ptr(xq), _ptr(xs), _ptr(rs),
+                                      _stream(None)), "cr_rmsnorm_quant_act")
+    return xq, xs, (x if residual is None else h), rs
+
+
+@_on_stream
+def cr_rmsnorm_backward(dr, h, gamma, rs, dres=None, dx=None, dgamma=None, work=None, with_dgamma: bool = True):
+    """The gradient of cr_rmsnorm_quant_act: dr [M, K] bf16, the gradient of
+    the layer's rotated input (as the layers' backward calls return it), with h
+    and rs of the forward -> (dx bf16 [M, K], dgamma fp32 [K], or None with
+    with_dgamma=False).  dres is the gradient reaching h by the residual path;
+    dx may be dr or dres itself.  work: uint8, at least
+    lib().cr_rmsnorm_backward_work_bytes(M, K) bytes."""
+    torch = _torch()
+    _need(dr, "dr", (torch.bfloat16,), 2)
+    M, K = dr.shape
+    _need(h, "h", (torch.bfloat16,), shape=(M, K))
+    code = _gamma(gamma, K)
+    _need(rs, "rs", (torch.float32,), shape=(M,))
+    if dres is not None:
+        _need(dres, "dres", (torch.bfloat16,), shape=(M, K))
+    if dx is None:
+        dx = torch.empty(M, K, dtype=torch.bfloat16, device=dr.device)
+    else:
+        _need(dx, "dx", (torch.bfloat16,), shape=(M, K))
+    if with_dgamma:
+        if dgamma is None:
+            dgamma = torch.empty(K, dtype=torch.float32, device=dr.device)
+        else:
+            _need(dgamma, "dgamma", (torch.float32,), shape=(K,))
+        work = _work_buffer(work, lib().cr_rmsnorm_backward_work_bytes(M, K), dr.device)
+    elif dgamma is not None:
+        raise ValueError("dgamma given with with_dgamma=False")
+    else:
+        work = None
+    _check(lib().cr_rmsnorm_backward(_ptr(dr), _ptr(h), _ptr(gamma), code, _ptr(rs), _ptr(dres), M, K, _ptr(dx),
+                                     _ptr(dgamma), _ptr(work), 0 if work is None else work.numel(), _stream(None)),
+           "cr_rmsnorm_backward")
+    return dx, dgamma
+
+
+def _work_buffer(work, need: int, device):
+    """The caller's uint8 work buffer, checked, or one of `need` bytes."""
+    torch = _torch()
+    if work is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _need(work, "work", (torch.uint8,), 1)
+    if work.numel() < need:
+        raise ValueError(f"work has {work.numel()} bytes, {need} are needed")
+    return work
+
+
+@_on_stream
+def cr_rotate(x, out=None):
+    """The block rotation alone, x [M, K] bf16 -> bf16: also its own backward
+    (cr_w4a8_ste_backward returns the gradient of the rotated input).  out may
+    be x itself."""
+    torch = _torch()
+    _need(x, "x", (torch.bfloat16,), 2)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", (torch.bfloat16,), shape=x.shape)
+    _check(lib().cr_rotate(_ptr(x), x.shape[0], x.shape[1], _ptr(out), _stream(None)), "cr_rotate")
+    return out
 
 
 def cr_mma_i8_peak(iters: int, stream=None) -> float:

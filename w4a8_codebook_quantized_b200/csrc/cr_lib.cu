@@ -20,6 +20,7 @@
 #include "k_elementwise.cuh"
 #include "k_gemm.cuh"
 #include "k_gemv.cuh"
+#include "k_norm.cuh"
 #include "k_peak.cuh"
 #include "k_quant.cuh"
 #include "k_rotquant.cuh"
@@ -125,7 +126,7 @@ cr_status current_device(DeviceState **out)
         }
         if (d.usable && !have_encode_tiled())
             d.usable = false;
-        if (d.usable && cr::rq::set_attributes() != cudaSuccess) {
+        if (d.usable && (cr::rq::set_attributes() != cudaSuccess || cr::nm::set_attributes() != cudaSuccess)) {
             cudaGetLastError();
             d.usable = false;
         }
@@ -1110,6 +1111,141 @@ cr_status cr_w4a8_ste_backward_ws(const uint16_t *grad, const uint8_t *qdata, co
                                   uint16_t *dx, uint16_t *wt_work, cr_stream_t stream)
 {
     return ste_backward_impl(grad, qdata, srel, codebook, s_channel, M, N, K, dx, stream, true, wt_work);
+}
+
+// ---------------------------------------------------------------- norm and rotation
+
+namespace {
+// Whether [a, a + na) and [b, b + nb) share a byte (null pointers share none).
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
+{
+    if (!a || !b || na <= 0 || nb <= 0)
+        return false;
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    return pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
+}
+
+// The same, but for exactly the same buffer.
+bool overlap_other(const void *a, int64_t na, const void *b, int64_t nb)
+{
+    return a != b && overlap(a, na, b, nb);
+}
+
+bool bad_out_dtype(cr_out_dtype t) { return t != CR_OUT_BF16 && t != CR_OUT_F32; }
+}  // namespace
+
+cr_status cr_rmsnorm_quant_act(const uint16_t *x, const uint16_t *residual, const void *gamma,
+                               cr_out_dtype gamma_dtype, double eps, int64_t M, int64_t K, int64_t MP, int act_qmax,
+                               uint16_t *h, int8_t *xq, float *xs, float *rs, cr_stream_t stream)
+{
+    if (M < 0 || K < 0 || MP < M || act_qmax < 1 || act_qmax > 127 || bad_out_dtype(gamma_dtype))
+        return CR_ERR_INVALID_ARG;
+    if (!(eps >= 1e-30 && eps <= 1e30))
+        return CR_ERR_INVALID_ARG;
+    const cr_status k = check_k(K);
+    if (k != CR_OK)
+        return k;
+    if (MP > INT_MAX)
+        return CR_ERR_UNSUPPORTED;
+    if (MP == 0)
+        return CR_OK;
+    if (!xq || !xs || (M > 0 && (!x || !gamma || (residual && !h))))
+        return CR_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(h) || !aligned16(xq) ||
+        !aligned16(xs) || !aligned16(rs))
+        return CR_ERR_ALIGNMENT;
+    if (residual && (overlap_other(h, 2 * M * K, x, 2 * M * K) || overlap_other(h, 2 * M * K, residual, 2 * M * K)))
+        return CR_ERR_INVALID_ARG;
+    DeviceState *d = nullptr;
+    const cr_status ds = current_device(&d);
+    if (ds != CR_OK)
+        return ds;
+    cr::nm::FwdArgs a;
+    a.x = x;
+    a.res = residual;
+    a.gamma = gamma;
+    a.eps = eps;
+    a.M = M;
+    a.K = K;
+    a.qmax = act_qmax;
+    a.h = h;
+    a.xq = xq;
+    a.xs = xs;
+    a.rs = rs;
+    return launched(cr::nm::launch_fwd(a, MP, gamma_dtype == CR_OUT_BF16, stream));
+}
+
+int64_t cr_rmsnorm_backward_work_bytes(int64_t M, int64_t K)
+{
+    if (M <= 0 || check_k(K) != CR_OK)
+        return 0;
+    return cr::nm::backward_ctas(M, K) * K * 4;
+}
+
+cr_status cr_rmsnorm_backward(const uint16_t *dr, const uint16_t *h, const void *gamma, cr_out_dtype gamma_dtype,
+                              const float *rs, const uint16_t *dres, int64_t M, int64_t K, uint16_t *dx,
+                              float *dgamma, void *work, int64_t work_bytes, cr_stream_t stream)
+{
+    if (M < 0 || K < 0 || bad_out_dtype(gamma_dtype))
+        return CR_ERR_INVALID_ARG;
+    const cr_status k = check_k(K);
+    if (k != CR_OK)
+        return k;
+    if (M > INT_MAX)
+        return CR_ERR_UNSUPPORTED;
+    if (M > 0 && (!dr || !h || !gamma || !rs || !dx))
+        return CR_ERR_INVALID_ARG;
+    if (!aligned16(dr) || !aligned16(h) || !aligned16(gamma) || !aligned16(rs) || !aligned16(dres) ||
+        !aligned16(dx) || !aligned16(dgamma) || !aligned16(work))
+        return CR_ERR_ALIGNMENT;
+    if (M > 0 && dgamma && (!work || work_bytes < cr_rmsnorm_backward_work_bytes(M, K)))
+        return CR_ERR_INVALID_ARG;
+    if (overlap(dx, 2 * M * K, h, 2 * M * K) || overlap_other(dx, 2 * M * K, dr, 2 * M * K) ||
+        overlap_other(dx, 2 * M * K, dres, 2 * M * K))
+        return CR_ERR_INVALID_ARG;
+    if (M == 0 && !dgamma)
+        return CR_OK;
+    DeviceState *d = nullptr;
+    const cr_status ds = current_device(&d);
+    if (ds != CR_OK)
+        return ds;
+    if (M == 0)  // an empty sum
+        return launched(cudaMemsetAsync(dgamma, 0, (size_t)K * 4, stream));
+    cr::nm::BwdArgs a;
+    a.dr = dr;
+    a.h = h;
+    a.gamma = gamma;
+    a.rs = rs;
+    a.dres = dres;
+    a.M = M;
+    a.K = K;
+    a.dx = dx;
+    a.part = dgamma ? static_cast<float *>(work) : nullptr;
+    return launched(cr::nm::launch_bwd(a, gamma_dtype == CR_OUT_BF16, dgamma, stream));
+}
+
+cr_status cr_rotate(const uint16_t *x, int64_t M, int64_t K, uint16_t *out, cr_stream_t stream)
+{
+    if (M < 0 || K < 0)
+        return CR_ERR_INVALID_ARG;
+    const cr_status k = check_k(K);
+    if (k != CR_OK)
+        return k;
+    if (M > INT_MAX)
+        return CR_ERR_UNSUPPORTED;
+    if (M == 0)
+        return CR_OK;
+    if (!x || !out)
+        return CR_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(out))
+        return CR_ERR_ALIGNMENT;
+    if (overlap_other(out, 2 * M * K, x, 2 * M * K))
+        return CR_ERR_INVALID_ARG;
+    DeviceState *d = nullptr;
+    const cr_status ds = current_device(&d);
+    if (ds != CR_OK)
+        return ds;
+    return launched(cr::nm::launch_rotate(x, M, K, out, d->num_sms, stream));
 }
 
 namespace {

@@ -1,0 +1,819 @@
+// k_norm.cuh -- what stands between two W4A8 layers: the root-mean-square norm
+// with the residual's addition, fused with the block rotation and the
+// per-token int8 quantisation of the next layer's input; its gradient; and the
+// block rotation alone.
+//
+// Forward, per row (k_rotquant.cuh has the rotation's definition and fp32
+// order, and the quantiser):
+//   h  = bf16(x + residual)             (h = x without a residual)
+//   rs = fp32(1 / sqrt(sum h^2 / K + eps))   sum, quotient and root in fp64
+//   v  = (h * rs) * gamma               two fp32 operations
+//   r  = v rotated block-wise;  xs = max |r| / qmax;  xq = clamp(rint(r / xs))
+// The sum is taken in fp64: a square of a bf16 value is exact there, and the
+// sum of a row keeps about 2^-50, so the fp32 result does not depend on the
+// order of the additions and the whole row is bit-reproducible.
+//
+// Backward, per row, with dr the gradient of r (straight through the
+// quantiser; the rotation is its own transpose and inverse):
+//   dv = dr rotated;  xh = h * rs;  g = dv * gamma;  c = sum_k(g * xh) / K
+//   dx = bf16(rs * (g - xh * c) [+ dres]);  dgamma[k] = sum_m dv * xh
+// all in fp32.
+//
+// All three are bound by HBM: the forward's floor is 2 bytes in per element
+// (4 with a residual) and 1 (3) out, the backward's 6 (8), the rotation's 4.
+#pragma once
+
+#include "cr_device.cuh"
+#include "k_rotquant.cuh"
+
+namespace cr {
+namespace nm {
+
+// ---------------------------------------------------------------- loads and sums
+
+// Sixteen consecutive bf16 values as eight words (element 2i in the low half
+// of word i).  Plain loads: the rows may be written earlier by this kernel.
+__device__ __forceinline__ void load16(const uint16_t *p, uint32_t (&w)[8])
+{
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
+    const uint4 b = *reinterpret_cast<const uint4 *>(p + 8);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+}
+
+__device__ __forceinline__ void store16(uint16_t *p, const uint32_t (&w)[8])
+{
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// w = bf16(w + r), element-wise: one fp32 addition of the exact values,
+// rounded once.
+__device__ __forceinline__ void add16(uint32_t (&w)[8], const uint32_t (&r)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        w[i] = to_bf16x2_bits(__fadd_rn(bf16_lo(w[i]), bf16_lo(r[i])), __fadd_rn(bf16_hi(w[i]), bf16_hi(r[i])));
+}
+
+// The magnitude of a bf16 value as a double, built from its bits (sign
+// dropped, exponent rebias 127 -> 1023): two integer instructions instead of a
+// conversion, which has a quarter of the rate.  Exact for normal values; zero
+// and subnormals come out as at most 2^-126, whose square does not reach the
+// 50th bit of a sum that has eps >= 1e-30 added.
+__device__ __forceinline__ double mag_lo(uint32_t w)
+{
+    return __hiloint2double((int)(((w & 0x7FFFu) << 13) + 0x38000000u), 0);
+}
+__device__ __forceinline__ double mag_hi(uint32_t w)
+{
+    return __hiloint2double((int)(((w >> 3) & 0x0FFFE000u) + 0x38000000u), 0);
+}
+
+// Sum of the squares of sixteen bf16 values, two chains.
+__device__ __forceinline__ double squares16(const uint32_t (&w)[8])
+{
+    double s0 = 0.0, s1 = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const double a = mag_lo(w[i]), b = mag_hi(w[i]);
+        s0 = __fma_rn(a, a, s0);
+        s1 = __fma_rn(b, b, s1);
+    }
+    return s0 + s1;
+}
+
+// rs of the row, from every thread's share of the sum of squares: the warps'
+// sums in shared memory, then one thread adds them and takes the root (the
+// fp64 division and root are some hundred instructions: one warp spends them).
+template <int THREADS>
+__device__ __forceinline__ float row_rs(double ss, int64_t K, double eps, double *warp_ss, float *rs_out)
+{
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+    if ((tid & 31) == 0)
+        warp_ss[tid >> 5] = ss;
+    __syncthreads();
+    if (tid == 0) {
+        double t = warp_ss[0];
+#pragma unroll
+        for (int w = 1; w < THREADS / 32; ++w)
+            t += warp_ss[w];
+        *rs_out = (float)(1.0 / sqrt(t / (double)K + eps));
+    }
+    __syncthreads();
+    return *rs_out;
+}
+
+// Sixteen consecutive weights as fp32 (GBF16: stored as bf16).
+template <bool GBF16>
+__device__ __forceinline__ void load_gamma16(const void *gamma, int64_t k, float (&g)[16])
+{
+    if constexpr (GBF16) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(gamma) + k);
+        const uint4 a = __ldg(p), b = __ldg(p + 1);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            g[2 * i] = bf16_lo(w[i]);
+            g[2 * i + 1] = bf16_hi(w[i]);
+        }
+    } else {
+        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(gamma) + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 a = __ldg(p + i);
+            g[4 * i] = a.x, g[4 * i + 1] = a.y, g[4 * i + 2] = a.z, g[4 * i + 3] = a.w;
+        }
+    }
+}
+
+// The maximum over the CTA of a non-negative, NaN-free value.
+template <int THREADS>
+__device__ __forceinline__ float block_max(float amax, float *warp_max)
+{
+    uint32_t bits = __float_as_uint(amax);
+    asm volatile("redux.sync.max.u32 %0, %0, 0xffffffff;" : "+r"(bits));
+    if ((threadIdx.x & 31) == 0)
+        warp_max[threadIdx.x >> 5] = __uint_as_float(bits);
+    __syncthreads();
+    float m = warp_max[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 32; ++w)
+        m = fmaxf(m, warp_max[w]);
+    return m;
+}
+
+// The row's scale and what the quantiser needs of it, from max |R| = 16 max |r|
+// (k_rotquant.cuh).
+struct RowScale {
+    float scale, inv16;
+    bool exact_row;
+    __device__ __forceinline__ RowScale(float rmax, int qmax)
+    {
+        const float rowmax = __fmul_rn(rmax, 0.0625f);
+        scale = (rowmax > 0.0f) ? __fdiv_rn(rowmax, (float)qmax) : 1.0f;
+        exact_row = rowmax > 0.0f && rowmax < 7.8886091e-31f;  // max |r| < 2^-100
+        inv16 = __fmul_rn(__frcp_rn(scale), 0.0625f);
+    }
+};
+
+struct FwdArgs {
+    const uint16_t *x, *res;
+    const void *gamma;
+    double eps;
+    int64_t M, K;
+    int qmax;
+    uint16_t *h;
+    int8_t *xq;
+    float *xs, *rs;
+};
+
+// Rows m >= M of the decode GEMV's padded operand: zeros with scale 1.
+__device__ __forceinline__ bool padding_row(const FwdArgs &a, int64_t m)
+{
+    if (m < a.M)
+        return false;
+    for (int64_t c = threadIdx.x; c < a.K / 16; c += blockDim.x)
+        reinterpret_cast<uint4 *>(a.xq + m * a.K)[c] = make_uint4(0u, 0u, 0u, 0u);
+    if (threadIdx.x == 0)
+        a.xs[m] = 1.0f;
+    return true;
+}
+
+// ---------------------------------------------------------------- forward, short batches
+//
+// One CTA per row and one 256-element block per half-warp, as
+// rotquant_rows_kernel: few CTAs run, and the chain of dependent steps is what
+// a decode step waits for.  J blocks per half-warp stay in registers from the
+// load to the store; kRecompute (longer rows) reads h back for each of its two
+// passes after the sum.
+template <int J, bool kRecompute, int THREADS, bool GBF16>
+__global__ void __launch_bounds__(THREADS) rmsnorm_rows_kernel(const FwdArgs a)
+{
+    constexpr int kHalfWarps = THREADS / 16;
+    __shared__ __align__(16) float tr_all[kHalfWarps][16 * 16 + 16];
+    __shared__ __align__(16) uint8_t tb_all[kHalfWarps][272];
+    __shared__ double warp_ss[THREADS / 32];
+    __shared__ float warp_max[THREADS / 32];
+    __shared__ float rs_sh;
+
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    if (threadIdx.x == 0 && (int64_t)blockIdx.x < a.M) {
+        bulk_prefetch_l2(a.x + (int64_t)blockIdx.x * a.K, (uint32_t)(a.K * 2));
+        if (a.res != nullptr)
+            bulk_prefetch_l2(a.res + (int64_t)blockIdx.x * a.K, (uint32_t)(a.K * 2));
+    }
+    // nothing is read or written before the previous kernel has completed
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const int64_t m = blockIdx.x;
+    if (padding_row(a, m))
+        return;
+    const int tid = threadIdx.x, hw = tid >> 4, L = tid & 15;
+    const unsigned hmask = 0xFFFFu << (16 * (hw & 1));
+    const int NB = (int)(a.K / 256);
+    const uint16_t *xrow = a.x + m * a.K;
+    const uint16_t *rrow = a.res != nullptr ? a.res + m * a.K : nullptr;
+    uint16_t *hrow = a.h + m * a.K;
+    int8_t *qrow = a.xq + m * a.K;
+    float *tr = tr_all[hw];
+    uint8_t *tb = tb_all[hw];
+
+    constexpr int kHeld = kRecompute ? 1 : J;
+    uint32_t w[kHeld][8];
+    double ss = 0.0;
+    auto load_h = [&](int b, uint32_t (&wj)[8]) {
+        load16(xrow + 256 * b + 16 * L, wj);
+        if (rrow != nullptr) {
+            uint32_t r[8];
+            load16(rrow + 256 * b + 16 * L, r);
+            add16(wj, r);
+            store16(hrow + 256 * b + 16 * L, wj);
+        }
+        ss += squares16(wj);
+    };
+    if constexpr (!kRecompute) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (hw + kHalfWarps * j < NB)
+                load_h(hw + kHalfWarps * j, w[j]);
+    } else {
+        for (int b = hw; b < NB; b += kHalfWarps)
+            load_h(b, w[0]);
+    }
+    const float rs = row_rs<THREADS>(ss, a.K, a.eps, warp_ss, &rs_sh);
+
+    float v[kHeld][16];
+    auto rotate = [&](int b, const uint32_t (&wj)[8], float (&vj)[16]) {
+        float g[16];
+        load_gamma16<GBF16>(a.gamma, 256 * b + 16 * L, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            vj[2 * i] = __fmul_rn(__fmul_rn(bf16_lo(wj[i]), rs), g[2 * i]);
+            vj[2 * i + 1] = __fmul_rn(__fmul_rn(bf16_hi(wj[i]), rs), g[2 * i + 1]);
+        }
+        rq::rotate_regs(L, tr, hmask, vj);
+    };
+    const uint16_t *again = rrow != nullptr ? hrow : xrow;  // where this thread finds its values of h again
+    float amax = 0.0f;
+    if constexpr (!kRecompute) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (hw + kHalfWarps * j < NB) {
+                rotate(hw + kHalfWarps * j, w[j], v[j]);
+                amax = fmaxf(amax, rq::max_abs16(v[j]));
+            }
+    } else {
+        for (int b = hw; b < NB; b += kHalfWarps) {
+            load16(again + 256 * b + 16 * L, w[0]);
+            rotate(b, w[0], v[0]);
+            amax = fmaxf(amax, rq::max_abs16(v[0]));
+        }
+    }
+    const RowScale s(block_max<THREADS>(amax, warp_max), a.qmax);
+    if constexpr (!kRecompute) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (hw + kHalfWarps * j < NB)
+                rq::quantise_store(v[j], s.scale, s.inv16, a.qmax, s.exact_row, L, tb, hmask,
+                                   qrow + 256 * (hw + kHalfWarps * j));
+    } else {
+        for (int b = hw; b < NB; b += kHalfWarps) {
+            load16(again + 256 * b + 16 * L, w[0]);
+            rotate(b, w[0], v[0]);
+            rq::quantise_store(v[0], s.scale, s.inv16, a.qmax, s.exact_row, L, tb, hmask, qrow + 256 * b);
+        }
+    }
+    if (tid == 0) {
+        a.xs[m] = s.scale;
+        if (a.rs != nullptr)
+            a.rs[m] = rs;
+    }
+}
+
+// ---------------------------------------------------------------- forward, many rows
+//
+// A half-warp owns a pair of blocks and works on both in packed fp32x2
+// arithmetic (each half rounded as the scalar instruction rounds it), as
+// rotquant_pairs_kernel: at these sizes the scalar form is bound by the
+// instructions it issues.
+template <int J, bool kRecompute, int THREADS, bool GBF16>
+__global__ void __launch_bounds__(THREADS) rmsnorm_pairs_kernel(const FwdArgs a)
+{
+    constexpr int kHalfWarps = THREADS / 16;
+    extern __shared__ __align__(16) uint64_t nm_smem[];
+    __shared__ double warp_ss[THREADS / 32];
+    __shared__ float warp_max[THREADS / 32];
+    __shared__ float rs_sh;
+
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    if (threadIdx.x == 0 && (int64_t)blockIdx.x < a.M) {
+        bulk_prefetch_l2(a.x + (int64_t)blockIdx.x * a.K, (uint32_t)(a.K * 2));
+        if (a.res != nullptr)
+            bulk_prefetch_l2(a.res + (int64_t)blockIdx.x * a.K, (uint32_t)(a.K * 2));
+    }
+    // nothing is read or written before the previous kernel has completed
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const int64_t m = blockIdx.x;
+    if (padding_row(a, m))
+        return;
+    const int tid = threadIdx.x, hw = tid >> 4, L = tid & 15;
+    const unsigned hmask = 0xFFFFu << (16 * (hw & 1));
+    const int NB = (int)(a.K / 256);
+    const int NP = (NB + 1) / 2;  // block pairs (2p, 2p + 1); the last one may be alone
+    const uint16_t *xrow = a.x + m * a.K;
+    const uint16_t *rrow = a.res != nullptr ? a.res + m * a.K : nullptr;
+    uint16_t *hrow = a.h + m * a.K;
+    int8_t *qrow = a.xq + m * a.K;
+    uint64_t *tr = nm_smem + 256 * hw;
+    uint8_t *tb = reinterpret_cast<uint8_t *>(tr) + 64 * (hw & 1);
+
+    constexpr int kHeld = kRecompute ? 1 : J;
+    uint32_t w0[kHeld][8], w1[kHeld][8];
+    double ss = 0.0;
+    auto load_h = [&](int p, uint32_t (&u0)[8], uint32_t (&u1)[8]) {
+        const int64_t k0 = 512 * (int64_t)p + 16 * L;
+        const bool two = 2 * p + 1 < NB;
+        load16(xrow + k0, u0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            u1[i] = 0u;
+        if (two)
+            load16(xrow + k0 + 256, u1);
+        if (rrow != nullptr) {
+            uint32_t r0[8], r1[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+            load16(rrow + k0, r0);
+            if (two)
+                load16(rrow + k0 + 256, r1);
+            add16(u0, r0);
+            add16(u1, r1);
+            store16(hrow + k0, u0);
+            if (two)
+                store16(hrow + k0 + 256, u1);
+        }
+        ss += squares16(u0);
+        if (two)
+            ss += squares16(u1);
+    };
+    if constexpr (!kRecompute) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (hw + kHalfWarps * j < NP)
+                load_h(hw + kHalfWarps * j, w0[j], w1[j]);
+    } else {
+        for (int p = hw; p < NP; p += kHalfWarps)
+            load_h(p, w0[0], w1[0]);
+    }
+    const float rs = row_rs<THREADS>(ss, a.K, a.eps, warp_ss, &rs_sh);
+    const uint64_t rs2 = rq::pk(__float_as_uint(rs), __float_as_uint(rs));
+
+    uint64_t v[kHeld][16];
+    auto rotate = [&](int p, const uint32_t (&u0)[8], const uint32_t (&u1)[8], uint64_t (&vj)[16]) {
+        float g0[16], g1[16];
+        const int64_t k0 = 512 * (int64_t)p + 16 * L;
+        load_gamma16<GBF16>(a.gamma, k0, g0);
+        if (2 * p + 1 < NB) {
+            load_gamma16<GBF16>(a.gamma, k0 + 256, g1);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                g1[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t lo = rq::pk(u0[i] << 16, u1[i] << 16);
+            const uint64_t hi = rq::pk(u0[i] & 0xFFFF0000u, u1[i] & 0xFFFF0000u);
+            vj[2 * i] = rq::mul2(rq::mul2(lo, rs2), rq::pk(__float_as_uint(g0[2 * i]), __float_as_uint(g1[2 * i])));
+            vj[2 * i + 1] = rq::mul2(rq::mul2(hi, rs2),
+                                     rq::pk(__float_as_uint(g0[2 * i + 1]), __float_as_uint(g1[2 * i + 1])));
+        }
+        rq::rotate_pair_regs(L, tr, hmask, vj);
+    };
+    auto reload = [&](int p) {  // this thread's values of h again
+        const uint16_t *src = (rrow != nullptr ? hrow : xrow) + 512 * (int64_t)p + 16 * L;
+        load16(src, w0[0]);
+        if (2 * p + 1 < NB)
+            load16(src + 256, w1[0]);
+        else
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w1[0][i] = 0u;
+    };
+    auto dst1 = [&](int p) { return 2 * p + 1 < NB ? qrow + 256 * (2 * p + 1) : nullptr; };
+    float amax = 0.0f;
+    if constexpr (!kRecompute) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int p = hw + kHalfWarps * j;
+            if (p < NP) {
+                rotate(p, w0[j], w1[j], v[j]);
+                amax = fmaxf(amax, rq::max_abs_pairs(v[j]));
+            }
+        }
+    } else {
+        for (int p = hw; p < NP; p += kHalfWarps) {
+            reload(p);
+            rotate(p, w0[0], w1[0], v[0]);
+            amax = fmaxf(amax, rq::max_abs_pairs(v[0]));
+        }
+    }
+    const RowScale s(block_max<THREADS>(amax, warp_max), a.qmax);
+    if constexpr (!kRecompute) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int p = hw + kHalfWarps * j;
+            if (p < NP)
+                rq::quantise_store_pair(v[j], s.scale, s.inv16, a.qmax, s.exact_row, L, tb, hmask, qrow + 512 * p,
+                                        dst1(p));
+        }
+    } else {
+        for (int p = hw; p < NP; p += kHalfWarps) {
+            reload(p);
+            rotate(p, w0[0], w1[0], v[0]);
+            rq::quantise_store_pair(v[0], s.scale, s.inv16, a.qmax, s.exact_row, L, tb, hmask, qrow + 512 * p,
+                                    dst1(p));
+        }
+    }
+    if (tid == 0) {
+        a.xs[m] = s.scale;
+        if (a.rs != nullptr)
+            a.rs[m] = rs;
+    }
+}
+
+// A launch as a programmatic dependent of the previous kernel on the stream.
+template <class... Args>
+inline cudaError_t launch_dependent(void (*kern)(Args...), int64_t grid, int threads, int smem, cudaStream_t stream,
+                                    Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <bool GBF16, int THREADS>
+inline cudaError_t launch_fwd_rows(const FwdArgs &a, int64_t MP, cudaStream_t stream)
+{
+    constexpr int kHalfWarps = THREADS / 16;
+    const int64_t per_hw = (a.K / 256 + kHalfWarps - 1) / kHalfWarps;  // blocks per half-warp
+    void (*kern)(FwdArgs) = per_hw <= 1   ? rmsnorm_rows_kernel<1, false, THREADS, GBF16>
+                            : per_hw == 2 ? rmsnorm_rows_kernel<2, false, THREADS, GBF16>
+                                          : rmsnorm_rows_kernel<1, true, THREADS, GBF16>;
+    return launch_dependent(kern, MP, THREADS, 0, stream, a);
+}
+
+// Opt the 384- and 512-thread CTAs of the packed form into their transpose
+// buffers (above 48 KB).  Once per device, before the first launch.
+inline cudaError_t set_attributes()
+{
+    struct Need {
+        void (*f)(FwdArgs);
+        int bytes;
+    };
+    const Need need[] = {
+        {rmsnorm_pairs_kernel<1, false, 512, true>, rq::smem_bytes<512>()},
+        {rmsnorm_pairs_kernel<1, false, 512, false>, rq::smem_bytes<512>()},
+        {rmsnorm_pairs_kernel<1, true, 512, true>, rq::smem_bytes<512>()},
+        {rmsnorm_pairs_kernel<1, true, 512, false>, rq::smem_bytes<512>()},
+        {rmsnorm_pairs_kernel<1, false, 384, true>, rq::smem_bytes<384>()},
+        {rmsnorm_pairs_kernel<1, false, 384, false>, rq::smem_bytes<384>()},
+    };
+    for (const Need &n : need) {
+        const cudaError_t e = cudaFuncSetAttribute(n.f, cudaFuncAttributeMaxDynamicSharedMemorySize, n.bytes);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
+}
+
+template <bool GBF16>
+inline cudaError_t launch_fwd_t(const FwdArgs &a, int64_t MP, cudaStream_t stream)
+{
+    if (MP <= rq::kShortRows)
+        return a.K >= 8192 ? launch_fwd_rows<GBF16, 512>(a, MP, stream) : launch_fwd_rows<GBF16, 256>(a, MP, stream);
+    const int64_t pairs = (a.K / 256 + 1) / 2;
+    if (pairs <= 4)
+        return launch_dependent(rmsnorm_pairs_kernel<1, false, 64, GBF16>, MP, 64, rq::smem_bytes<64>(), stream, a);
+    if (pairs <= 8)
+        return launch_dependent(rmsnorm_pairs_kernel<1, false, 128, GBF16>, MP, 128, rq::smem_bytes<128>(), stream, a);
+    if (pairs <= 16)
+        return launch_dependent(rmsnorm_pairs_kernel<1, false, 256, GBF16>, MP, 256, rq::smem_bytes<256>(), stream, a);
+    if (pairs <= 24)
+        return launch_dependent(rmsnorm_pairs_kernel<1, false, 384, GBF16>, MP, 384, rq::smem_bytes<384>(), stream, a);
+    if (pairs <= 32)
+        return launch_dependent(rmsnorm_pairs_kernel<1, false, 512, GBF16>, MP, 512, rq::smem_bytes<512>(), stream, a);
+    return launch_dependent(rmsnorm_pairs_kernel<1, true, 512, GBF16>, MP, 512, rq::smem_bytes<512>(), stream, a);
+}
+
+// Short batches take the scalar form, 512 threads for K >= 8192 and 256 below;
+// longer ones the packed form with one half-warp per block pair where that fits
+// in 512 threads (K <= 16384), and the re-reading form beyond.
+inline cudaError_t launch_fwd(const FwdArgs &a, int64_t MP, bool gamma_bf16, cudaStream_t stream)
+{
+    return gamma_bf16 ? launch_fwd_t<true>(a, MP, stream) : launch_fwd_t<false>(a, MP, stream);
+}
+
+// ---------------------------------------------------------------- the rotation back in row order
+
+// Rotate one block held in row order (v[b] = element 16L + b) and return it in
+// row order, scaled: v[b] = rotated element 16L + b.  A second transpose
+// through `tr` after rotate_regs: column L goes out as 16 scalar stores, row L
+// comes back as four 16-byte loads; chunk c of row a lives at chunk position
+// c ^ ((a >> 1) & 3), as in rotate_regs.
+__device__ __forceinline__ void rotate_rows(int L, float *tr, unsigned hmask, float (&v)[16])
+{
+    rq::rotate_regs(L, tr, hmask, v);
+#pragma unroll
+    for (int a = 0; a < 16; ++a)
+        tr[16 * a + 4 * ((L >> 2) ^ ((a >> 1) & 3)) + (L & 3)] = __fmul_rn(v[a], 0.0625f);
+    __syncwarp(hmask);
+    const float4 *rowp = reinterpret_cast<const float4 *>(tr + 16 * L);
+    const int sw = (L >> 1) & 3;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float4 t = rowp[c ^ sw];
+        v[4 * c] = t.x, v[4 * c + 1] = t.y, v[4 * c + 2] = t.z, v[4 * c + 3] = t.w;
+    }
+    __syncwarp(hmask);
+}
+
+constexpr int kRotThreads = 256;
+
+// out = bf16(x rotated): a half-warp per block, grid-stride over all blocks of
+// all rows.  out may be x: a block is read and written by the same half-warp.
+__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const uint16_t *x, int64_t blocks, uint16_t *out)
+{
+    __shared__ __align__(16) float tr_all[kRotThreads / 16][16 * 16 + 16];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int hw = threadIdx.x >> 4, L = threadIdx.x & 15;
+    const unsigned hmask = 0xFFFFu << (16 * (hw & 1));
+    float *tr = tr_all[hw];
+    for (int64_t b = (int64_t)blockIdx.x * (kRotThreads / 16) + hw; b < blocks;
+         b += (int64_t)gridDim.x * (kRotThreads / 16)) {
+        uint32_t w[8];
+        load16(x + 256 * b + 16 * L, w);
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[2 * i] = bf16_lo(w[i]);
+            v[2 * i + 1] = bf16_hi(w[i]);
+        }
+        rotate_rows(L, tr, hmask, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = to_bf16x2_bits(v[2 * i], v[2 * i + 1]);
+        store16(out + 256 * b + 16 * L, w);
+    }
+}
+
+inline cudaError_t launch_rotate(const uint16_t *x, int64_t M, int64_t K, uint16_t *out, int num_sms,
+                                 cudaStream_t stream)
+{
+    const int64_t blocks = M * (K / 256);
+    int64_t grid = (blocks + kRotThreads / 16 - 1) / (kRotThreads / 16);
+    const int64_t cap = 8 * (int64_t)num_sms;
+    if (grid > cap)
+        grid = cap;
+    return launch_dependent(rotate_kernel, grid, kRotThreads, 0, stream, x, blocks, out);
+}
+
+// ---------------------------------------------------------------- backward
+//
+// A persistent grid over rows, so that a CTA adds up its share of dgamma in
+// registers (one value per element of its blocks) and writes it once, as row
+// `blockIdx.x` of the partials [P, K]; a second kernel adds the partials in a
+// fixed order, so dgamma is the same from run to run.  kWide (rows longer than
+// the registers hold): dv is computed twice per row, and the CTA's partial row
+// is added to in memory by the thread that owns the element.
+struct BwdArgs {
+    const uint16_t *dr, *h;
+    const void *gamma;
+    const float *rs;
+    const uint16_t *dres;
+    int64_t M, K;
+    uint16_t *dx;
+    float *part;  // [gridDim.x, K], or null: no dgamma
+};
+
+// Sum over the CTA; `slot` alternates between two rows of warp sums, so one
+// barrier per call is enough.
+template <int THREADS>
+__device__ __forceinline__ float block_sum(float s, float (*warp_sum)[THREADS / 32], int slot)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if ((threadIdx.x & 31) == 0)
+        warp_sum[slot][threadIdx.x >> 5] = s;
+    __syncthreads();
+    float t = warp_sum[slot][0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 32; ++w)
+        t += warp_sum[slot][w];
+    return t;
+}
+
+template <int J, bool kWide, int THREADS, bool GBF16>
+__global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(const BwdArgs a)
+{
+    constexpr int kHalfWarps = THREADS / 16;
+    __shared__ __align__(16) float tr_all[kHalfWarps][16 * 16 + 16];
+    __shared__ float warp_sum[2][THREADS / 32];
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const int tid = threadIdx.x, hw = tid >> 4, L = tid & 15;
+    const unsigned hmask = 0xFFFFu << (16 * (hw & 1));
+    const int NB = (int)(a.K / 256);
+    const float inv_k = 1.0f / (float)a.K;
+    float *tr = tr_all[hw];
+    float *prow = a.part != nullptr ? a.part + (int64_t)blockIdx.x * a.K : nullptr;
+    constexpr int kHeld = kWide ? 1 : J;
+    float acc[kHeld][16];
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            acc[j][i] = 0.0f;
+
+    // dv of one block, and h packed
+    auto load_dv = [&](int64_t row, int b, float (&dv)[16], uint32_t (&hw8)[8]) {
+        uint32_t w[8];
+        load16(a.dr + row + 256 * b + 16 * L, w);
+        load16(a.h + row + 256 * b + 16 * L, hw8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            dv[2 * i] = bf16_lo(w[i]);
+            dv[2 * i + 1] = bf16_hi(w[i]);
+        }
+        rotate_rows(L, tr, hmask, dv);
+    };
+    auto finish = [&](int64_t row, int b, const float (&g)[16], const uint32_t (&hw8)[8], float rs, float c) {
+        uint32_t r[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u}, o[8];
+        if (a.dres != nullptr)
+            load16(a.dres + row + 256 * b + 16 * L, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float lo = rs * (g[2 * i] - bf16_lo(hw8[i]) * rs * c) + bf16_lo(r[i]);
+            const float hi = rs * (g[2 * i + 1] - bf16_hi(hw8[i]) * rs * c) + bf16_hi(r[i]);
+            o[i] = to_bf16x2_bits(lo, hi);
+        }
+        store16(a.dx + row + 256 * b + 16 * L, o);
+    };
+
+    int slot = 0;
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, slot ^= 1) {
+        const int64_t row = m * a.K;
+        const float rs = a.rs[m];
+        float s = 0.0f;
+        if constexpr (!kWide) {
+            float g[J][16];
+            uint32_t hp[J][8];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int b = hw + kHalfWarps * j;
+                if (b < NB) {
+                    load_dv(row, b, g[j], hp[j]);
+                    float gm[16];
+                    load_gamma16<GBF16>(a.gamma, 256 * b + 16 * L, gm);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float xh = (i & 1 ? bf16_hi(hp[j][i >> 1]) : bf16_lo(hp[j][i >> 1])) * rs;
+                        acc[j][i] += g[j][i] * xh;
+                        g[j][i] *= gm[i];
+                        s += g[j][i] * xh;
+                    }
+                }
+            }
+            const float c = block_sum<THREADS>(s, warp_sum, slot) * inv_k;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (hw + kHalfWarps * j < NB)
+                    finish(row, hw + kHalfWarps * j, g[j], hp[j], rs, c);
+        } else {
+            float g[16], gm[16];
+            uint32_t hp[8];
+            for (int b = hw; b < NB; b += kHalfWarps) {
+                load_dv(row, b, g, hp);
+                load_gamma16<GBF16>(a.gamma, 256 * b + 16 * L, gm);
+                float4 *pp = reinterpret_cast<float4 *>(prow + 256 * b + 16 * L);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float d[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = 4 * q + e;
+                        const float xh = (i & 1 ? bf16_hi(hp[i >> 1]) : bf16_lo(hp[i >> 1])) * rs;
+                        d[e] = g[i] * xh;
+                        s += g[i] * gm[i] * xh;
+                    }
+                    if (prow != nullptr) {
+                        float4 t = m == blockIdx.x ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : pp[q];
+                        t.x += d[0], t.y += d[1], t.z += d[2], t.w += d[3];
+                        pp[q] = t;
+                    }
+                }
+            }
+            const float c = block_sum<THREADS>(s, warp_sum, slot) * inv_k;
+            for (int b = hw; b < NB; b += kHalfWarps) {
+                load_dv(row, b, g, hp);
+                load_gamma16<GBF16>(a.gamma, 256 * b + 16 * L, gm);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    g[i] *= gm[i];
+                finish(row, b, g, hp, rs, c);
+            }
+        }
+    }
+    if constexpr (!kWide) {
+        if (prow != nullptr) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int b = hw + kHalfWarps * j;
+                if (b < NB) {
+                    float4 *pp = reinterpret_cast<float4 *>(prow + 256 * b + 16 * L);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        pp[q] = make_float4(acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]);
+                }
+            }
+        }
+    }
+}
+
+// dgamma[k] = sum over p of part[p, k], in a fixed order: a CTA takes 32
+// columns, its eight warps every eighth partial row each, then one warp adds
+// the eight.
+__global__ void __launch_bounds__(256) dgamma_kernel(const float *__restrict__ part, int P, int64_t K,
+                                                     float *__restrict__ dgamma)
+{
+    __shared__ float sh[8][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t k = 32 * (int64_t)blockIdx.x + lane;  // K is a multiple of 256
+    float s = 0.0f;
+#pragma unroll 8
+    for (int p = w; p < P; p += 8)
+        s += part[(int64_t)p * K + k];
+    sh[w][lane] = s;
+    __syncthreads();
+    if (w == 0) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            s += sh[i][lane];
+        dgamma[k] = s;
+    }
+}
+
+// CTAs of the backward's grid, and with it the partial rows of dgamma: a
+// function of the shape alone, so that the caller's workspace has a fixed size.
+inline int64_t backward_ctas(int64_t M, int64_t K)
+{
+    const int64_t most = K <= 1024 ? 148 * 8 : K <= 2048 ? 148 * 4 : K <= 4096 ? 148 * 2 : 148;
+    return M < most ? M : most;
+}
+
+template <bool GBF16>
+inline cudaError_t launch_bwd_t(const BwdArgs &a, float *dgamma, cudaStream_t stream)
+{
+    const int64_t P = backward_ctas(a.M, a.K);
+    cudaError_t e;
+    if (a.K <= 1024)
+        e = launch_dependent(rmsnorm_backward_kernel<1, false, 64, GBF16>, P, 64, 0, stream, a);
+    else if (a.K <= 2048)
+        e = launch_dependent(rmsnorm_backward_kernel<1, false, 128, GBF16>, P, 128, 0, stream, a);
+    else if (a.K <= 4096)
+        e = launch_dependent(rmsnorm_backward_kernel<1, false, 256, GBF16>, P, 256, 0, stream, a);
+    else if (a.K <= 8192)
+        e = launch_dependent(rmsnorm_backward_kernel<1, false, 512, GBF16>, P, 512, 0, stream, a);
+    else if (a.K <= 16384)
+        e = launch_dependent(rmsnorm_backward_kernel<2, false, 512, GBF16>, P, 512, 0, stream, a);
+    else
+        e = launch_dependent(rmsnorm_backward_kernel<1, true, 512, GBF16>, P, 512, 0, stream, a);
+    if (e != cudaSuccess || dgamma == nullptr)
+        return e;
+    return launch_dependent(dgamma_kernel, a.K / 32, 256, 0, stream, (const float *)a.part, (int)P, a.K, dgamma);
+}
+
+inline cudaError_t launch_bwd(const BwdArgs &a, bool gamma_bf16, float *dgamma, cudaStream_t stream)
+{
+    return gamma_bf16 ? launch_bwd_t<true>(a, dgamma, stream) : launch_bwd_t<false>(a, dgamma, stream);
+}
+
+}  // namespace nm
+}  // namespace cr

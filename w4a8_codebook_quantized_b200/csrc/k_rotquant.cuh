@@ -71,21 +71,12 @@ __device__ __forceinline__ void h4_quad(float &a0, float &a1, float &a2, float &
     a3 = y3;
 }
 
-// Rotate one 256-element block.  On return lane L of the half-warp holds
-// v[a] = 16 x rotated element 16a + L (a = 0..15).  `tr` is this half-warp's
-// 16 x 16 fp32 transpose buffer (16-byte aligned).
-__device__ __forceinline__ void rotate_block(const uint16_t *__restrict__ blk, int L, float *tr, unsigned hmask,
-                                             float (&v)[16])
+// Rotate one 256-element block held as v[b] = element 16L + b of lane L.  On
+// return lane L of the half-warp holds v[a] = 16 x rotated element 16a + L
+// (a = 0..15).  `tr` is this half-warp's 16 x 16 fp32 transpose buffer
+// (16-byte aligned).
+__device__ __forceinline__ void rotate_regs(int L, float *tr, unsigned hmask, float (&v)[16])
 {
-    const uint4 *src = reinterpret_cast<const uint4 *>(blk + 16 * L);
-    const uint4 p0 = __ldg(src);
-    const uint4 p1 = __ldg(src + 1);
-    const uint32_t w[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);             // element 2i: low half
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);  // element 2i+1: high half
-    }
     // stride 1 (digit d0 = b % 4), then stride 4 (digit d1 = b / 4)
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -126,6 +117,22 @@ __device__ __forceinline__ void rotate_block(const uint16_t *__restrict__ blk, i
     // works on R with the scale multiplied by 16 and gets the same integers
     // (rows whose values reach the subnormal range take an exact path that
     // applies the 1/16 per element).
+}
+
+// The same for a block of bf16 values in global memory.
+__device__ __forceinline__ void rotate_block(const uint16_t *__restrict__ blk, int L, float *tr, unsigned hmask,
+                                             float (&v)[16])
+{
+    const uint4 *src = reinterpret_cast<const uint4 *>(blk + 16 * L);
+    const uint4 p0 = __ldg(src);
+    const uint4 p1 = __ldg(src + 1);
+    const uint32_t w[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);             // element 2i: low half
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);  // element 2i+1: high half
+    }
+    rotate_regs(L, tr, hmask, v);
 }
 
 // Quantise this lane's 16 column values of one block and store them in row
@@ -389,29 +396,13 @@ __device__ __forceinline__ void h4_quad2(uint64_t &a0, uint64_t &a1, uint64_t &a
     a3 = y3;
 }
 
-// Rotate a pair of 256-element blocks: blk0 into the low halves, blk1 into
-// the high halves (blk1 == nullptr stands for a block of zeros).  On return
-// lane L of the half-warp holds v[a] = 16 x rotated element 16a + L of both
-// blocks (a = 0..15).  `tr` is this half-warp's 16 x 16 buffer of pairs
+// Rotate a pair of 256-element blocks held as v[b] = element 16L + b of both
+// blocks (the first in the low halves, the second in the high halves).  On
+// return lane L of the half-warp holds v[a] = 16 x rotated element 16a + L of
+// both blocks (a = 0..15).  `tr` is this half-warp's 16 x 16 buffer of pairs
 // (2 KB, 16-byte aligned).
-__device__ __forceinline__ void rotate_pair(const uint16_t *__restrict__ blk0, const uint16_t *__restrict__ blk1,
-                                            int L, uint64_t *tr, unsigned hmask, uint64_t (&v)[16])
+__device__ __forceinline__ void rotate_pair_regs(int L, uint64_t *tr, unsigned hmask, uint64_t (&v)[16])
 {
-    const uint4 *s0 = reinterpret_cast<const uint4 *>(blk0 + 16 * L);
-    const uint4 p0 = __ldg(s0), p1 = __ldg(s0 + 1);
-    uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0;
-    if (blk1 != nullptr) {
-        const uint4 *s1 = reinterpret_cast<const uint4 *>(blk1 + 16 * L);
-        q0 = __ldg(s1);
-        q1 = __ldg(s1 + 1);
-    }
-    const uint32_t w0[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-    const uint32_t w1[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[2 * i] = pk(w0[i] << 16, w1[i] << 16);                      // element 2i: low bf16
-        v[2 * i + 1] = pk(w0[i] & 0xFFFF0000u, w1[i] & 0xFFFF0000u);  // element 2i+1: high bf16
-    }
     // stride 1 (digit d0 = b % 4), then stride 4 (digit d1 = b / 4)
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -449,6 +440,29 @@ __device__ __forceinline__ void rotate_pair(const uint16_t *__restrict__ blk0, c
     // works on R with the scale multiplied by 16 and gets the same integers
     // (rows whose values reach the subnormal range take an exact path that
     // applies the 1/16 per element).
+}
+
+// The same for two blocks of bf16 values in global memory (blk1 == nullptr
+// stands for a block of zeros).
+__device__ __forceinline__ void rotate_pair(const uint16_t *__restrict__ blk0, const uint16_t *__restrict__ blk1,
+                                            int L, uint64_t *tr, unsigned hmask, uint64_t (&v)[16])
+{
+    const uint4 *s0 = reinterpret_cast<const uint4 *>(blk0 + 16 * L);
+    const uint4 p0 = __ldg(s0), p1 = __ldg(s0 + 1);
+    uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0;
+    if (blk1 != nullptr) {
+        const uint4 *s1 = reinterpret_cast<const uint4 *>(blk1 + 16 * L);
+        q0 = __ldg(s1);
+        q1 = __ldg(s1 + 1);
+    }
+    const uint32_t w0[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+    const uint32_t w1[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[2 * i] = pk(w0[i] << 16, w1[i] << 16);                      // element 2i: low bf16
+        v[2 * i + 1] = pk(w0[i] & 0xFFFF0000u, w1[i] & 0xFFFF0000u);  // element 2i+1: high bf16
+    }
+    rotate_pair_regs(L, tr, hmask, v);
 }
 
 // max |v| over both halves of 16 pairs as a tree (fmaxf drops NaN operands, so
