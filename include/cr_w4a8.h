@@ -607,6 +607,77 @@ cr_status cr_rmsnorm_backward(const uint16_t *dr, const uint16_t *h, const void 
 cr_status cr_rotate(const uint16_t *x, int64_t M, int64_t K, uint16_t *out, cr_stream_t stream);
 
 /*
+ * (22) The gradient of a gated layer (9): both projections recomputed from the
+ * packed codes, the activation's gradient fused into that contraction's
+ * epilogue, and the straight-through input gradient.
+ *
+ * Defined by: ai-toolkit convrot_w4a8_quant.py, _w4a8_linear_ste_backward (the
+ * training path keeps only the packed codes and decodes them again), applied
+ * to h3-rs src/weights.rs, swiglu_interleaved.  With g, u the fp32 outputs of
+ * rows 2f and 2f + 1 of the interleaved layer, computed exactly as in (3), and
+ * s = 1 / (1 + e^-g):
+ *   dz[m, 2f]     = bf16( dout[m, f] * u * s * (1 + g * (1 - s)) )
+ *   dz[m, 2f + 1] = bf16( dout[m, f] * g * s )
+ *   dx[m, k]      = bf16( sum_n dz[m, n] * w[n, k] )     (w as in (13))
+ * dx is the gradient of the layer's rotated input, as in (13): (20) or (21)
+ * take it back.  dz, the gradient of the projections' outputs, is an output of
+ * its own (its column sums are the bias's gradient).
+ *
+ * dout [M, N / 2] bf16; xq [>= M, K] int8 and xs [>= M] fp32: the quantised
+ * activations of the forward; the interleaved layer as in (9).  dx [M, K] bf16,
+ * dz [M, N] bf16, written.  N must be a multiple of 8 (CR_ERR_UNSUPPORTED
+ * otherwise); N == 0 writes dx = 0.  work: at least
+ * cr_w4a8_swiglu_backward_work_bytes(M, N, K) bytes (the decoded weight, 3 N K),
+ * 16-byte aligned; CR_ERR_INVALID_ARG when smaller.  Nothing is allocated.
+ */
+int64_t cr_w4a8_swiglu_backward_work_bytes(int64_t M, int64_t N, int64_t K);
+cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const float *xs, const uint8_t *qdata,
+                                  const uint8_t *srel, const float *codebook, const float *s_channel,
+                                  const float *bias, int64_t M, int64_t N, int64_t K, uint16_t *dx, uint16_t *dz,
+                                  void *work, int64_t work_bytes, cr_stream_t stream);
+
+/*
+ * (23) Softmax cross entropy over the outputs of a W4A8 head, without storing
+ * them: the contraction runs over the vocabulary in pieces and its epilogue
+ * reduces each tile of outputs.
+ *
+ * The pages end at the layer; the head's outputs y [M, V] are those of (3) in
+ * fp32 (V rows of the layer), and
+ *   lse[m]  = log sum_n e^y[m, n]
+ *   loss[m] = lse[m] - y[m, targets[m]];  0 where targets[m] == ignore_index;
+ *             NaN where the target is any other value outside 0 .. V - 1
+ * A bias of -inf takes an entry out of the softmax.  V >= 1 (CR_ERR_INVALID_ARG
+ * otherwise), any V.  M <= 8 takes the decode GEMV.
+ *
+ * xq [>= M, K] int8, xs [>= M] fp32, the layer as in (3); targets [M] int64.
+ * loss [M], lse [M] fp32, written.  work: at least
+ * cr_w4a8_cross_entropy_work_bytes(M, V, K) bytes, 16-byte aligned
+ * (CR_ERR_INVALID_ARG when smaller): a decoded piece of the weight (64 MB or
+ * 256 K bytes, whichever is more) and 8 bytes per row and 256 outputs.  Nothing
+ * is allocated.
+ *
+ * (23b) Its gradient with respect to the layer's rotated input:
+ *   dl[m, n] = bf16( dloss[m] * (e^(y[m, n] - lse[m]) - [n == targets[m]]) ),
+ *              0 in ignored rows, NaN in rows with an invalid target
+ *   dx[m, k] = bf16( sum_n dl[m, n] * w[n, k] )   (w as in (13); the sum in fp32)
+ * lse from (23) on the same arguments; dloss [M] fp32, the gradient of loss
+ * (1 / count for the mean over count rows).  dx [M, K] bf16, written: (20) or
+ * (21) take it back.  work: at least
+ * cr_w4a8_cross_entropy_backward_work_bytes(M, V, K) bytes.
+ */
+int64_t cr_w4a8_cross_entropy_work_bytes(int64_t M, int64_t V, int64_t K);
+cr_status cr_w4a8_cross_entropy(const int8_t *xq, const float *xs, const uint8_t *qdata, const uint8_t *srel,
+                                const float *codebook, const float *s_channel, const float *bias,
+                                const int64_t *targets, int64_t ignore_index, int64_t M, int64_t V, int64_t K,
+                                float *loss, float *lse, void *work, int64_t work_bytes, cr_stream_t stream);
+int64_t cr_w4a8_cross_entropy_backward_work_bytes(int64_t M, int64_t V, int64_t K);
+cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, const uint8_t *qdata, const uint8_t *srel,
+                                         const float *codebook, const float *s_channel, const float *bias,
+                                         const int64_t *targets, int64_t ignore_index, const float *lse,
+                                         const float *dloss, int64_t M, int64_t V, int64_t K, uint16_t *dx, void *work,
+                                         int64_t work_bytes, cr_stream_t stream);
+
+/*
  * (15) Self-test of the failure path: launches one CTA whose thread waits,
  * with the library's bounded wait, on an mbarrier that nothing completes.
  * After limit_ns (1 ms .. 1 s, CR_ERR_INVALID_ARG otherwise) the wait gives

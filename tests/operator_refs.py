@@ -111,3 +111,62 @@ def logits64(layer, xq, xs):
 def gradient_weight(layer):
     """w[n, k] = bf16(w8 * bf16(s_channel)), as float64."""
     return bf16_round(grid(layer) * bf16_round(layer.s_channel)[:, None])
+
+
+def swiglu_backward(layer, xq, xs, dout):
+    """(dx, dz, bound of dz's fp32 error / 2^-24, bound of dx's error) of a
+    gated layer with interleaved rows, float64."""
+    z = logits64(layer, xq, xs)
+    g, u = z[:, 0::2], z[:, 1::2]
+    s = 0.5 * (1 + np.tanh(0.5 * g))
+    dz = np.empty_like(z)
+    dz[:, 0::2] = dout * u * s * (1 + g * (1 - s))
+    dz[:, 1::2] = dout * g * s
+    # g and u carry 4 roundings each (float(acc), two products, the bias), with
+    # the bias's share bounded by |y| + |bias|; the derivatives of the three
+    # factors are at most 1 + |g| in size; exp, the fast division and the
+    # products add about 16 more.
+    b = 0.0 if layer.bias is None else 2 * np.abs(layer.bias)
+    eg, eu = 4 * (np.abs(g) + (b if np.isscalar(b) else b[0::2])), 4 * (np.abs(u) + (b if np.isscalar(b) else b[1::2]))
+    e = np.empty_like(z)
+    e[:, 0::2] = np.abs(dout) * (np.abs(u) * (1 + np.abs(g)) * (16 + eg) + eu * (1 + np.abs(g)))
+    e[:, 1::2] = np.abs(dout) * (np.abs(g) * 16 + eg * (1 + np.abs(g)))
+    w = gradient_weight(layer)
+    # dz is rounded to bf16 (2^-8) before the contraction; fp32 accumulation
+    # of N terms
+    e_dx = (2.0 ** -8 * np.abs(dz) + 2.0 ** -23 * e) @ np.abs(w) + z.shape[1] * 2.0 ** -24 * (np.abs(dz) @ np.abs(w))
+    return dz @ w, dz, e, e_dx
+
+
+def cross_entropy(layer, xq, xs, targets, ignore=-100):
+    """(loss, lse, logits) in float64."""
+    y = logits64(layer, xq, xs)
+    m = y.max(1)
+    base = np.where(np.isfinite(m), m, 0.0)
+    with np.errstate(divide="ignore"):
+        lse = base + np.log(np.exp(y - base[:, None]).sum(1))
+    ok = targets != ignore
+    loss = np.zeros(len(lse))
+    valid = ok & (targets >= 0) & (targets < y.shape[1])
+    loss[valid] = lse[valid] - y[valid, targets[valid]]
+    loss[ok & ~valid] = np.nan
+    return loss, lse, y
+
+
+def cross_entropy_backward(layer, xq, xs, targets, lse, dloss, ignore=-100):
+    """(dx, bound of its error before the last rounding) in float64."""
+    y = logits64(layer, xq, xs)
+    p = np.exp(y - lse[:, None])
+    hot = np.zeros_like(p)
+    ok = targets != ignore
+    hot[ok, targets[ok]] = 1.0
+    d = np.where(ok, dloss, 0.0)[:, None] * (p - hot)
+    assert np.isfinite(d).all()
+    w = gradient_weight(layer)
+    # an exponential: its argument's fp32 error (logit, lse and product, 2^-24
+    # of each magnitude, 4 roundings) and 2^-22 of the unit's own; then bf16
+    ay = np.where(p > 0, np.abs(y), 0.0)  # a masked entry has no error
+    e = np.where(ok, np.abs(dloss), 0.0)[:, None] * p * (4 * (ay + np.abs(lse)[:, None]) + 8) * 2.0 ** -24
+    e_dx = (2.0 ** -8 * np.abs(d) + 2 * e + 2.0 ** -133) @ np.abs(w)
+    e_dx = e_dx + y.shape[1] * 2.0 ** -24 * (np.abs(d) @ np.abs(w))
+    return d @ w, e_dx

@@ -1,0 +1,440 @@
+"""The gated layer's gradient and the cross entropy of a W4A8 head, on the GPU
+against 64-bit restatements; the operators run together as a training step."""
+import numpy as np
+import pytest
+import torch
+
+import w4a8_codebook_quantized_b200 as cr
+from w4a8_codebook_quantized_b200 import inputs
+
+from gpu_util import Guarded, bf16_dev, dev, host
+from operator_refs import (assert_bf16_near, bf16_round, cross_entropy, cross_entropy_backward, f64, gradient_weight,
+                           grid, hadamard, logits64, rotate64, swiglu_backward, to_bf16)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    cr.lib()
+    yield
+    cr.cr_check_device_error()
+
+
+def _quantised(M, K, seed, rows=None):
+    """int8 activations and scales as the rotation leaves them; `rows` >= M
+    rows in the buffers, the rest poisoned."""
+    rng = np.random.default_rng([seed, M, K])
+    z = rng.standard_normal((M, K))
+    xq = np.rint(z * (127 / np.abs(z).max(1, keepdims=True))).astype(np.int8)
+    xs = rng.uniform(0.02, 0.05, M).astype(np.float32)
+    rows = M if rows is None else rows
+    pq, ps = np.full((rows, K), 77, np.int8), np.full(rows, np.nan, np.float32)
+    pq[:M], ps[:M] = xq, xs
+    return xq, xs, dev(pq), dev(ps)
+
+
+def _layer_dev(ly):
+    return [dev(a) for a in (ly.qdata, ly.srel, ly.codebook, ly.s_channel)], None if ly.bias is None else dev(ly.bias)
+
+
+def _work(name, *shape):
+    return Guarded((getattr(cr.lib(), name + "_work_bytes")(*shape),), torch.uint8)
+
+
+# ---------------------------------------------------------------- gated layer
+
+@pytest.mark.parametrize("M,N,K,bias", [(1, 8, 256, False), (1, 264, 512, True), (8, 520, 256, False),
+                                        (37, 1000, 768, True), (128, 256, 256, False), (129, 2824, 1280, True),
+                                        (257, 512, 1024, False), (700, 6400, 256, True)])
+def test_swiglu_backward(M, N, K, bias):
+    """One row to several tiles, ragged rows and columns (N / 2 a multiple of
+    4 only), both GEMM forms."""
+    ly = inputs.layer(N, K, M + N, with_bias=bias)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 3, rows=M + 3)
+    dout = to_bf16(np.random.default_rng([M, N]).standard_normal((M, N // 2)))
+    w, b = _layer_dev(ly)
+    dx, dz = Guarded((M, K), torch.bfloat16), Guarded((M, N), torch.bfloat16)
+    work = _work("cr_w4a8_swiglu_backward", M, N, K)
+    cr.cr_w4a8_swiglu_backward(dout.cuda(), xq_d, xs_d, *w, bias=b, dx=dx.tensor, dz=dz.tensor, work=work.tensor)
+    torch.cuda.synchronize()
+    assert dx.intact() and dz.intact() and work.intact()
+    rx, rz, ez, ex = swiglu_backward(ly, xq, xs, f64(dout))
+    assert_bf16_near(dz.tensor, rz, ez, "dz")
+    assert_bf16_near(dx.tensor, rx, 0.0, "dx", extra=ex)
+    dx2, dz2 = cr.cr_w4a8_swiglu_backward(dout.cuda(), xq_d, xs_d, *w, bias=b)
+    assert torch.equal(dx2, dx.tensor) and torch.equal(dz2, dz.tensor)
+    # the contraction is the layer's own straight-through backward on dz
+    assert torch.equal(dx2, cr.cr_w4a8_ste_backward(dz2, *w))
+
+
+def test_swiglu_backward_of_large_gates():
+    """Gates of either sign far past where e^-|g| underflows."""
+    M, N, K = 16, 64, 256
+    ly = inputs.layer(N, K, 1, with_bias=True)
+    ly.bias[0::2] = np.linspace(-3e4, 3e4, N // 2)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 4)
+    dout = to_bf16(np.ones((M, N // 2)))
+    w, b = _layer_dev(ly)
+    dx, dz = cr.cr_w4a8_swiglu_backward(dout.cuda(), xq_d, xs_d, *w, bias=b)
+    rx, rz, ez, ex = swiglu_backward(ly, xq, xs, f64(dout))
+    assert torch.isfinite(dz).all() and torch.isfinite(dx).all()
+    assert_bf16_near(dz, rz, ez, "dz")
+
+
+def test_swiglu_backward_against_differences():
+    """dz against central differences of the forward's own formula."""
+    M, N, K = 3, 32, 256
+    ly = inputs.layer(N, K, 2)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 5)
+    dout = np.ones((M, N // 2))
+    w, b = _layer_dev(ly)
+    _, dz = cr.cr_w4a8_swiglu_backward(to_bf16(dout).cuda(), xq_d, xs_d, *w)
+    z = logits64(ly, xq, xs)
+
+    def f(zz):
+        g, u = zz[:, 0::2], zz[:, 1::2]
+        return g / (1 + np.exp(-g)) * u
+
+    step = 1e-5
+    num = np.empty_like(z)
+    for c in range(2):
+        e = np.zeros_like(z)
+        e[:, c::2] = step
+        num[:, c::2] = (f(z + e) - f(z - e)) / (2 * step)
+    scale = np.abs(num).max()
+    assert (np.abs(f64(dz) - num) <= 2.0 ** -8 * np.abs(num) + 1e-6 * scale).all()
+
+
+# ---------------------------------------------------------------- cross entropy
+
+def _targets(M, V, seed, ignored=True):
+    rng = np.random.default_rng([seed, M, V])
+    t = rng.integers(0, V, M)
+    if M > 1:
+        t[0], t[-1] = V - 1, 0
+    if ignored and M > 2:
+        t[1::3] = -100
+    return t
+
+
+CE_SHAPES = [(1, 1, 256, False), (1, 300, 512, True), (3, 4097, 256, False), (8, 2048, 768, True), (9, 257, 256, False),
+             (100, 255, 512, True), (129, 1000, 256, False), (300, 10007, 256, True), (513, 5000, 1024, False)]
+
+
+@pytest.mark.parametrize("M,V,K,bias", CE_SHAPES)
+def test_cross_entropy_forward(M, V, K, bias):
+    ly = inputs.layer(V, K, M + V, with_bias=bias)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 6, rows=M + 1)
+    t = _targets(M, V, 7)
+    w, b = _layer_dev(ly)
+    loss, lse = Guarded((M,), torch.float32), Guarded((M,), torch.float32)
+    work = _work("cr_w4a8_cross_entropy", M, V, K)
+    cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, dev(t), bias=b, loss=loss.tensor, lse=lse.tensor, work=work.tensor)
+    torch.cuda.synchronize()
+    assert loss.intact() and lse.intact() and work.intact()
+    r_loss, r_lse, y = cross_entropy(ly, xq, xs, t)
+    # a logit carries 4 roundings of its magnitude; a sum of V exponentials in
+    # 32-column chains, each 2^-22, and the log: well under 2^-19 in all
+    ymax = np.abs(y).max(1) + (0.0 if ly.bias is None else 2 * np.abs(ly.bias).max())
+    tol = 6 * ymax * 2.0 ** -24 + 2.0 ** -19
+    assert (np.abs(f64(lse.tensor) - r_lse) <= tol + 2.0 ** -24 * np.abs(r_lse)).all()
+    assert (np.abs(f64(loss.tensor) - r_loss) <= 2 * tol + 2.0 ** -24 * np.abs(r_loss)).all()
+    assert (f64(loss.tensor)[t == -100] == 0).all()
+    again = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, dev(t), bias=b)
+    assert torch.equal(again[0], loss.tensor) and torch.equal(again[1], lse.tensor)
+
+
+@pytest.mark.parametrize("M,V,K,bias", CE_SHAPES)
+def test_cross_entropy_backward(M, V, K, bias):
+    ly = inputs.layer(V, K, M + V, with_bias=bias)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 6, rows=M + 2)
+    t = _targets(M, V, 7)
+    _, r_lse, _ = cross_entropy(ly, xq, xs, t)
+    lse32 = r_lse.astype(np.float32)
+    dloss = np.random.default_rng(M).uniform(-1, 1, M).astype(np.float32)
+    w, b = _layer_dev(ly)
+    dx = Guarded((M, K), torch.bfloat16)
+    work = _work("cr_w4a8_cross_entropy_backward", M, V, K)
+    work.tensor.fill_(0xFF)  # NaN everywhere: nothing is read before it is written
+    cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(t), dev(lse32), dev(dloss), bias=b, dx=dx.tensor,
+                                      work=work.tensor)
+    torch.cuda.synchronize()
+    assert dx.intact() and work.intact()
+    rx, ex = cross_entropy_backward(ly, xq, xs, t, lse32.astype(np.float64), dloss.astype(np.float64))
+    assert_bf16_near(dx.tensor, rx, 0.0, "dx", extra=ex)
+    assert (f64(dx.tensor)[t == -100] == 0).all()
+    again = cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(t), dev(lse32), dev(dloss), bias=b)
+    assert torch.equal(again, dx.tensor)
+
+
+@pytest.mark.parametrize("M", [4, 40])
+def test_cross_entropy_of_masked_entries(M):
+    """A bias of -inf takes entries out: a whole tile of them, all but one, and
+    a target that is masked (loss inf).  Far logits and a lowest-value mask."""
+    V, K = 1100, 256
+    ly = inputs.layer(V, K, 5, with_bias=True)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 8)
+    t = np.full(M, 700)
+    t[1] = 10  # masked below
+    for mask in (-np.inf, np.finfo(np.float32).min):
+        ly.bias[:600] = mask
+        w, b = _layer_dev(ly)
+        loss, lse = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, dev(t), bias=b)
+        r_loss, r_lse, _ = cross_entropy(ly, xq, xs, t)
+        assert np.allclose(f64(lse), r_lse, rtol=1e-6)
+        assert np.allclose(f64(loss)[t == 700], r_loss[t == 700], rtol=1e-5, atol=1e-5)
+        assert f64(loss)[1] == np.inf if mask == -np.inf else f64(loss)[1] > 1e38
+        dx = cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(t), lse, torch.ones(M, device="cuda"), bias=b)
+        rx, ex = cross_entropy_backward(ly, xq, xs, t, f64(lse), np.ones(M))
+        assert_bf16_near(dx, rx, 0.0, "dx", extra=ex)
+    ly.bias[:] = -np.inf
+    ly.bias[701] = 2e4
+    w, b = _layer_dev(ly)
+    loss, lse = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, dev(np.full(M, 701)), bias=b)
+    assert np.abs(f64(loss)).max() <= 2e4 * 2.0 ** -22
+    ly.bias[:] = -np.inf
+    w, b = _layer_dev(ly)
+    loss, lse = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, dev(t), bias=b)
+    assert (f64(lse) == -np.inf).all()
+
+
+@pytest.mark.parametrize("M", [5, 30])
+def test_cross_entropy_of_invalid_targets(M):
+    """A target outside the vocabulary: NaN in its row alone; another
+    ignore_index; all rows ignored."""
+    V, K = 600, 256
+    ly = inputs.layer(V, K, 6)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 9)
+    t = _targets(M, V, 10, ignored=False)
+    bad = t.copy()
+    for i, v in enumerate((V, -1, -2 ** 63, 2 ** 63 - 1)):
+        bad[i] = v
+    w, _ = _layer_dev(ly)
+    one = torch.ones(M, device="cuda")
+    loss, lse = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, dev(t))
+    dx = cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(t), lse, one)
+    loss2, lse2 = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, dev(bad))
+    dx2 = cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(bad), lse, one)
+    assert torch.isnan(loss2[:4]).all() and torch.isnan(dx2[:4]).all()
+    assert torch.equal(loss2[4:], loss[4:]) and torch.equal(lse2, lse) and torch.equal(dx2[4:], dx[4:])
+    t3 = np.full(M, 7)
+    loss3, _ = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, dev(t3), ignore_index=7)
+    nan = torch.full((M,), float("nan"), device="cuda")
+    dx3 = cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(t3), nan, nan, ignore_index=7)
+    assert (loss3 == 0).all() and (dx3 == 0).all()
+
+
+def test_cross_entropy_gradient_against_differences():
+    """dx along directions of the activations' scale: d loss / d xs[m] is
+    sum_k dx[m, k] * xq[m, k] for a linear head (straight through)."""
+    M, V, K = 6, 500, 256
+    ly = inputs.layer(V, K, 7)
+    # channel scales exact in bf16, so that the gradient's weight is the forward's up to its own rounding
+    ly.s_channel[:] = bf16_round(ly.s_channel)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 11)
+    t = _targets(M, V, 12, ignored=False)
+    w, _ = _layer_dev(ly)
+    _, lse = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, dev(t))
+    dx = f64(cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(t), lse, torch.ones(M, device="cuda")))
+    h = 1e-6
+    up, dn = (cross_entropy(ly, xq, xs.astype(np.float64) + s, t)[0] for s in (h, -h))
+    num = (up - dn) / (2 * h)
+    got = (dx * xq).sum(1)
+    tol = 3 * 2.0 ** -8 * (np.abs(dx) * np.abs(xq)).sum(1)  # bf16 of dl, w and dx
+    assert (np.abs(got - num) <= tol).all()
+
+
+def test_cross_entropy_pieces():
+    """A vocabulary of several pieces, the last one ragged, forward and
+    backward (a wide layer makes the pieces short)."""
+    M, V, K = 70, 2 * 512 + 77, 131072
+    ly = inputs.layer(V, K, 8)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 13)
+    t = _targets(M, V, 14)
+    t[5], t[6], t[7] = 511, 512, V - 1
+    w, _ = _layer_dev(ly)
+    loss, lse = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, dev(t))
+    r_loss, r_lse, y = cross_entropy(ly, xq, xs, t)
+    tol = 6 * np.abs(y).max(1) * 2.0 ** -24 + 2.0 ** -19
+    assert (np.abs(f64(lse) - r_lse) <= tol + 2.0 ** -24 * np.abs(r_lse)).all()
+    assert (np.abs(f64(loss) - r_loss) <= 2 * tol + 2.0 ** -24 * np.abs(r_loss)).all()
+    dloss = np.full(M, 0.25, np.float32)
+    work = _work("cr_w4a8_cross_entropy_backward", M, V, K)
+    work.tensor.fill_(0xFF)
+    dx = cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(t), lse, dev(dloss), work=work.tensor)
+    assert work.intact()
+    rx, ex = cross_entropy_backward(ly, xq, xs, t, f64(lse), dloss.astype(np.float64))
+    assert_bf16_near(dx, rx, 0.0, "dx", extra=ex)
+
+
+def test_cross_entropy_row_blocks():
+    """More rows than one block of the gradient holds: rows of later blocks
+    equal those computed alone."""
+    M, V, K = 8192 + 300, 700, 256
+    ly = inputs.layer(V, K, 9)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 15)
+    t = dev(_targets(M, V, 16))
+    w, _ = _layer_dev(ly)
+    loss, lse = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, t)
+    dl = torch.rand(M, device="cuda")
+    dx = cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, t, lse, dl)
+    s = slice(8192, M)
+    loss2, lse2 = cr.cr_w4a8_cross_entropy(xq_d[s].contiguous(), xs_d[s].clone(), *w, t[s].clone())
+    dx2 = cr.cr_w4a8_cross_entropy_backward(xq_d[s].contiguous(), xs_d[s].clone(), *w, t[s].clone(), lse2, dl[s].clone())
+    assert torch.equal(loss[s], loss2) and torch.equal(lse[s], lse2) and torch.equal(dx[s], dx2)
+
+
+def test_no_rows():
+    ly = inputs.layer(64, 256, 1)
+    w, _ = _layer_dev(ly)
+    xq, xs = torch.empty(0, 256, dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda")
+    t = torch.empty(0, dtype=torch.int64, device="cuda")
+    loss, lse = cr.cr_w4a8_cross_entropy(xq, xs, *w, t)
+    assert loss.shape == (0,)
+    assert cr.cr_w4a8_cross_entropy_backward(xq, xs, *w, t, lse, loss).shape == (0, 256)
+    dx, dz = cr.cr_w4a8_swiglu_backward(torch.empty(0, 32, dtype=torch.bfloat16, device="cuda"), xq, xs, *w)
+    assert dx.shape == (0, 256) and dz.shape == (0, 64)
+
+
+def test_refusals():
+    ly = inputs.layer(64, 256, 1)
+    w, _ = _layer_dev(ly)
+    _, _, xq, xs = _quantised(4, 256, 1)
+    t = torch.zeros(4, dtype=torch.int64, device="cuda")
+    one = torch.ones(4, device="cuda")
+    small = torch.empty(64, dtype=torch.uint8, device="cuda")
+    do = torch.zeros(4, 32, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(TypeError):
+        cr.cr_w4a8_cross_entropy(xq, xs, *w, t.int())
+    with pytest.raises(ValueError):
+        cr.cr_w4a8_cross_entropy(xq[:2], xs, *w, t)
+    with pytest.raises(ValueError):
+        cr.cr_w4a8_cross_entropy(xq, xs, *w, t, work=small)
+    with pytest.raises(ValueError):
+        cr.cr_w4a8_cross_entropy_backward(xq, xs, *w, t, one[:3], one)
+    with pytest.raises(ValueError):
+        cr.cr_w4a8_cross_entropy_backward(xq, xs, *w, t, one, one, work=small)
+    with pytest.raises(ValueError):
+        cr.cr_w4a8_swiglu_backward(do[:, :16].contiguous(), xq, xs, *w)
+    with pytest.raises(ValueError):
+        cr.cr_w4a8_swiglu_backward(do, xq, xs, *w, work=small)
+    with pytest.raises(TypeError):
+        cr.cr_w4a8_swiglu_backward(do.float(), xq, xs, *w)
+    ly = inputs.layer(12, 256, 1)  # 12 rows: not a multiple of 8
+    w2, _ = _layer_dev(ly)
+    with pytest.raises(cr.CrError):
+        cr.cr_w4a8_swiglu_backward(do[:, :6].contiguous(), xq, xs, *w2)
+
+
+# ---------------------------------------------------------------- together
+
+class _Block:
+    """norm -> gated layer -> down projection -> + residual -> norm -> head and
+    its loss, with the gradients, in this package's calls."""
+
+    def __init__(self, M, K, F, V, seed=0):
+        rng = np.random.default_rng(seed)
+        self.ly = {n: inputs.layer(a, b, i) for i, (n, a, b) in enumerate((("gu", 2 * F, K), ("down", K, F),
+                                                                           ("head", V, K)))}
+        self.w = {n: _layer_dev(ly)[0] for n, ly in self.ly.items()}
+        self.gamma = [(1 + 0.1 * rng.standard_normal(K)).astype(np.float32) for _ in range(2)]
+        self.g = [dev(g) for g in self.gamma]
+        self.x = bf16_dev(inputs.activations(M, K, seed))
+        self.t = dev(_targets(M, V, seed))
+        self.dloss = torch.full((M,), 1.0 / M, device="cuda")
+
+    def step(self, **kw):
+        x, w = self.x, self.w
+        xq, xs, h0, r0 = cr.cr_rmsnorm_quant_act(x, self.g[0], **kw)
+        a = cr.cr_w4a8_gemm_swiglu(xq, xs, *w["gu"], **kw)
+        aq, asc = cr.cr_rotate_quant_act(a, **kw)
+        y = cr.cr_w4a8_gemm(aq, asc, *w["down"], **kw)
+        hq, hs, h1, r1 = cr.cr_rmsnorm_quant_act(y, self.g[1], residual=x, **kw)
+        loss, lse = cr.cr_w4a8_cross_entropy(hq, hs, *w["head"], self.t, **kw)
+        d = cr.cr_w4a8_cross_entropy_backward(hq, hs, *w["head"], self.t, lse, self.dloss, **kw)
+        dh1, dg1 = cr.cr_rmsnorm_backward(d, h1, self.g[1], r1, **kw)
+        da = cr.cr_rotate(cr.cr_w4a8_ste_backward(dh1, *w["down"], **kw), **kw)
+        d0, dz = cr.cr_w4a8_swiglu_backward(da, xq, xs, *w["gu"], **kw)
+        dx, dg0 = cr.cr_rmsnorm_backward(d0, x, self.g[0], r0, dres=dh1, **kw)
+        return {"loss": loss, "lse": lse, "h1": h1, "a": a, "dh1": dh1, "dz": dz, "dx": dx, "dg0": dg0, "dg1": dg1}
+
+
+def test_training_step_gradients():
+    """The whole step's gradients against the same chain in float64, built
+    from the real-valued layers (rotated weights as decoded), where only the
+    activations' quantisation and bf16 rounding separate the two: the
+    gradients of a chain of seven such steps agree to a few percent in norm."""
+    M, K, F, V = 48, 512, 768, 1000
+    blk = _Block(M, K, F, V)
+    got = blk.step()
+    x = f64(blk.x)
+    W = {n: grid(ly) * ly.s_channel.astype(np.float64)[:, None] for n, ly in blk.ly.items()}
+    t = host(blk.t)
+
+    def norm(h, g):
+        return h / np.sqrt((h ** 2).mean(1, keepdims=True) + 1e-6) * g
+
+    def forward(x, g0, g1):
+        z = rotate64(norm(x, g0)) @ W["gu"].T
+        gt, up = z[:, 0::2], z[:, 1::2]
+        a = gt / (1 + np.exp(-gt)) * up
+        h1 = x + rotate64(a) @ W["down"].T
+        y = rotate64(norm(h1, g1)) @ W["head"].T
+        lse = np.log(np.exp(y).sum(1))
+        ok = t >= 0
+        return (lse[ok] - y[ok, t[ok]]).sum() / M
+
+    g0, g1 = (g.astype(np.float64) for g in blk.gamma)
+    rng = np.random.default_rng(5)
+    assert abs(float(got["loss"].sum()) / M - forward(x, g0, g1)) < 0.02 * forward(x, g0, g1)
+    # directional derivatives along the gradient itself and along random directions
+    for name, arg in (("dx", 0), ("dg0", 1), ("dg1", 2)):
+        grad = f64(got[name])
+        along = grad / np.linalg.norm(grad)
+        base = [x, g0, g1]
+        eps = 1e-4
+        up, dn = list(base), list(base)
+        up[arg], dn[arg] = base[arg] + eps * along, base[arg] - eps * along
+        num = (forward(*up) - forward(*dn)) / (2 * eps)
+        assert abs(num - np.linalg.norm(grad)) <= 0.1 * abs(num), name
+
+
+def test_training_step_on_a_stream_and_in_a_graph():
+    """The same step on another stream, and captured and replayed on new
+    inputs while eager steps run between the replays."""
+    blk = _Block(40, 512, 256, 300, seed=1)
+    ref = blk.step()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = blk.step()
+    s.synchronize()
+    assert all(torch.equal(ref[k], got[k]) for k in ref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = blk.step()
+    for seed in (2, 3):
+        blk.x.copy_(bf16_dev(inputs.activations(40, 512, seed)))
+        graph.replay()
+        eager = blk.step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(eager[k], out[k]) for k in out)
+
+
+def test_two_streams_at_once():
+    """Two steps whose kernels overlap share no workspace."""
+    blks = [_Block(64, 512, 512, 900, seed=s) for s in (4, 5)]
+    refs = [b.step() for b in blks]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in blks]
+    outs = []
+    for _ in range(5):
+        for b, s in zip(blks, streams):
+            with torch.cuda.stream(s):
+                outs.append(b.step())
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert all(torch.equal(refs[i % 2][k], o[k]) for k in o)

@@ -116,3 +116,60 @@ def test_norm_gradient_formula_against_differences():
         e = np.zeros(K)
         e[k] = step
         assert abs((loss(h, gamma + e) - loss(h, gamma - e)) / (2 * step) - dg[k]) < 1e-6
+
+
+def test_swiglu_backward_validation(L):
+    need = L.cr_w4a8_swiglu_backward_work_bytes(4, 8, 256)
+    assert need >= 3 * 8 * 256 and L.cr_w4a8_swiglu_backward_work_bytes(4, 8, 300) == 0
+
+    def call(ptrs=(A,) * 8, M=4, N=8, K=256, dx=B, dz=C, work=A, wb=need):
+        return L.cr_w4a8_swiglu_backward(*ptrs, M, N, K, dx, dz, work, wb, None)
+
+    assert call(M=-1) == INVALID and call(M=2 ** 31) == UNSUPPORTED and call(N=-8) == INVALID
+    assert call(N=12) == UNSUPPORTED and call(K=320) == UNSUPPORTED
+    for i in range(7):  # dout, xq, xs, qdata, srel, codebook, s_channel; the bias is optional
+        assert call(ptrs=tuple(None if j == i else A for j in range(8))) == INVALID
+    for i in range(8):
+        assert call(ptrs=tuple(MIS if j == i else A for j in range(8))) == ALIGNMENT
+    assert call(dx=None) == INVALID and call(dz=None) == INVALID and call(work=None) == INVALID
+    assert call(dx=MIS) == ALIGNMENT and call(dz=MIS) == ALIGNMENT and call(work=MIS) == ALIGNMENT
+    assert call(wb=need - 1) == INVALID
+    assert call(ptrs=(None,) * 8, M=0, dx=None, dz=None, work=None, wb=0) == OK
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_cross_entropy_validation(L, backward):
+    name = "cr_w4a8_cross_entropy" + ("_backward" if backward else "")
+    need = getattr(L, name + "_work_bytes")(16, 8, 256)
+    assert need > 0 and getattr(L, name + "_work_bytes")(16, 0, 256) == 0
+
+    def call(ptrs=(A,) * 8, M=16, V=8, K=256, two=(B, C), dx=A, work=A, wb=need):
+        f = getattr(L, name)
+        if backward:
+            return f(*ptrs, -100, *two, M, V, K, dx, work, wb, None)
+        return f(*ptrs, -100, M, V, K, *two, work, wb, None)
+
+    assert call(M=-1) == INVALID and call(V=-1) == INVALID and call(V=0) == INVALID and call(K=320) == UNSUPPORTED
+    assert call(M=2 ** 31) == UNSUPPORTED and call(V=2 ** 31) == UNSUPPORTED
+    for i in (0, 1, 2, 3, 4, 5, 7):  # xq, xs, the layer, targets; the bias (6) is optional
+        assert call(ptrs=tuple(None if j == i else A for j in range(8))) == INVALID
+    for i in range(8):
+        assert call(ptrs=tuple(MIS if j == i else A for j in range(8))) == ALIGNMENT
+    for two in ((None, C), (B, None)):
+        assert call(two=two) == INVALID
+    for two in ((MIS, C), (B, MIS)):
+        assert call(two=two) == ALIGNMENT
+    if backward:
+        assert call(dx=None) == INVALID and call(dx=MIS) == ALIGNMENT
+    assert call(work=None) == INVALID and call(work=MIS) == ALIGNMENT and call(wb=need - 1) == INVALID
+    assert call(ptrs=(None,) * 8, M=0, two=(None, None), dx=None, work=None, wb=0) == OK
+
+
+def test_work_sizes_are_bounded(L):
+    """The cross entropy's buffers do not grow with the vocabulary or with the
+    rows beyond one block, but for the 8 bytes per 256 outputs."""
+    f, b = L.cr_w4a8_cross_entropy_work_bytes, L.cr_w4a8_cross_entropy_backward_work_bytes
+    assert b(8192, 262144, 4096) <= 600 << 20
+    assert b(1 << 20, 262144, 4096) == b(8192, 262144, 4096)
+    assert f(2048, 262144, 4096) <= (64 << 20) + (2048 * 1024 * 8) + (1 << 20)
+    assert f(1 << 20, 131072, 4096) == f(32768, 131072, 4096)

@@ -32,6 +32,7 @@ __all__ = [
     "cr_w4a8_ste_backward", "cr_w4a8_dequant_t_bf16", "cr_selftest_wait_timeout", "cr_gemm_s8",
     "cr_w4a8_gemm_ws", "cr_w4a8_linear_ws", "cr_w4a8_ste_backward_ws", "cr_mma_i8_peak",
     "cr_rmsnorm_quant_act", "cr_rmsnorm_backward", "cr_rotate",
+    "cr_w4a8_swiglu_backward", "cr_w4a8_cross_entropy", "cr_w4a8_cross_entropy_backward",
     "cr_status_string", "cr_version",
     "gemv_rows",
 ]
@@ -116,6 +117,14 @@ def lib() -> ctypes.CDLL:
             L.cr_rmsnorm_backward_work_bytes.restype = i64
             L.cr_rmsnorm_backward.argtypes = [P, P, P, i32, P, P, i64, i64, P, P, P, i64, P]
             L.cr_rotate.argtypes = [P, i64, i64, P, P]
+            layer = [P, P, P, P, P]  # qdata, srel, codebook, s_channel, bias
+            L.cr_w4a8_swiglu_backward.argtypes = [P, P, P, *layer, i64, i64, i64, P, P, P, i64, P]
+            L.cr_w4a8_cross_entropy.argtypes = [P, P, *layer, P, i64, i64, i64, i64, P, P, P, i64, P]
+            L.cr_w4a8_cross_entropy_backward.argtypes = [P, P, *layer, P, i64, P, P, i64, i64, i64, P, P, i64, P]
+            for name in ("cr_w4a8_swiglu_backward", "cr_w4a8_cross_entropy", "cr_w4a8_cross_entropy_backward"):
+                work_bytes = getattr(L, name + "_work_bytes")
+                work_bytes.argtypes = [i64, i64, i64]
+                work_bytes.restype = i64
             LP = ctypes.POINTER(CrLayer)
             L.cr_w4a8_gemv_grouped.argtypes = [P, P, P, i64, i64, LP, i32, i32, P]
             L.cr_w4a8_linear_grouped.argtypes = [P, P, i64, i64, LP, i32, i32, i32, P, P, P]
@@ -1088,6 +1097,98 @@ def cr_rotate(x, out=None):
         _need(out, "out", (torch.bfloat16,), shape=x.shape)
     _check(lib().cr_rotate(_ptr(x), x.shape[0], x.shape[1], _ptr(out), _stream(None)), "cr_rotate")
     return out
+
+
+# ---------------------------------------------------------------- gated layer's gradient, cross entropy
+
+def _activations(xq, xs, M, K):
+    torch = _torch()
+    _need(xq, "xq", (torch.int8,), 2)
+    _need(xs, "xs", (torch.float32,), 1)
+    if xq.shape[1] != K or xq.shape[0] < M or xs.shape[0] < M:
+        raise ValueError(f"xq {tuple(xq.shape)} / xs {tuple(xs.shape)} do not match M={M}, K={K}")
+
+
+@_on_stream
+def cr_w4a8_swiglu_backward(dout, xq, xs, qdata, srel, codebook, s_channel, bias=None, dx=None, dz=None, work=None):
+    """The gradient of a gated layer (interleaved gate/up rows [2F, K], as
+    cr_w4a8_linear_swiglu runs it): dout [M, F] bf16 and the forward's quantised
+    activations -> (dx bf16 [M, K], the gradient of the rotated input; dz bf16
+    [M, 2F], that of the interleaved projections' outputs).  2F % 8 == 0.
+    work: uint8, at least lib().cr_w4a8_swiglu_backward_work_bytes(M, 2F, K)."""
+    torch = _torch()
+    N, K = _layer(qdata, srel, codebook, s_channel, bias)
+    _need(dout, "dout", (torch.bfloat16,), 2)
+    M = dout.shape[0]
+    if 2 * dout.shape[1] != N:
+        raise ValueError(f"dout has {dout.shape[1]} columns, the interleaved layer {N} rows")
+    _activations(xq, xs, M, K)
+    if dx is None:
+        dx = torch.empty(M, K, dtype=torch.bfloat16, device=dout.device)
+    else:
+        _need(dx, "dx", (torch.bfloat16,), shape=(M, K))
+    if dz is None:
+        dz = torch.empty(M, N, dtype=torch.bfloat16, device=dout.device)
+    else:
+        _need(dz, "dz", (torch.bfloat16,), shape=(M, N))
+    work = _work_buffer(work, lib().cr_w4a8_swiglu_backward_work_bytes(M, N, K), dout.device)
+    _check(lib().cr_w4a8_swiglu_backward(_ptr(dout), _ptr(xq), _ptr(xs), _ptr(qdata), _ptr(srel), _ptr(codebook),
+                                         _ptr(s_channel), _ptr(bias), M, N, K, _ptr(dx), _ptr(dz), _ptr(work),
+                                         work.numel(), _stream(None)), "cr_w4a8_swiglu_backward")
+    return dx, dz
+
+
+@_on_stream
+def cr_w4a8_cross_entropy(xq, xs, qdata, srel, codebook, s_channel, targets, bias=None, ignore_index: int = -100,
+                          loss=None, lse=None, work=None):
+    """Softmax cross entropy of a W4A8 head [V, K] on quantised activations,
+    without storing the outputs: targets [M] int64 -> (loss fp32 [M], 0 in rows
+    whose target is ignore_index; lse fp32 [M]).  Any V >= 1.
+    work: uint8, at least lib().cr_w4a8_cross_entropy_work_bytes(M, V, K)."""
+    torch = _torch()
+    V, K = _layer(qdata, srel, codebook, s_channel, bias)
+    _need(targets, "targets", (torch.int64,), 1)
+    M = targets.shape[0]
+    _activations(xq, xs, M, K)
+    if loss is None:
+        loss = torch.empty(M, dtype=torch.float32, device=xq.device)
+    else:
+        _need(loss, "loss", (torch.float32,), shape=(M,))
+    if lse is None:
+        lse = torch.empty(M, dtype=torch.float32, device=xq.device)
+    else:
+        _need(lse, "lse", (torch.float32,), shape=(M,))
+    work = _work_buffer(work, lib().cr_w4a8_cross_entropy_work_bytes(M, V, K), xq.device)
+    _check(lib().cr_w4a8_cross_entropy(_ptr(xq), _ptr(xs), _ptr(qdata), _ptr(srel), _ptr(codebook), _ptr(s_channel),
+                                       _ptr(bias), _ptr(targets), int(ignore_index), M, V, K, _ptr(loss), _ptr(lse),
+                                       _ptr(work), work.numel(), _stream(None)), "cr_w4a8_cross_entropy")
+    return loss, lse
+
+
+@_on_stream
+def cr_w4a8_cross_entropy_backward(xq, xs, qdata, srel, codebook, s_channel, targets, lse, dloss, bias=None,
+                                   ignore_index: int = -100, dx=None, work=None):
+    """The gradient of cr_w4a8_cross_entropy with respect to the head's rotated
+    input: lse [M] of the forward and dloss [M] fp32, the gradient of its loss
+    (1 / count for a mean) -> dx bf16 [M, K].
+    work: uint8, at least lib().cr_w4a8_cross_entropy_backward_work_bytes(M, V, K)."""
+    torch = _torch()
+    V, K = _layer(qdata, srel, codebook, s_channel, bias)
+    _need(targets, "targets", (torch.int64,), 1)
+    M = targets.shape[0]
+    _activations(xq, xs, M, K)
+    _need(lse, "lse", (torch.float32,), shape=(M,))
+    _need(dloss, "dloss", (torch.float32,), shape=(M,))
+    if dx is None:
+        dx = torch.empty(M, K, dtype=torch.bfloat16, device=xq.device)
+    else:
+        _need(dx, "dx", (torch.bfloat16,), shape=(M, K))
+    work = _work_buffer(work, lib().cr_w4a8_cross_entropy_backward_work_bytes(M, V, K), xq.device)
+    _check(lib().cr_w4a8_cross_entropy_backward(_ptr(xq), _ptr(xs), _ptr(qdata), _ptr(srel), _ptr(codebook),
+                                                _ptr(s_channel), _ptr(bias), _ptr(targets), int(ignore_index),
+                                                _ptr(lse), _ptr(dloss), M, V, K, _ptr(dx), _ptr(work), work.numel(),
+                                                _stream(None)), "cr_w4a8_cross_entropy_backward")
+    return dx
 
 
 def cr_mma_i8_peak(iters: int, stream=None) -> float:

@@ -364,6 +364,15 @@ __device__ __forceinline__ void tma_store_2d(const void *tmap, int32_t x, int32_
                  : "memory");
 }
 
+// The same, adding the box's fp32 elements to those in memory.
+__device__ __forceinline__ void tma_add_2d(const void *tmap, int32_t x, int32_t y, const void *smem_src)
+{
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     tmap),
+                 "r"(x), "r"(y), "r"(smem_u32(smem_src))
+                 : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
 // Wait until at most N committed bulk groups still read their shared-memory source.

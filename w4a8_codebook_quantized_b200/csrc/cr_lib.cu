@@ -17,6 +17,7 @@
 
 #include "cr_w4a8.h"
 #include "cr_device.cuh"
+#include "k_ce.cuh"
 #include "k_elementwise.cuh"
 #include "k_gemm.cuh"
 #include "k_gemv.cuh"
@@ -36,15 +37,13 @@ struct DeviceState {
     cudaMemPool_t pool = nullptr;  // stream-ordered pool for the weight transients (release threshold 0)
     // kernel attributes set once (cudaFuncSetAttribute is idempotent; atomic
     // flags so that concurrent first calls do not race on the flag itself)
-    std::atomic<bool> gemm_attr_set{false};
-    std::atomic<bool> gemm_pair_attr_set{false};
+    std::atomic<bool> gemm_attr_set[6] = {};       // by gm::Mode
+    std::atomic<bool> gemm_pair_attr_set[6] = {};
     std::atomic<bool> gemv_attr_set{false};
     std::atomic<bool> gemv_split_attr_set{false};
     std::atomic<bool> gemv32_attr_set{false};
     std::atomic<bool> gemv32_split_attr_set{false};
     std::atomic<bool> gemv_grouped_attr_set{false};
-    std::atomic<bool> gemm_bf16_attr_set{false};
-    std::atomic<bool> gemm_pair_bf16_attr_set{false};
     std::atomic<bool> peak_attr_set{false};
     // side stream and events on which cr_w4a8_linear's prefill path decodes
     // the weight while the activations are rotated and quantised
@@ -457,87 +456,107 @@ cr_status side_stream(DeviceState &d)
     return CR_OK;
 }
 
+// A tcgen05 GEMM over A [M, K] and B [N, K] (both int8 or both bf16, by
+// MODE), `to` the output's tensor map (any map when nothing leaves through it):
+// CTA pairs (256 x 256 tiles) when there is at least one tile per SM pair,
+// otherwise one CTA per 128 x 256 tile.
+struct GemmEpilogue {
+    const float *xs = nullptr, *ws = nullptr, *bias = nullptr;
+    int out_f32 = 0, swiglu = 0, tma_out = 1;
+    void *out = nullptr;
+    int32_t *acc_out = nullptr;
+    cr::gm::EpiArgs ex;
+};
+
+template <int MODE>
+cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtensorMap *to, int64_t M, int64_t N,
+                      int64_t K, const GemmEpilogue &e, cudaStream_t stream)
+{
+    using namespace cr;
+    auto map = [&](CUtensorMap *m, const void *base, int64_t rows, uint32_t box_rows) {
+        return gm::is_bf16(MODE) ? make_tmap_bf16(m, base, (uint64_t)K, (uint64_t)rows, 64u, box_rows)
+                                 : make_tmap_i8(m, base, (uint64_t)K, (uint64_t)rows, box_rows);
+    };
+    auto opt_in = [](std::atomic<bool> &flag, const void *kern, size_t bytes) {
+        if (flag)
+            return true;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        flag = true;
+        return true;
+    };
+    const int64_t pair_tiles = ((M + 255) / 256) * ((N + gm::BN - 1) / gm::BN);
+    const bool use_pair = pair_tiles >= d.num_sms / 2;
+    CUtensorMap ta, tb;
+    if (!map(&ta, A, M, (uint32_t)gm::BM) || !map(&tb, B, N, use_pair ? 128u : (uint32_t)gm::BN))
+        return CR_ERR_CUDA;
+    const CUtensorMap &tm_out = to ? *to : ta;  // placeholder when the output does not go through TMA
+    if (use_pair) {
+        if (!opt_in(d.gemm_pair_attr_set[MODE], (const void *)gm::gemm_pair_kernel<MODE>, gm::pair::kSmemBytes))
+            return CR_ERR_CUDA;
+        const int64_t pairs = pair_tiles < d.num_sms / 2 ? pair_tiles : d.num_sms / 2;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(2 * pairs));
+        cfg.blockDim = dim3(gm::kThreads);
+        cfg.dynamicSmemBytes = gm::pair::kSmemBytes;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return launched(cudaLaunchKernelEx(&cfg, gm::gemm_pair_kernel<MODE>, ta, tb, tm_out, e.xs, e.ws, e.bias, (int)M,
+                                           (int)N, (int)K, e.out_f32, e.swiglu, e.tma_out, e.out, e.acc_out, e.ex));
+    }
+    if (!opt_in(d.gemm_attr_set[MODE], (const void *)gm::gemm_kernel<MODE>, gm::kSmemBytes))
+        return CR_ERR_CUDA;
+    const int64_t tiles = ((M + gm::BM - 1) / gm::BM) * ((N + gm::BN - 1) / gm::BN);
+    const int grid = (int)(tiles < d.num_sms ? tiles : d.num_sms);
+    gm::gemm_kernel<MODE><<<grid, gm::kThreads, gm::kSmemBytes, stream>>>(ta, tb, tm_out, e.xs, e.ws, e.bias, (int)M,
+                                                                         (int)N, (int)K, e.out_f32, e.swiglu, e.tma_out,
+                                                                         e.out, e.acc_out, e.ex);
+    return launched(cudaGetLastError());
+}
+
+// The tensor map of a row-major output [M, cols] leaving in boxes of 32 rows x
+// 128 bytes, 128-byte swizzle; rows must be multiples of 16 bytes.
+bool make_tmap_out(CUtensorMap *to, void *out, int64_t M, int64_t cols, bool f32)
+{
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)M};
+    const cuuint64_t strides[1] = {(cuuint64_t)cols * (f32 ? 4u : 2u)};
+    const cuuint32_t box[2] = {f32 ? 32u : 64u, 32u};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return g_encode_tiled(to, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The int8 contraction with the fused epilogue on an int8 weight w8 [N, K]
-// (already decoded): tcgen05 GEMM on CTA pairs (256 x 256 tiles) when there
-// is at least one tile per SM pair, otherwise one CTA per 128 x 256 tile.
+// (already decoded).
 cr_status gemm_on_w8(DeviceState &d, const int8_t *xq, const float *xs, const int8_t *w8, const float *s_channel,
                      const float *bias, int64_t M, int64_t N, int64_t K, cr_out_dtype out_dtype, void *out,
                      int32_t *acc_out, cudaStream_t stream, int swiglu)
 {
-    using namespace cr;
-    cr_status st = CR_OK;
-    if (!d.gemm_attr_set) {
-        if (cudaFuncSetAttribute(gm::gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)gm::kSmemBytes) != cudaSuccess) {
-            cudaGetLastError();
-            return CR_ERR_CUDA;
-        }
-        d.gemm_attr_set = true;
-    }
-    CUtensorMap ta, tb, to;
-    const int out_f32 = out_dtype == CR_OUT_F32;
+    GemmEpilogue e;
+    e.xs = xs;
+    e.ws = s_channel;
+    e.bias = bias;
+    e.out_f32 = out_dtype == CR_OUT_F32;
+    e.swiglu = swiglu;
+    e.out = out;
+    e.acc_out = acc_out;
     const int64_t OC = swiglu ? N / 2 : N;  // output columns
-    const int vec_ok = out_f32 ? (OC % 4 == 0) : (OC % 8 == 0);
     // Output through TMA bulk stores when rows are 16-byte multiples and the
-    // int32 accumulators are not requested: 32-row x 128-byte boxes, 128B swizzle.
-    const int tma_out = vec_ok && acc_out == nullptr;
-    if (st == CR_OK && (!make_tmap_i8(&ta, xq, (uint64_t)K, (uint64_t)M, (uint32_t)gm::BM) ||
-                        !make_tmap_i8(&tb, w8, (uint64_t)K, (uint64_t)N, (uint32_t)gm::BN)))
-        st = CR_ERR_CUDA;
-    if (st == CR_OK) {
-        to = ta;  // placeholder when the output does not go through TMA
-        if (tma_out) {
-            const cuuint64_t dims[2] = {(cuuint64_t)OC, (cuuint64_t)M};
-            const cuuint64_t strides[1] = {(cuuint64_t)OC * (out_f32 ? 4u : 2u)};
-            const cuuint32_t box[2] = {out_f32 ? 32u : 64u, 32u};
-            const cuuint32_t estr[2] = {1u, 1u};
-            if (g_encode_tiled(&to, out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out,
-                               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-                st = CR_ERR_CUDA;
-        }
-    }
-    const int64_t pair_tiles = ((M + 255) / 256) * ((N + gm::BN - 1) / gm::BN);
-    const bool use_pair = pair_tiles >= d.num_sms / 2;
-    if (st == CR_OK && use_pair) {
-        CUtensorMap tb_half;
-        if (!d.gemm_pair_attr_set) {
-            if (cudaFuncSetAttribute(gm::gemm_pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)gm::pair::kSmemBytes) != cudaSuccess) {
-                cudaGetLastError();
-                st = CR_ERR_CUDA;
-            } else {
-                d.gemm_pair_attr_set = true;
-            }
-        }
-        if (st == CR_OK && !make_tmap_i8(&tb_half, w8, (uint64_t)K, (uint64_t)N, 128u))
-            st = CR_ERR_CUDA;
-        if (st == CR_OK) {
-            const int64_t pairs = pair_tiles < d.num_sms / 2 ? pair_tiles : d.num_sms / 2;
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((unsigned)(2 * pairs));
-            cfg.blockDim = dim3(gm::kThreads);
-            cfg.dynamicSmemBytes = gm::pair::kSmemBytes;
-            cfg.stream = stream;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = 2;
-            attr[0].val.clusterDim.y = 1;
-            attr[0].val.clusterDim.z = 1;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            st = launched(cudaLaunchKernelEx(&cfg, gm::gemm_pair_kernel<false>, ta, tb_half, to, xs, s_channel, bias, (int)M,
-                                             (int)N, (int)K, out_f32, swiglu, tma_out, out, acc_out));
-        }
-    } else if (st == CR_OK) {
-        const int64_t tiles = ((M + gm::BM - 1) / gm::BM) * ((N + gm::BN - 1) / gm::BN);
-        const int grid = (int)(tiles < d.num_sms ? tiles : d.num_sms);
-        gm::gemm_kernel<false><<<grid, gm::kThreads, gm::kSmemBytes, stream>>>(ta, tb, to, xs, s_channel, bias, (int)M,
-                                                                         (int)N, (int)K, out_f32, swiglu, tma_out, out,
-                                                                         acc_out);
-        st = launched(cudaGetLastError());
-    }
-    return st;
+    // int32 accumulators are not requested.
+    e.tma_out = (e.out_f32 ? OC % 4 == 0 : OC % 8 == 0) && acc_out == nullptr;
+    CUtensorMap to;
+    if (e.tma_out && !make_tmap_out(&to, out, M, OC, e.out_f32))
+        return CR_ERR_CUDA;
+    return launch_gemm<cr::gm::kI8>(d, xq, w8, e.tma_out ? &to : nullptr, M, N, K, e, stream);
 }
 
 // The prefill contraction.  When `activations` is given (cr_w4a8_linear), it
@@ -992,8 +1011,8 @@ cr_status cr_w4a8_dequant_t_bf16(const uint8_t *qdata, const uint8_t *srel, cons
     st = current_device(&d);
     if (st != CR_OK)
         return st;
-    return launched(cr::ew::launch_dequant_t_bf16(qdata, srel, codebook, s_channel, (int)N, (int)K, wt, d->num_sms,
-                                                  stream));
+    return launched(cr::ew::launch_dequant_t_bf16(qdata, srel, codebook, s_channel, (int)N, (int)K, (int)N, wt,
+                                                  d->num_sms, stream));
 }
 
 namespace {
@@ -1026,14 +1045,6 @@ cr_status ste_backward_impl(const uint16_t *grad, const uint8_t *qdata, const ui
     if (st != CR_OK)
         return st;
     using namespace cr;
-    if (!d->gemm_bf16_attr_set) {
-        if (cudaFuncSetAttribute(gm::gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)gm::kSmemBytes) != cudaSuccess) {
-            cudaGetLastError();
-            return CR_ERR_CUDA;
-        }
-        d->gemm_bf16_attr_set = true;
-    }
     // the transposed bf16 weight: the caller's transient, or one from the
     // stream-ordered pool
     uint16_t *wt = wt_work;
@@ -1042,53 +1053,16 @@ cr_status ste_backward_impl(const uint16_t *grad, const uint8_t *qdata, const ui
         cudaGetLastError();
         return CR_ERR_CUDA;
     }
-    st = launched(ew::launch_dequant_t_bf16(qdata, srel, codebook, s_channel, (int)N, (int)K, wt, d->num_sms, stream));
+    st = launched(ew::launch_dequant_t_bf16(qdata, srel, codebook, s_channel, (int)N, (int)K, (int)N, wt, d->num_sms,
+                                            stream));
     // dx [M, K] = grad [M, N] x wt [K, N]^T: the GEMM's rows are M, its columns K, its reduction N
-    CUtensorMap ta, tb, to;
-    if (st == CR_OK && (!make_tmap_bf16(&ta, grad, (uint64_t)N, (uint64_t)M, 64u, (uint32_t)gm::BM) ||
-                        !make_tmap_bf16(&tb, wt, (uint64_t)N, (uint64_t)K, 64u, (uint32_t)gm::BN) ||
-                        !make_tmap_bf16(&to, dx, (uint64_t)K, (uint64_t)M, 64u, 32u)))
+    CUtensorMap to;
+    if (st == CR_OK && !make_tmap_out(&to, dx, M, K, false))
         st = CR_ERR_CUDA;
-    // 256 x 256 tiles on CTA pairs when there is at least one per SM pair
-    const int64_t pair_tiles = ((M + 255) / 256) * ((K + gm::BN - 1) / gm::BN);
-    if (st == CR_OK && pair_tiles >= d->num_sms / 2) {
-        CUtensorMap tb_half;
-        if (!d->gemm_pair_bf16_attr_set) {
-            if (cudaFuncSetAttribute(gm::gemm_pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)gm::pair::kSmemBytes) != cudaSuccess) {
-                cudaGetLastError();
-                st = CR_ERR_CUDA;
-            } else {
-                d->gemm_pair_bf16_attr_set = true;
-            }
-        }
-        if (st == CR_OK && !make_tmap_bf16(&tb_half, wt, (uint64_t)N, (uint64_t)K, 64u, 128u))
-            st = CR_ERR_CUDA;
-        if (st == CR_OK) {
-            const int64_t pairs = pair_tiles < d->num_sms / 2 ? pair_tiles : d->num_sms / 2;
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((unsigned)(2 * pairs));
-            cfg.blockDim = dim3(gm::kThreads);
-            cfg.dynamicSmemBytes = gm::pair::kSmemBytes;
-            cfg.stream = stream;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = 2;
-            attr[0].val.clusterDim.y = 1;
-            attr[0].val.clusterDim.z = 1;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            st = launched(cudaLaunchKernelEx(&cfg, gm::gemm_pair_kernel<true>, ta, tb_half, to, (const float *)nullptr,
-                                             (const float *)nullptr, (const float *)nullptr, (int)M, (int)K, (int)N,
-                                             0, 0, 1, (void *)dx, (int32_t *)nullptr));
-        }
-    } else if (st == CR_OK) {
-        const int64_t tiles = ((M + gm::BM - 1) / gm::BM) * ((K + gm::BN - 1) / gm::BN);
-        const int grid = (int)(tiles < d->num_sms ? tiles : d->num_sms);
-        gm::gemm_kernel<true><<<grid, gm::kThreads, gm::kSmemBytes, stream>>>(
-            ta, tb, to, nullptr, nullptr, nullptr, (int)M, (int)K, (int)N, /*out_f32=*/0, /*swiglu=*/0,
-            /*tma_out=*/1, dx, nullptr);
-        st = launched(cudaGetLastError());
+    if (st == CR_OK) {
+        GemmEpilogue e;
+        e.out = dx;
+        st = launch_gemm<gm::kBf16>(*d, grad, wt, &to, M, K, N, e, stream);
     }
     if (!ws_given && cudaFreeAsync(wt, stream) != cudaSuccess) {
         cudaGetLastError();
@@ -1246,6 +1220,320 @@ cr_status cr_rotate(const uint16_t *x, int64_t M, int64_t K, uint16_t *out, cr_s
     if (ds != CR_OK)
         return ds;
     return launched(cr::nm::launch_rotate(x, M, K, out, d->num_sms, stream));
+}
+
+// ---------------------------------------------------------------- gated layer's gradient, cross entropy
+
+namespace {
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// A work buffer handed out in 256-byte aligned parts.
+struct Parts {
+    uint8_t *base;
+    int64_t used = 0;
+    explicit Parts(void *p) : base(static_cast<uint8_t *>(p)) {}
+    void *take(int64_t bytes)
+    {
+        void *p = base ? base + used : nullptr;
+        used += round_up(bytes, 256);
+        return p;
+    }
+};
+
+struct SwigluWork {
+    int8_t *w8;
+    uint16_t *wt;
+    int64_t bytes;
+    SwigluWork(void *work, int64_t N, int64_t K)
+    {
+        Parts p(work);
+        w8 = static_cast<int8_t *>(p.take(N * K));
+        wt = static_cast<uint16_t *>(p.take(2 * N * K));
+        bytes = p.used;
+    }
+};
+
+// The cross entropy runs over the vocabulary in pieces of `piece` entries (a
+// multiple of the GEMM's tile width; the last one may be shorter) and over the
+// rows in blocks, so that its buffers do not grow with V or M: a decoded piece
+// holds at most kPieceElems weights, a block's gradient of a piece at most
+// kPieceElems values, and a block at most kFwdRows / kBwdRows rows.  64 Mi
+// elements keep every contraction of a piece at tens of tiles per SM pair
+// while its operands (64 and 128 MB) stay near the L2's 126 MB.
+constexpr int64_t kPieceElems = 64ll << 20;
+constexpr int64_t kFwdRows = 32768, kBwdRows = 8192;
+
+int64_t ce_piece(int64_t V, int64_t per_entry)
+{
+    int64_t most = kPieceElems / per_entry / cr::gm::BN * cr::gm::BN;
+    if (most < cr::gm::BN)
+        most = cr::gm::BN;
+    const int64_t n = (V + most - 1) / most;
+    return round_up((V + n - 1) / n, cr::gm::BN);
+}
+
+struct CeFwdWork {
+    int64_t rows, piece, slices;
+    int8_t *w8 = nullptr;
+    float *y = nullptr;
+    float2 *part;
+    float *tlogit;
+    int64_t bytes;
+    CeFwdWork(void *work, int64_t M, int64_t V, int64_t K)
+    {
+        Parts p(work);
+        rows = M < kFwdRows ? M : kFwdRows;
+        piece = ce_piece(V, K);
+        if (M <= CR_GEMV_MAX_M) {
+            slices = (V + cr::ce::kSlice - 1) / cr::ce::kSlice;
+            y = static_cast<float *>(p.take(4 * M * V));
+        } else {
+            slices = (V + cr::gm::BN - 1) / cr::gm::BN;
+            w8 = static_cast<int8_t *>(p.take((piece < V ? piece : V) * K));
+        }
+        part = static_cast<float2 *>(p.take(8 * slices * rows));
+        tlogit = static_cast<float *>(p.take(4 * rows));
+        bytes = p.used;
+    }
+};
+
+struct CeBwdWork {
+    int64_t rows, piece;
+    int8_t *w8;
+    uint16_t *wt, *dl;
+    float *acc;  // fp32 sum over the pieces (null: one piece)
+    int64_t bytes;
+    CeBwdWork(void *work, int64_t M, int64_t V, int64_t K)
+    {
+        Parts p(work);
+        rows = M < kBwdRows ? M : kBwdRows;
+        piece = ce_piece(V, rows > K ? rows : K);
+        const int64_t most = piece < V ? piece : round_up(V, 8);
+        w8 = static_cast<int8_t *>(p.take(most * K));
+        wt = static_cast<uint16_t *>(p.take(2 * most * K));
+        dl = static_cast<uint16_t *>(p.take(2 * most * rows));
+        acc = piece < V ? static_cast<float *>(p.take(4 * rows * K)) : nullptr;
+        bytes = p.used;
+    }
+};
+
+bool good_shape(int64_t M, int64_t N, int64_t K)
+{
+    return M > 0 && N > 0 && M <= INT_MAX && N <= INT_MAX && check_k(K) == CR_OK;
+}
+
+// The arguments both directions of the cross entropy share.
+cr_status check_ce(const int8_t *xq, const float *xs, const uint8_t *qdata, const uint8_t *srel,
+                   const float *codebook, const float *s_channel, const float *bias, const int64_t *targets, int64_t M,
+                   int64_t V, int64_t K, const void *a, const void *b, const void *c)
+{
+    if (V == 0 && M > 0)  // the softmax of no outputs
+        return CR_ERR_INVALID_ARG;
+    // a, b, c: the direction's own buffers, `a` in the place of the output
+    cr_status st = check_contraction(xq, xs, qdata, srel, codebook, s_channel, bias, M, V, K, CR_OUT_F32,
+                                     const_cast<void *>(a), nullptr);
+    if (st != CR_OK || M == 0)
+        return st;
+    if (!targets || !b || !c)
+        return CR_ERR_INVALID_ARG;
+    if (!aligned16(targets) || !aligned16(b) || !aligned16(c))
+        return CR_ERR_ALIGNMENT;
+    return CR_OK;
+}
+
+cr_status check_work(const void *work, int64_t have, int64_t need)
+{
+    if (!work || have < need)
+        return CR_ERR_INVALID_ARG;
+    return aligned16(work) ? CR_OK : CR_ERR_ALIGNMENT;
+}
+}  // namespace
+
+int64_t cr_w4a8_swiglu_backward_work_bytes(int64_t M, int64_t N, int64_t K)
+{
+    return good_shape(M, N, K) ? SwigluWork(nullptr, N, K).bytes : 0;
+}
+
+cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const float *xs, const uint8_t *qdata,
+                                  const uint8_t *srel, const float *codebook, const float *s_channel,
+                                  const float *bias, int64_t M, int64_t N, int64_t K, uint16_t *dx, uint16_t *dz,
+                                  void *work, int64_t work_bytes, cr_stream_t stream)
+{
+    if (M < 0 || M > INT_MAX)
+        return M < 0 ? CR_ERR_INVALID_ARG : CR_ERR_UNSUPPORTED;
+    cr_status st = check_backward(qdata, srel, codebook, s_channel, N, K, dout, dx, /*empty=*/M == 0);
+    if (st != CR_OK || M == 0)
+        return st;
+    if (!dx)
+        return CR_ERR_INVALID_ARG;
+    if (!aligned16(dx))
+        return CR_ERR_ALIGNMENT;
+    if (N == 0)  // an empty sum: dx = 0
+        return launched(cudaMemsetAsync(dx, 0, (size_t)(M * K) * 2, stream));
+    st = check_contraction(xq, xs, qdata, srel, codebook, s_channel, bias, M, N, K, CR_OUT_BF16, dz, nullptr);
+    if (st != CR_OK)
+        return st;
+    const SwigluWork w(work, N, K);
+    st = check_work(work, work_bytes, w.bytes);
+    if (st != CR_OK)
+        return st;
+    DeviceState *d = nullptr;
+    st = current_device(&d);
+    if (st != CR_OK)
+        return st;
+    using namespace cr;
+    CUtensorMap tz, tx;
+    if (!make_tmap_out(&tz, dz, M, N, false) || !make_tmap_out(&tx, dx, M, K, false))
+        return CR_ERR_CUDA;
+    st = launched(ew::launch_decode(qdata, srel, codebook, N, K, w.w8, d->num_sms, stream));
+    if (st != CR_OK)
+        return st;
+    GemmEpilogue e;
+    e.xs = xs;
+    e.ws = s_channel;
+    e.bias = bias;
+    e.ex.dout = dout;
+    st = launch_gemm<gm::kSwigluGrad>(*d, xq, w.w8, &tz, M, N, K, e, stream);
+    if (st != CR_OK)
+        return st;
+    st = launched(ew::launch_dequant_t_bf16(qdata, srel, codebook, s_channel, (int)N, (int)K, (int)N, w.wt, d->num_sms,
+                                            stream));
+    if (st != CR_OK)
+        return st;
+    GemmEpilogue g;
+    g.out = dx;
+    return launch_gemm<gm::kBf16>(*d, dz, w.wt, &tx, M, K, N, g, stream);
+}
+
+int64_t cr_w4a8_cross_entropy_work_bytes(int64_t M, int64_t V, int64_t K)
+{
+    return good_shape(M, V, K) ? CeFwdWork(nullptr, M, V, K).bytes : 0;
+}
+
+cr_status cr_w4a8_cross_entropy(const int8_t *xq, const float *xs, const uint8_t *qdata, const uint8_t *srel,
+                                const float *codebook, const float *s_channel, const float *bias,
+                                const int64_t *targets, int64_t ignore_index, int64_t M, int64_t V, int64_t K,
+                                float *loss, float *lse, void *work, int64_t work_bytes, cr_stream_t stream)
+{
+    cr_status st = check_ce(xq, xs, qdata, srel, codebook, s_channel, bias, targets, M, V, K, loss, lse, lse);
+    if (st != CR_OK || M == 0)
+        return st;
+    const CeFwdWork w(work, M, V, K);
+    st = check_work(work, work_bytes, w.bytes);
+    if (st != CR_OK)
+        return st;
+    DeviceState *d = nullptr;
+    st = current_device(&d);
+    if (st != CR_OK)
+        return st;
+    using namespace cr;
+    if (M <= CR_GEMV_MAX_M) {
+        // a decode batch: the GEMV streams the packed codes; its outputs are small
+        st = run_gemv(d->num_sms, d->gemv_attr_set, xq, xs, qdata, srel, codebook, s_channel, bias, M, V, K,
+                      CR_OUT_F32, w.y, nullptr, stream, /*pdl=*/true, 0, &d->gemv32_attr_set);
+        if (st == CR_OK)
+            st = launched(ce::launch_stats(w.y, M, V, targets, w.part, w.tlogit, stream));
+        if (st == CR_OK)
+            st = launched(ce::launch_loss(w.part, w.slices, M, targets, ignore_index, V, w.tlogit, loss, lse, stream));
+        return st;
+    }
+    for (int64_t m0 = 0; m0 < M; m0 += w.rows) {
+        const int64_t rows = M - m0 < w.rows ? M - m0 : w.rows;
+        for (int64_t n0 = 0; n0 < V; n0 += w.piece) {
+            const int64_t n = V - n0 < w.piece ? V - n0 : w.piece;
+            st = launched(ew::launch_decode(qdata + n0 * (K / 2), srel + n0 * (K / 16), codebook, n, K, w.w8,
+                                            d->num_sms, stream));
+            if (st != CR_OK)
+                return st;
+            GemmEpilogue e;
+            e.xs = xs + m0;
+            e.ws = s_channel + n0;
+            e.bias = bias ? bias + n0 : nullptr;
+            e.ex.targets = targets + m0;
+            e.ex.ignore = ignore_index;
+            e.ex.V = V;
+            e.ex.n0 = (int)n0;
+            e.ex.part = w.part;
+            e.ex.tlogit = w.tlogit;
+            st = launch_gemm<gm::kCeStats>(*d, xq + m0 * K, w.w8, nullptr, rows, n, K, e, stream);
+            if (st != CR_OK)
+                return st;
+        }
+        st = launched(ce::launch_loss(w.part, w.slices, rows, targets + m0, ignore_index, V, w.tlogit, loss + m0,
+                                      lse + m0, stream));
+        if (st != CR_OK)
+            return st;
+    }
+    return CR_OK;
+}
+
+int64_t cr_w4a8_cross_entropy_backward_work_bytes(int64_t M, int64_t V, int64_t K)
+{
+    return good_shape(M, V, K) ? CeBwdWork(nullptr, M, V, K).bytes : 0;
+}
+
+cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, const uint8_t *qdata, const uint8_t *srel,
+                                         const float *codebook, const float *s_channel, const float *bias,
+                                         const int64_t *targets, int64_t ignore_index, const float *lse,
+                                         const float *dloss, int64_t M, int64_t V, int64_t K, uint16_t *dx, void *work,
+                                         int64_t work_bytes, cr_stream_t stream)
+{
+    cr_status st = check_ce(xq, xs, qdata, srel, codebook, s_channel, bias, targets, M, V, K, dx, lse, dloss);
+    if (st != CR_OK || M == 0)
+        return st;
+    const CeBwdWork w(work, M, V, K);
+    st = check_work(work, work_bytes, w.bytes);
+    if (st != CR_OK)
+        return st;
+    DeviceState *d = nullptr;
+    st = current_device(&d);
+    if (st != CR_OK)
+        return st;
+    using namespace cr;
+    for (int64_t m0 = 0; m0 < M; m0 += w.rows) {
+        const int64_t rows = M - m0 < w.rows ? M - m0 : w.rows;
+        for (int64_t n0 = 0; n0 < V; n0 += w.piece) {
+            const int64_t n = V - n0 < w.piece ? V - n0 : w.piece, np = round_up(n, 8);
+            const uint8_t *q = qdata + n0 * (K / 2), *s = srel + n0 * (K / 16);
+            st = launched(ew::launch_decode(q, s, codebook, n, K, w.w8, d->num_sms, stream));
+            if (st != CR_OK)
+                return st;
+            // dl [rows, np]: the gradient of the piece's outputs
+            CUtensorMap tl, tx;
+            if (!make_tmap_out(&tl, w.dl, rows, np, false) ||
+                !(w.acc ? make_tmap_out(&tx, w.acc, rows, K, true) : make_tmap_out(&tx, dx + m0 * K, rows, K, false)))
+                return CR_ERR_CUDA;
+            GemmEpilogue e;
+            e.xs = xs + m0;
+            e.ws = s_channel + n0;
+            e.bias = bias ? bias + n0 : nullptr;
+            e.ex.targets = targets + m0;
+            e.ex.ignore = ignore_index;
+            e.ex.V = V;
+            e.ex.n0 = (int)n0;
+            e.ex.lse = lse + m0;
+            e.ex.dloss = dloss + m0;
+            st = launch_gemm<gm::kCeGrad>(*d, xq + m0 * K, w.w8, &tl, rows, n, K, e, stream);
+            if (st != CR_OK)
+                return st;
+            st = launched(ew::launch_dequant_t_bf16(q, s, codebook, s_channel + n0, (int)n, (int)K, (int)np, w.wt,
+                                                    d->num_sms, stream));
+            if (st != CR_OK)
+                return st;
+            GemmEpilogue g;
+            g.out_f32 = w.acc != nullptr;
+            st = w.acc && n0 > 0 ? launch_gemm<gm::kBf16Add>(*d, w.dl, w.wt, &tx, rows, K, np, g, stream)
+                                 : launch_gemm<gm::kBf16>(*d, w.dl, w.wt, &tx, rows, K, np, g, stream);
+            if (st != CR_OK)
+                return st;
+        }
+        if (w.acc) {
+            st = launched(ce::launch_to_bf16(w.acc, rows * K, dx + m0 * K, d->num_sms, stream));
+            if (st != CR_OK)
+                return st;
+        }
+    }
+    return CR_OK;
 }
 
 namespace {

@@ -1,0 +1,142 @@
+// k_ce.cuh -- softmax cross entropy over the outputs of a W4A8 head: what
+// surrounds the contractions (k_gemm.cuh holds the epilogues that reduce a
+// tile of outputs, or turn it into its gradient, without storing it).
+//
+//   lse[m] = log sum_n e^y[m, n],   loss[m] = lse[m] - y[m, target[m]]
+//
+// A row's statistics come as pairs (reference in log2, sum of 2^(y log2 e -
+// reference)), one per column slice, [slices, M]; joining two pairs rescales
+// the smaller reference's sum.
+#pragma once
+
+#include "cr_device.cuh"
+#include "k_gemm.cuh"
+
+namespace cr {
+namespace ce {
+
+constexpr int kThreads = 256;
+constexpr int kSlice = 2048;  // columns per CTA of stats_kernel
+
+__device__ __forceinline__ void join(float2 &a, const float2 b)
+{
+    const float m = fmaxf(a.x, b.x);
+    const float base = m == __int_as_float(0xFF800000) ? 0.0f : m;
+    a.y = a.y * gm::ex2(a.x - base) + b.y * gm::ex2(b.x - base);
+    a.x = m;
+}
+
+// Statistics of stored fp32 outputs y [M, V] (a decode batch, whose outputs
+// the GEMV wrote), kSlice columns per CTA: grid (slices, M).
+__global__ void __launch_bounds__(kThreads) stats_kernel(const float *__restrict__ y, int64_t M, int64_t V,
+                                                         const int64_t *__restrict__ targets,
+                                                         float2 *__restrict__ part, float *__restrict__ tlogit)
+{
+    const float kNegInf = __int_as_float(0xFF800000);
+    __shared__ float2 sh[kThreads / 32];
+    const int64_t m = blockIdx.y, n0 = (int64_t)blockIdx.x * kSlice;
+    const float *row = y + m * V;
+    const int64_t t = targets[m];
+    float v[kSlice / kThreads];
+    float mx = kNegInf;
+#pragma unroll
+    for (int i = 0; i < kSlice / kThreads; ++i) {
+        const int64_t n = n0 + i * kThreads + threadIdx.x;
+        v[i] = n < V ? row[n] : kNegInf;
+        if (n == t && n < V)
+            tlogit[m] = v[i];
+        mx = fmaxf(mx, v[i]);
+    }
+    float2 a = make_float2(__fmul_rn(mx, gm::kLog2e), 0.0f);
+    const float base = a.x == kNegInf ? 0.0f : a.x;
+#pragma unroll
+    for (int i = 0; i < kSlice / kThreads; ++i)
+        a.y += gm::ex2(__fmaf_rn(v[i], gm::kLog2e, -base));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        join(a, make_float2(__shfl_xor_sync(0xFFFFFFFFu, a.x, o), __shfl_xor_sync(0xFFFFFFFFu, a.y, o)));
+    if ((threadIdx.x & 31) == 0)
+        sh[threadIdx.x >> 5] = a;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 1; w < kThreads / 32; ++w)
+            join(a, sh[w]);
+        part[(int64_t)blockIdx.x * M + m] = a;
+    }
+}
+
+// lse and loss of 32 rows per CTA from their statistics: a warp takes every
+// eighth slice of the rows (lane = row: whole sectors), then warp 0 joins the
+// eight in a fixed order.  The last steps are in fp64: a few operations per
+// row, and the loss is often a small difference of larger numbers.
+__global__ void __launch_bounds__(kThreads) loss_kernel(const float2 *__restrict__ part, int64_t slices, int64_t M,
+                                                        const int64_t *__restrict__ targets, int64_t ignore, int64_t V,
+                                                        const float *__restrict__ tlogit, float *__restrict__ loss,
+                                                        float *__restrict__ lse)
+{
+    __shared__ float2 sh[kThreads / 32][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t m = 32 * (int64_t)blockIdx.x + lane;
+    float2 a = make_float2(__int_as_float(0xFF800000), 0.0f);
+    if (m < M) {
+#pragma unroll 4
+        for (int64_t s = w; s < slices; s += kThreads / 32)
+            join(a, part[s * M + m]);
+    }
+    sh[w][lane] = a;
+    __syncthreads();
+    if (w == 0 && m < M) {
+#pragma unroll
+        for (int i = 1; i < kThreads / 32; ++i)
+            join(a, sh[i][lane]);
+        // the references are in units of the fp32 constant that made them
+        const double l = (double)a.x / (double)gm::kLog2e + log((double)a.y);
+        lse[m] = (float)l;
+        const int64_t t = targets[m];
+        float out = 0.0f;
+        if (t != ignore)
+            out = (t >= 0 && t < V) ? (float)(l - (double)tlogit[m]) : __int_as_float(0x7FC00000);
+        loss[m] = out;
+    }
+}
+
+// fp32 -> bf16, four elements per thread and step.
+__global__ void __launch_bounds__(kThreads) to_bf16_kernel(const float4 *__restrict__ src, int64_t n4,
+                                                           uint2 *__restrict__ dst)
+{
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n4; i += (int64_t)gridDim.x * kThreads) {
+        const float4 v = src[i];
+        dst[i] = make_uint2(to_bf16x2_bits(v.x, v.y), to_bf16x2_bits(v.z, v.w));
+    }
+}
+
+inline cudaError_t launch_stats(const float *y, int64_t M, int64_t V, const int64_t *targets, float2 *part,
+                                float *tlogit, cudaStream_t stream)
+{
+    stats_kernel<<<dim3((unsigned)((V + kSlice - 1) / kSlice), (unsigned)M), kThreads, 0, stream>>>(y, M, V, targets,
+                                                                                                    part, tlogit);
+    return cudaGetLastError();
+}
+
+inline cudaError_t launch_loss(const float2 *part, int64_t slices, int64_t M, const int64_t *targets, int64_t ignore,
+                               int64_t V, const float *tlogit, float *loss, float *lse, cudaStream_t stream)
+{
+    loss_kernel<<<(unsigned)((M + 31) / 32), kThreads, 0, stream>>>(part, slices, M, targets, ignore, V, tlogit, loss,
+                                                                    lse);
+    return cudaGetLastError();
+}
+
+inline cudaError_t launch_to_bf16(const float *src, int64_t n, uint16_t *dst, int num_sms, cudaStream_t stream)
+{
+    const int64_t n4 = n / 4;
+    int64_t grid = (n4 + kThreads - 1) / kThreads;
+    if (grid > 8 * (int64_t)num_sms)
+        grid = 8 * (int64_t)num_sms;
+    to_bf16_kernel<<<(unsigned)grid, kThreads, 0, stream>>>(reinterpret_cast<const float4 *>(src), n4,
+                                                            reinterpret_cast<uint2 *>(dst));
+    return cudaGetLastError();
+}
+
+}  // namespace ce
+}  // namespace cr

@@ -199,14 +199,15 @@ inline cudaError_t launch_interleave_rows(const void *src, void *dst, int64_t ro
 // the 16 bf16 pairs (row 2p, row 2p + 1) of those columns into a shared tile
 // of 4-byte pairs [128 k][36] (lanes on consecutive pairs: no bank
 // conflicts); the tile then leaves as 128 rows of 64 bf16 (16-byte stores, 8
-// lanes per 128-byte row).  N must be a multiple of 8 and K of 128.
+// lanes per 128-byte row).  wt has NP columns, NP a multiple of 8, N <= NP;
+// columns N .. NP - 1 are zeros.  K must be a multiple of 128.
 constexpr int kTN = 64, kTK = 128, kTPairs = 36;  // 32 row pairs + 4 of padding (16-byte aligned rows)
 
 __global__ void __launch_bounds__(kThreads) dequant_t_bf16_kernel(const uint8_t *__restrict__ qdata,
                                                                   const uint8_t *__restrict__ srel,
                                                                   const float *__restrict__ codebook,
                                                                   const float *__restrict__ s_channel, int N, int K,
-                                                                  uint16_t *__restrict__ wt)
+                                                                  int NP, uint16_t *__restrict__ wt)
 {
     __shared__ __align__(16) uint32_t tile[kTK][kTPairs];
     __shared__ uint4 lut[256];
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) dequant_t_bf16_kernel(const uint8_t 
     __syncthreads();
     lut[threadIdx.x] = lut_entry(threadIdx.x, cb);  // kThreads == 256 scale bytes
     __syncthreads();
-    const int tiles_k = K / kTK, tiles_n = (N + kTN - 1) / kTN;
+    const int tiles_k = K / kTK, tiles_n = (NP + kTN - 1) / kTN;
     const int p = threadIdx.x & 31, g = threadIdx.x >> 5;
     // n fastest: CTAs running together write neighbouring 128-byte strips of
     // the same 128 rows of wt (whole rows between them), not one strip each
@@ -224,15 +225,20 @@ __global__ void __launch_bounds__(kThreads) dequant_t_bf16_kernel(const uint8_t 
     for (int t = blockIdx.x; t < tiles_k * tiles_n; t += gridDim.x) {
         const int tk = t / tiles_n, tn = t - tk * tiles_n;
         const int n0 = tn * kTN, k0 = tk * kTK, n = n0 + 2 * p;
-        if (n < N) {  // N % 8 == 0: both rows of the pair exist
+        if (n < NP) {
             const int kg = k0 / 16 + g;  // this thread's group
             uint32_t lo[4], hi[4];
             float sch[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
+                uint32_t *w = r ? hi : lo;
+                if (n + r >= N) {
+                    w[0] = w[1] = w[2] = w[3] = 0u;
+                    sch[r] = 0.0f;
+                    continue;
+                }
                 const uint2 c = *reinterpret_cast<const uint2 *>(qdata + (int64_t)(n + r) * (K / 2) + 8 * kg);
                 const uint4 T = lut[srel[(int64_t)(n + r) * (K / 16) + kg]];
-                uint32_t *w = r ? hi : lo;
                 decode8(c.x, T, w[0], w[1]);
                 decode8(c.y, T, w[2], w[3]);
                 sch[r] = __bfloat162float(__float2bfloat16_rn(s_channel[n + r]));
@@ -255,8 +261,8 @@ __global__ void __launch_bounds__(kThreads) dequant_t_bf16_kernel(const uint8_t 
         __syncthreads();
         for (int i = threadIdx.x; i < kTK * (kTN / 8); i += kThreads) {
             const int kr = i >> 3, ch = i & 7, nn = n0 + 8 * ch;
-            if (nn < N)  // N % 8 == 0: a 16-byte chunk is wholly inside or outside
-                *reinterpret_cast<uint4 *>(wt + (int64_t)(k0 + kr) * N + nn) =
+            if (nn < NP)  // NP % 8 == 0: a 16-byte chunk is wholly inside or outside
+                *reinterpret_cast<uint4 *>(wt + (int64_t)(k0 + kr) * NP + nn) =
                     *reinterpret_cast<const uint4 *>(&tile[kr][4 * ch]);
         }
         __syncthreads();
@@ -264,13 +270,14 @@ __global__ void __launch_bounds__(kThreads) dequant_t_bf16_kernel(const uint8_t 
 }
 
 inline cudaError_t launch_dequant_t_bf16(const uint8_t *qdata, const uint8_t *srel, const float *codebook,
-                                         const float *s_channel, int N, int K, uint16_t *wt, int num_sms,
+                                         const float *s_channel, int N, int K, int NP, uint16_t *wt, int num_sms,
                                          cudaStream_t stream)
 {
-    const int64_t tiles = (int64_t)(K / kTK) * ((N + kTN - 1) / kTN);
+    const int64_t tiles = (int64_t)(K / kTK) * ((NP + kTN - 1) / kTN);
     const int64_t cap = (int64_t)num_sms * 8;
     const int grid = (int)(tiles < cap ? tiles : cap);
-    dequant_t_bf16_kernel<<<grid < 1 ? 1 : grid, kThreads, 0, stream>>>(qdata, srel, codebook, s_channel, N, K, wt);
+    dequant_t_bf16_kernel<<<grid < 1 ? 1 : grid, kThreads, 0, stream>>>(qdata, srel, codebook, s_channel, N, K, NP,
+                                                                        wt);
     return cudaGetLastError();
 }
 

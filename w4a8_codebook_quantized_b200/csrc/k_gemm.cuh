@@ -31,6 +31,29 @@
 namespace cr {
 namespace gm {
 
+// What a GEMM's operands are and what its epilogue does with the accumulators.
+enum Mode : int {
+    kI8 = 0,         // int8; the layer's outputs (with SwiGLU when asked)
+    kBf16 = 1,       // bf16 x bf16 -> fp32; the accumulators are the outputs
+    kBf16Add = 2,    // the same, added to the fp32 outputs already there
+    kSwigluGrad = 3, // int8; the gradient of interleaved gate/up outputs
+    kCeStats = 4,    // int8; softmax statistics of the outputs
+    kCeGrad = 5      // int8; the cross entropy's gradient of the outputs
+};
+
+constexpr bool is_bf16(int mode) { return mode == kBf16 || mode == kBf16Add; }
+
+// What the epilogues beyond the layer's own read and write.
+struct EpiArgs {
+    const uint16_t *dout = nullptr;    // kSwigluGrad: [M, N / 2] bf16
+    const int64_t *targets = nullptr;  // kCe*: [M]
+    int64_t ignore = 0, V = 0;         // kCe*: the target that has no loss; the whole vocabulary
+    int n0 = 0;                        // kCe*: the vocabulary entry of column 0
+    float2 *part = nullptr;            // kCeStats: [tiles, M] (reference in log2, sum)
+    float *tlogit = nullptr;           // kCeStats: [M], the target's output
+    const float *lse = nullptr, *dloss = nullptr;  // kCeGrad: [M]
+};
+
 constexpr int BM = 128, BN = 256, BK = 128;  // BK in int8 elements = bytes
 constexpr int kStages = 4;
 constexpr int kABytes = BM * BK;              // 16 KB
@@ -63,6 +86,33 @@ __device__ __forceinline__ void tile_coords(int tile, int tiles_n, int &tm, int 
     tn = tile - tm * tiles_n;
 }
 
+// One 128-byte unit (32 words a lane) of a warp's 32 rows -> staging buffer ->
+// TMA bulk store (ADD: bulk reduction, fp32 addition in memory).
+template <bool ADD>
+__device__ __forceinline__ void store_unit_rows(const uint32_t (&p)[32], int ucol0, int row0, int lane,
+                                                const CUtensorMap *tmOut, uint8_t *stg, uint32_t &units_issued)
+{
+    if (units_issued >= 1) {
+        if (lane == 0)
+            bulk_wait_read<0>();  // the previous store has read the staging buffer
+        __syncwarp();
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4 *>(stg + lane * 128 + ((c ^ (lane & 7)) * 16)) =
+            make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if constexpr (ADD)
+            tma_add_2d(tmOut, ucol0, row0, stg);
+        else
+            tma_store_2d(tmOut, ucol0, row0, stg);
+        bulk_commit();
+    }
+    ++units_issued;
+}
+
 // Epilogue of one 128 x 256 accumulator tile for one warp: its 32 TMEM lanes
 // are rows row0 + lane; `tbase` addresses lane 0 of the warp's quarter at the
 // tile's first column; the output columns are col_base + [0, 256).  Fast path
@@ -73,8 +123,9 @@ __device__ __forceinline__ void tile_coords(int tile, int tiles_n, int &tm, int 
 // thread stores its own row.  release() hands the accumulator back once every
 // column is in registers.
 // RAW: the accumulator holds fp32 values that are the outputs themselves
-// (bf16 GEMM); no scales, bias or SwiGLU.
-template <bool RAW, class Release>
+// (bf16 GEMM); no scales, bias or SwiGLU.  ADD: the fp32 outputs are added to
+// what is there, by the bulk stores' own reduction (tma_out only).
+template <bool RAW, bool ADD, class Release>
 __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_base, int lane, float xm, bool row_ok,
                                               const float *wsv, const float *bsv, bool has_bias, int M, int N,
                                               int out_f32, int swiglu, int tma_out, const CUtensorMap *tmOut,
@@ -115,25 +166,8 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_
             }
         }
     };
-    // one 128-byte unit of the warp's 32 rows -> staging buffer -> TMA bulk store
     auto store_unit = [&](const uint32_t (&p)[32], int ucol0) {
-        if (units_issued >= 1) {
-            if (lane == 0)
-                bulk_wait_read<0>();  // the previous store has read the staging buffer
-            __syncwarp();
-        }
-        uint8_t *stg = stage_buf;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4 *>(stg + lane * 128 + ((c ^ (lane & 7)) * 16)) =
-                make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_2d(tmOut, ucol0, row0, stg);
-            bulk_commit();
-        }
-        ++units_issued;
+        store_unit_rows<ADD>(p, ucol0, row0, lane, tmOut, stage_buf, units_issued);
     };
     uint32_t cur[32], nxt[32], packed[32];
     if (!RAW && swiglu) {
@@ -287,16 +321,262 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_
     }
 }
 
-// BF16: A and B are bf16 (K counted in bf16 elements, 64 per 128-byte
+// The 32 fp32 outputs of accumulator columns [c0, c0 + 32) of one row, as the
+// layer's epilogue computes them (wsv, bsv: the tile's channel scales and bias).
+__device__ __forceinline__ void outputs32(const uint32_t (&v)[32], int c0, float xm, const float *wsv,
+                                          const float *bsv, bool has_bias, float (&y)[32])
+{
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        const float4 w4 = *reinterpret_cast<const float4 *>(wsv + c0 + j);
+        const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            y[j + e] = __fmul_rn(__int2float_rn((int32_t)v[j + e]), __fmul_rn(xm, wv[e]));
+        if (has_bias) {
+            const float4 b4 = *reinterpret_cast<const float4 *>(bsv + c0 + j);
+            const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[j + e] = __fadd_rn(y[j + e], bv[e]);
+        }
+    }
+}
+
+// Gradient of silu(g) * u with respect to g and u, for the gradient d of the
+// product: with s = sigmoid(g), du = d g s and dg = d u s (1 + g (1 - s)).
+// t = e^-|g| lies in (0, 1], so the divisor of the fast division lies in
+// [1, 2] (at most 2 ulp), as in swiglu_value.
+__device__ __forceinline__ uint32_t swiglu_grad(float g, float u, float d)
+{
+    const float t = expf(-fabsf(g));
+    const float r = __fdividef(1.0f, 1.0f + t), q = t * r;
+    const float s = g >= 0.0f ? r : q, os = g >= 0.0f ? q : r;  // sigmoid and 1 - sigmoid
+    const float ds = d * s;
+    return to_bf16x2_bits(ds * u * (1.0f + g * os), ds * g);
+}
+
+// Sixteen bf16 of a row of dout as eight words, columns [f0, f0 + 16) of
+// [M, F]: F % 4 == 0, so 8-byte loads are aligned and a group of four columns
+// lies inside the row or past it.
+__device__ __forceinline__ void load_dout16(const uint16_t *drow, int f0, int F, bool row_ok, uint32_t (&d)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint2 w = make_uint2(0u, 0u);
+        if (row_ok && f0 + 4 * i < F)
+            w = __ldg(reinterpret_cast<const uint2 *>(drow + f0 + 4 * i));
+        d[2 * i] = w.x;
+        d[2 * i + 1] = w.y;
+    }
+}
+
+// Epilogue of kSwigluGrad for one warp's 32 rows of a tile: accumulator
+// columns 2f and 2f + 1 are gate and up of output column f; their gradients
+// leave as the same two columns of dz [M, N] bf16.  Each row's 16 values of
+// dout for the next 32 columns are loaded while the current ones are used.
+template <class Release>
+__device__ __forceinline__ void epilogue_swiglu_grad(uint32_t tbase, int row0, int col_base, int lane, float xm,
+                                                     bool row_ok, const float *wsv, const float *bsv, bool has_bias,
+                                                     int N, const EpiArgs &ex, const CUtensorMap *tmOut,
+                                                     uint8_t *stage_buf, uint32_t &units_issued, Release release)
+{
+    const int F = N >> 1, f_base = col_base >> 1;
+    const uint16_t *drow = ex.dout + (int64_t)(row0 + lane) * F;
+    uint32_t dn[8], cur[32], packed[32];
+    load_dout16(drow, f_base, F, row_ok, dn);
+    for (int un = 0; un < BN / 64; ++un) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c0 = 64 * un + 32 * k;
+            __syncwarp();
+            tmem_ld_32cols(tbase + (uint32_t)c0, cur);
+            uint32_t d[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                d[i] = dn[i];
+            if (c0 + 32 < BN)
+                load_dout16(drow, f_base + (c0 + 32) / 2, F, row_ok, dn);
+            tmem_ld_wait();
+            if (c0 + 32 == BN)
+                release();
+            float y[32];
+            outputs32(cur, c0, xm, wsv, bsv, has_bias, y);
+#pragma unroll
+            for (int p = 0; p < 16; ++p) {
+                const float dv = __uint_as_float((p & 1) ? d[p >> 1] & 0xFFFF0000u : d[p >> 1] << 16);
+                packed[16 * k + p] = swiglu_grad(y[2 * p], y[2 * p + 1], dv);
+            }
+        }
+        if (col_base + 64 * un < N)
+            store_unit_rows<false>(packed, col_base + 64 * un, row0, lane, tmOut, stage_buf, units_issued);
+    }
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x by the special-function unit (2 ulp; 0 for x = -inf, inf for +inf).
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Epilogue of kCeStats for one warp's 32 rows: each row's sum of exponentials
+// over the tile's (at most 256) columns, relative to its maximum there.  The
+// reference is kept in the base-2 domain as the rounded product max * log2(e),
+// and every term is 2^(fma(y, log2 e, -reference)), so the pair (reference,
+// sum) carries no error of the reference's rounding.  Columns past N are left
+// out; -inf outputs (a bias that masks a vocabulary entry) contribute 0, also
+// where a whole tile has nothing else.
+template <class Release>
+__device__ __forceinline__ void epilogue_ce_stats(uint32_t tbase, int row, int tile_n, int lane, float xm, bool row_ok,
+                                                  const float *wsv, const float *bsv, bool has_bias, int M, int N,
+                                                  const EpiArgs &ex, Release release)
+{
+    const float kNegInf = __int_as_float(0xFF800000);
+    const int col_base = tile_n * BN;
+    const int64_t t = row_ok ? ex.targets[row] : -1, lo = (int64_t)ex.n0 + col_base;
+    const int tcol = (t >= lo && t < lo + BN && t - ex.n0 < N) ? (int)(t - lo) : -1;  // the target in this tile
+    float ref = kNegInf, s0 = 0.0f, s1 = 0.0f, tl = 0.0f;
+    for (int ch = 0; ch < BN / 32; ++ch) {
+        uint32_t cur[32];
+        __syncwarp();
+        tmem_ld_32cols(tbase + (uint32_t)(32 * ch), cur);
+        tmem_ld_wait();
+        if (ch + 1 == BN / 32)
+            release();
+        float y[32];
+        outputs32(cur, 32 * ch, xm, wsv, bsv, has_bias, y);
+        if (col_base + 32 * ch + 32 > N) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (col_base + 32 * ch + j >= N)
+                    y[j] = kNegInf;
+        }
+        if ((tcol >> 5) == ch) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if ((tcol & 31) == j)
+                    tl = y[j];
+        }
+        float m0 = y[0], m1 = y[1];
+#pragma unroll
+        for (int j = 2; j < 32; j += 2) {
+            m0 = fmaxf(m0, y[j]);
+            m1 = fmaxf(m1, y[j + 1]);
+        }
+        const float next = fmaxf(ref, __fmul_rn(fmaxf(m0, m1), kLog2e));
+        const float base = next == kNegInf ? 0.0f : next;
+        const float scale = ex2(ref - base);  // 0 at the first chunk
+        s0 *= scale;
+        s1 *= scale;
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            s0 += ex2(__fmaf_rn(y[j], kLog2e, -base));
+            s1 += ex2(__fmaf_rn(y[j + 1], kLog2e, -base));
+        }
+        ref = next;
+    }
+    if (row_ok) {
+        ex.part[(int64_t)(ex.n0 / BN + tile_n) * M + row] = make_float2(ref, s0 + s1);
+        if (tcol >= 0)
+            ex.tlogit[row] = tl;
+    }
+}
+
+// Epilogue of kCeGrad: dl[m, n] = dloss[m] * (e^(y - lse[m]) - [n = target]),
+// zero for ignored rows, to bf16; columns from N to the buffer's width (a
+// multiple of 8) are written as zeros.  A target outside the vocabulary makes
+// its row NaN.
+template <class Release>
+__device__ __forceinline__ void epilogue_ce_grad(uint32_t tbase, int row0, int col_base, int lane, float xm,
+                                                 bool row_ok, const float *wsv, const float *bsv, bool has_bias,
+                                                 int N, const EpiArgs &ex, const CUtensorMap *tmOut,
+                                                 uint8_t *stage_buf, uint32_t &units_issued, Release release)
+{
+    const int row = row0 + lane;
+    float scale = 0.0f, lse2 = __int_as_float(0x7F800000);  // an ignored row: every exponential 0
+    int tcol = -1;
+    if (row_ok) {
+        const int64_t t = ex.targets[row];
+        if (t != ex.ignore) {
+            lse2 = __fmul_rn(ex.lse[row], kLog2e);
+            scale = (t >= 0 && t < ex.V) ? ex.dloss[row] : __int_as_float(0x7FC00000);
+            const int64_t lo = (int64_t)ex.n0 + col_base;
+            tcol = (t >= lo && t < lo + BN) ? (int)(t - lo) : -1;
+        }
+    }
+    uint32_t cur[32], packed[32];
+    for (int un = 0; un < BN / 64; ++un) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c0 = 64 * un + 32 * k;
+            __syncwarp();
+            tmem_ld_32cols(tbase + (uint32_t)c0, cur);
+            tmem_ld_wait();
+            if (c0 + 32 == BN)
+                release();
+            float y[32];
+            outputs32(cur, c0, xm, wsv, bsv, has_bias, y);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                y[j] = ex2(__fmaf_rn(y[j], kLog2e, -lse2));
+            if ((tcol >> 5) == (c0 >> 5)) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if ((tcol & 31) == j)
+                        y[j] -= 1.0f;
+            }
+            if (col_base + c0 + 32 > N) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (col_base + c0 + j >= N)
+                        y[j] = 0.0f;
+            }
+#pragma unroll
+            for (int p = 0; p < 16; ++p)
+                packed[16 * k + p] = to_bf16x2_bits(y[2 * p] * scale, y[2 * p + 1] * scale);
+        }
+        if (col_base + 64 * un < N)
+            store_unit_rows<false>(packed, col_base + 64 * un, row0, lane, tmOut, stage_buf, units_issued);
+    }
+}
+
+// The tile's epilogue for one warp, by mode.
+template <int MODE, class Release>
+__device__ __forceinline__ void epilogue_any(uint32_t tbase, int row0, int tile_n, int lane, float xm, bool row_ok,
+                                             const float *wsv, const float *bsv, bool has_bias, int M, int N,
+                                             int out_f32, int swiglu, int tma_out, const CUtensorMap *tmOut,
+                                             uint8_t *stage_buf, uint32_t &units_issued, void *out, int32_t *acc_out,
+                                             const float *ws, const float *bias, const EpiArgs &ex, Release release)
+{
+    if constexpr (MODE == kSwigluGrad)
+        epilogue_swiglu_grad(tbase, row0, tile_n * BN, lane, xm, row_ok, wsv, bsv, has_bias, N, ex, tmOut, stage_buf,
+                             units_issued, release);
+    else if constexpr (MODE == kCeStats)
+        epilogue_ce_stats(tbase, row0 + lane, tile_n, lane, xm, row_ok, wsv, bsv, has_bias, M, N, ex, release);
+    else if constexpr (MODE == kCeGrad)
+        epilogue_ce_grad(tbase, row0, tile_n * BN, lane, xm, row_ok, wsv, bsv, has_bias, N, ex, tmOut, stage_buf,
+                         units_issued, release);
+    else
+        epilogue_tile<is_bf16(MODE), MODE == kBf16Add>(tbase, row0, tile_n * BN, lane, xm, row_ok, wsv, bsv, has_bias,
+                                                       M, N, out_f32, swiglu, tma_out, tmOut, stage_buf, units_issued,
+                                                       out, acc_out, ws, bias, release);
+}
+
+// BF16 modes: A and B are bf16 (K counted in bf16 elements, 64 per 128-byte
 // stage row), tcgen05.mma kind::f16 into fp32, and the epilogue writes the
 // accumulators as they are (xs, ws, bias, swiglu and acc_out unused).
-template <bool BF16>
+template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmOut, const float *__restrict__ xs,
                 const float *__restrict__ ws, const float *__restrict__ bias, int M, int N, int K, int out_f32,
-                int swiglu, int tma_out, void *__restrict__ out, int32_t *__restrict__ acc_out)
+                int swiglu, int tma_out, void *__restrict__ out, int32_t *__restrict__ acc_out, const EpiArgs ex)
 {
+    constexpr bool BF16 = is_bf16(MODE);
     extern __shared__ uint8_t smem_raw[];
     Smem &sh = smem_aligned_1024<Smem>(smem_raw);
 
@@ -451,9 +731,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool row_ok = row < M;
             const float xm = (!BF16 && row_ok) ? xs[row] : 0.0f;
             const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * BN);
-            epilogue_tile<BF16>(tbase, tm * BM + 32 * q, tn * BN, lane, xm, row_ok, sh.wsb[buf], sh.biasb[buf],
+            epilogue_any<MODE>(tbase, tm * BM + 32 * q, tn, lane, xm, row_ok, sh.wsb[buf], sh.biasb[buf],
                           bias != nullptr, M, N, out_f32, swiglu, tma_out, &tmOut, sh.epi[q], units_issued, out, acc_out, ws,
-                          bias, [&]() {
+                          bias, ex, [&]() {
                               tc_fence_before();
                               __syncwarp();
                               if (lane == 0)
@@ -507,13 +787,14 @@ constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 }  // namespace pair
 
 // BF16 as for gemm_kernel.
-template <bool BF16>
+template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmOut, const float *__restrict__ xs,
                      const float *__restrict__ ws, const float *__restrict__ bias, int M, int N, int K, int out_f32,
-                     int swiglu, int tma_out, void *__restrict__ out, int32_t *__restrict__ acc_out)
+                     int swiglu, int tma_out, void *__restrict__ out, int32_t *__restrict__ acc_out, const EpiArgs ex)
 {
+    constexpr bool BF16 = is_bf16(MODE);
     extern __shared__ uint8_t smem_raw[];
     pair::Smem &sh = smem_aligned_1024<pair::Smem>(smem_raw);
 
@@ -678,8 +959,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float xm = (!BF16 && row_ok) ? xs[row0 + lane] : 0.0f;
             const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * BN);
             const uint32_t release_addr = mapa_shared(smem_u32(&sh.tmem_empty[buf]), 0);
-            epilogue_tile<BF16>(tbase, row0, tn * BN, lane, xm, row_ok, sh.wsb[buf], sh.biasb[buf], bias != nullptr, M,
-                          N, out_f32, swiglu, tma_out, &tmOut, sh.epi[q], units_issued, out, acc_out, ws, bias, [&]() {
+            epilogue_any<MODE>(tbase, row0, tn, lane, xm, row_ok, sh.wsb[buf], sh.biasb[buf], bias != nullptr, M,
+                          N, out_f32, swiglu, tma_out, &tmOut, sh.epi[q], units_issued, out, acc_out, ws, bias, ex, [&]() {
                               tc_fence_before();
                               __syncwarp();
                               if (lane == 0)
