@@ -657,9 +657,9 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
  * is allocated.
  *
  * (23b) Its gradient with respect to the layer's rotated input:
- *   dl[m, n] = bf16( dloss[m] * (e^(y[m, n] - lse[m]) - [n == targets[m]]) ),
+ *   dl[m, n] = bf16( e^(y[m, n] - lse[m]) - [n == targets[m]] )
+ *   dx[m, k] = bf16( dloss[m] * sum_n dl[m, n] * w[n, k] )   (w as in (13); the sum in fp32);
  *              0 in ignored rows, NaN in rows with an invalid target
- *   dx[m, k] = bf16( sum_n dl[m, n] * w[n, k] )   (w as in (13); the sum in fp32)
  * lse from (23) on the same arguments; dloss [M] fp32, the gradient of loss
  * (1 / count for the mean over count rows).  dx [M, K] bf16, written: (20) or
  * (21) take it back.  work: at least

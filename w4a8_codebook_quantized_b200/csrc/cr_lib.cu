@@ -37,8 +37,8 @@ struct DeviceState {
     cudaMemPool_t pool = nullptr;  // stream-ordered pool for the weight transients (release threshold 0)
     // kernel attributes set once (cudaFuncSetAttribute is idempotent; atomic
     // flags so that concurrent first calls do not race on the flag itself)
-    std::atomic<bool> gemm_attr_set[6] = {};       // by gm::Mode
-    std::atomic<bool> gemm_pair_attr_set[6] = {};
+    std::atomic<bool> gemm_attr_set[cr::gm::kModes] = {};  // by gm::Mode
+    std::atomic<bool> gemm_pair_attr_set[cr::gm::kModes] = {};
     std::atomic<bool> gemv_attr_set{false};
     std::atomic<bool> gemv_split_attr_set{false};
     std::atomic<bool> gemv32_attr_set{false};
@@ -488,7 +488,8 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
         return true;
     };
     const int64_t pair_tiles = ((M + 255) / 256) * ((N + gm::BN - 1) / gm::BN);
-    const bool use_pair = pair_tiles >= d.num_sms / 2;
+    const int splits = gm::is_bf16(MODE) ? e.ex.splits : 1;
+    const bool use_pair = splits > 1 ? M > gm::BM : pair_tiles >= d.num_sms / 2;
     CUtensorMap ta, tb;
     if (!map(&ta, A, M, (uint32_t)gm::BM) || !map(&tb, B, N, use_pair ? 128u : (uint32_t)gm::BN))
         return CR_ERR_CUDA;
@@ -496,10 +497,11 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
     if (use_pair) {
         if (!opt_in(d.gemm_pair_attr_set[MODE], (const void *)gm::gemm_pair_kernel<MODE>, gm::pair::kSmemBytes))
             return CR_ERR_CUDA;
-        const int64_t pairs = pair_tiles < d.num_sms / 2 ? pair_tiles : d.num_sms / 2;
+        const int64_t units = pair_tiles * splits;
+        const int64_t pairs = units < d.num_sms / 2 ? units : d.num_sms / 2;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(2 * pairs));
-        cfg.blockDim = dim3(gm::kThreads);
+        cfg.blockDim = dim3(gm::threads(MODE));
         cfg.dynamicSmemBytes = gm::pair::kSmemBytes;
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];
@@ -514,24 +516,26 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
     }
     if (!opt_in(d.gemm_attr_set[MODE], (const void *)gm::gemm_kernel<MODE>, gm::kSmemBytes))
         return CR_ERR_CUDA;
-    const int64_t tiles = ((M + gm::BM - 1) / gm::BM) * ((N + gm::BN - 1) / gm::BN);
+    const int64_t tiles = ((M + gm::BM - 1) / gm::BM) * ((N + gm::BN - 1) / gm::BN) * splits;
     const int grid = (int)(tiles < d.num_sms ? tiles : d.num_sms);
-    gm::gemm_kernel<MODE><<<grid, gm::kThreads, gm::kSmemBytes, stream>>>(ta, tb, tm_out, e.xs, e.ws, e.bias, (int)M,
+    gm::gemm_kernel<MODE><<<grid, gm::threads(MODE), gm::kSmemBytes, stream>>>(ta, tb, tm_out, e.xs, e.ws, e.bias, (int)M,
                                                                          (int)N, (int)K, e.out_f32, e.swiglu, e.tma_out,
                                                                          e.out, e.acc_out, e.ex);
     return launched(cudaGetLastError());
 }
 
 // The tensor map of a row-major output [M, cols] leaving in boxes of 32 rows x
-// 128 bytes, 128-byte swizzle; rows must be multiples of 16 bytes.
-bool make_tmap_out(CUtensorMap *to, void *out, int64_t M, int64_t cols, bool f32)
+// 128 bytes, 128-byte swizzle (half: 64 bytes, 64-byte swizzle, as the
+// eight-warp epilogues store); rows must be multiples of 16 bytes.
+bool make_tmap_out(CUtensorMap *to, void *out, int64_t M, int64_t cols, bool f32, bool half = false)
 {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)M};
     const cuuint64_t strides[1] = {(cuuint64_t)cols * (f32 ? 4u : 2u)};
-    const cuuint32_t box[2] = {f32 ? 32u : 64u, 32u};
+    const cuuint32_t box[2] = {(f32 ? 32u : 64u) / (half ? 2u : 1u), 32u};
     const cuuint32_t estr[2] = {1u, 1u};
     return g_encode_tiled(to, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims,
-                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          half ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1240,15 +1244,39 @@ struct Parts {
     }
 };
 
+// How a bf16 contraction [M, K] over `red` terms is spread over the SMs when
+// it has too few tiles to fill them: the reduction in `n` ranges, each with its
+// own fp32 copy of the outputs (`rows` rows, so that no tile's store reaches the
+// next copy), added up afterwards in a fixed order.  One SM pair works a 256 x
+// 256 tile, one SM a 128 x 256 tile when M <= 128; a range keeps at least 8
+// blocks of 64 terms.  148 SMs: the caller's buffers may not depend on more
+// than the shape.
+struct SplitPlan {
+    int n = 1;
+    int64_t rows = 0;
+    SplitPlan(int64_t M, int64_t K, int64_t red)
+    {
+        const int64_t bm = M <= cr::gm::BM ? cr::gm::BM : 2 * cr::gm::BM, slots = M <= cr::gm::BM ? 148 : 74;
+        const int64_t tiles = (M + bm - 1) / bm * ((K + cr::gm::BN - 1) / cr::gm::BN), blocks = (red + 63) / 64;
+        int64_t s = slots / tiles < blocks / 8 ? slots / tiles : blocks / 8;
+        if (s > 1)
+            n = (int)(s < 32 ? s : 32);
+        rows = n > 1 ? round_up(M, bm) : M;
+    }
+};
+
 struct SwigluWork {
     int8_t *w8;
     uint16_t *wt;
+    float *acc;  // the split reduction's copies (null: not split)
+    SplitPlan split;
     int64_t bytes;
-    SwigluWork(void *work, int64_t N, int64_t K)
+    SwigluWork(void *work, int64_t M, int64_t N, int64_t K) : split(M, K, N)
     {
         Parts p(work);
         w8 = static_cast<int8_t *>(p.take(N * K));
         wt = static_cast<uint16_t *>(p.take(2 * N * K));
+        acc = split.n > 1 ? static_cast<float *>(p.take(4 * split.n * split.rows * K)) : nullptr;
         bytes = p.used;
     }
 };
@@ -1301,18 +1329,19 @@ struct CeBwdWork {
     int64_t rows, piece;
     int8_t *w8;
     uint16_t *wt, *dl;
-    float *acc;  // fp32 sum over the pieces (null: one piece)
+    float *acc;  // fp32 sums over the pieces, per range of a split reduction (null: one piece, not split)
+    SplitPlan split;
     int64_t bytes;
     CeBwdWork(void *work, int64_t M, int64_t V, int64_t K)
+        : rows(M < kBwdRows ? M : kBwdRows), piece(ce_piece(V, rows > K ? rows : K)),
+          split(rows, K, piece < V ? piece : V)
     {
         Parts p(work);
-        rows = M < kBwdRows ? M : kBwdRows;
-        piece = ce_piece(V, rows > K ? rows : K);
         const int64_t most = piece < V ? piece : round_up(V, 8);
         w8 = static_cast<int8_t *>(p.take(most * K));
         wt = static_cast<uint16_t *>(p.take(2 * most * K));
         dl = static_cast<uint16_t *>(p.take(2 * most * rows));
-        acc = piece < V ? static_cast<float *>(p.take(4 * rows * K)) : nullptr;
+        acc = piece < V || split.n > 1 ? static_cast<float *>(p.take(4 * split.n * split.rows * K)) : nullptr;
         bytes = p.used;
     }
 };
@@ -1351,7 +1380,7 @@ cr_status check_work(const void *work, int64_t have, int64_t need)
 
 int64_t cr_w4a8_swiglu_backward_work_bytes(int64_t M, int64_t N, int64_t K)
 {
-    return good_shape(M, N, K) ? SwigluWork(nullptr, N, K).bytes : 0;
+    return good_shape(M, N, K) ? SwigluWork(nullptr, M, N, K).bytes : 0;
 }
 
 cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const float *xs, const uint8_t *qdata,
@@ -1373,7 +1402,7 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
     st = check_contraction(xq, xs, qdata, srel, codebook, s_channel, bias, M, N, K, CR_OUT_BF16, dz, nullptr);
     if (st != CR_OK)
         return st;
-    const SwigluWork w(work, N, K);
+    const SwigluWork w(work, M, N, K);
     st = check_work(work, work_bytes, w.bytes);
     if (st != CR_OK)
         return st;
@@ -1383,7 +1412,8 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
         return st;
     using namespace cr;
     CUtensorMap tz, tx;
-    if (!make_tmap_out(&tz, dz, M, N, false) || !make_tmap_out(&tx, dx, M, K, false))
+    if (!make_tmap_out(&tz, dz, M, N, false, /*half=*/true) ||
+        !(w.acc ? make_tmap_out(&tx, w.acc, w.split.n * w.split.rows, K, true) : make_tmap_out(&tx, dx, M, K, false)))
         return CR_ERR_CUDA;
     st = launched(ew::launch_decode(qdata, srel, codebook, N, K, w.w8, d->num_sms, stream));
     if (st != CR_OK)
@@ -1401,8 +1431,13 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
     if (st != CR_OK)
         return st;
     GemmEpilogue g;
-    g.out = dx;
-    return launch_gemm<gm::kBf16>(*d, dz, w.wt, &tx, M, K, N, g, stream);
+    g.out_f32 = w.acc != nullptr;
+    g.ex.splits = w.split.n;
+    g.ex.split_rows = (int)w.split.rows;
+    st = launch_gemm<gm::kBf16>(*d, dz, w.wt, &tx, M, K, N, g, stream);
+    if (st == CR_OK && w.acc)
+        st = launched(ce::launch_sum_to_bf16(w.acc, w.split.n, w.split.rows, M, K, dx, d->num_sms, stream));
+    return st;
 }
 
 int64_t cr_w4a8_cross_entropy_work_bytes(int64_t M, int64_t V, int64_t K)
@@ -1454,6 +1489,7 @@ cr_status cr_w4a8_cross_entropy(const int8_t *xq, const float *xs, const uint8_t
             e.ex.V = V;
             e.ex.n0 = (int)n0;
             e.ex.part = w.part;
+            e.ex.slices = (int)w.slices;
             e.ex.tlogit = w.tlogit;
             st = launch_gemm<gm::kCeStats>(*d, xq + m0 * K, w.w8, nullptr, rows, n, K, e, stream);
             if (st != CR_OK)
@@ -1500,8 +1536,9 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
                 return st;
             // dl [rows, np]: the gradient of the piece's outputs
             CUtensorMap tl, tx;
-            if (!make_tmap_out(&tl, w.dl, rows, np, false) ||
-                !(w.acc ? make_tmap_out(&tx, w.acc, rows, K, true) : make_tmap_out(&tx, dx + m0 * K, rows, K, false)))
+            if (!make_tmap_out(&tl, w.dl, rows, np, false, /*half=*/true) ||
+                !(w.acc ? make_tmap_out(&tx, w.acc, w.split.n > 1 ? w.split.n * w.split.rows : rows, K, true)
+                        : make_tmap_out(&tx, dx + m0 * K, rows, K, false)))
                 return CR_ERR_CUDA;
             GemmEpilogue e;
             e.xs = xs + m0;
@@ -1512,7 +1549,6 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
             e.ex.V = V;
             e.ex.n0 = (int)n0;
             e.ex.lse = lse + m0;
-            e.ex.dloss = dloss + m0;
             st = launch_gemm<gm::kCeGrad>(*d, xq + m0 * K, w.w8, &tl, rows, n, K, e, stream);
             if (st != CR_OK)
                 return st;
@@ -1522,13 +1558,21 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
                 return st;
             GemmEpilogue g;
             g.out_f32 = w.acc != nullptr;
-            st = w.acc && n0 > 0 ? launch_gemm<gm::kBf16Add>(*d, w.dl, w.wt, &tx, rows, K, np, g, stream)
-                                 : launch_gemm<gm::kBf16>(*d, w.dl, w.wt, &tx, rows, K, np, g, stream);
+            // a short last piece has fewer blocks of terms than ranges: every range keeps one
+            g.ex.splits = (int)((np + 63) / 64 < w.split.n ? (np + 63) / 64 : w.split.n);
+            g.ex.split_rows = (int)w.split.rows;
+            g.ex.targets = targets + m0;
+            g.ex.ignore = ignore_index;
+            g.ex.V = V;
+            g.ex.dloss = dloss + m0;
+            st = w.acc && n0 > 0 ? launch_gemm<gm::kBf16RowsAdd>(*d, w.dl, w.wt, &tx, rows, K, np, g, stream)
+                                 : launch_gemm<gm::kBf16Rows>(*d, w.dl, w.wt, &tx, rows, K, np, g, stream);
             if (st != CR_OK)
                 return st;
         }
         if (w.acc) {
-            st = launched(ce::launch_to_bf16(w.acc, rows * K, dx + m0 * K, d->num_sms, stream));
+            st = launched(ce::launch_sum_to_bf16(w.acc, w.split.n, w.split.rows, rows, K, dx + m0 * K, d->num_sms,
+                                                 stream));
             if (st != CR_OK)
                 return st;
         }

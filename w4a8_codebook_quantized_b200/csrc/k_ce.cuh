@@ -5,8 +5,7 @@
 //   lse[m] = log sum_n e^y[m, n],   loss[m] = lse[m] - y[m, target[m]]
 //
 // A row's statistics come as pairs (reference in log2, sum of 2^(y log2 e -
-// reference)), one per column slice, [slices, M]; joining two pairs rescales
-// the smaller reference's sum.
+// reference)), one per column slice, [M, slices].
 #pragma once
 
 #include "cr_device.cuh"
@@ -18,17 +17,11 @@ namespace ce {
 constexpr int kThreads = 256;
 constexpr int kSlice = 2048;  // columns per CTA of stats_kernel
 
-__device__ __forceinline__ void join(float2 &a, const float2 b)
-{
-    const float m = fmaxf(a.x, b.x);
-    const float base = m == __int_as_float(0xFF800000) ? 0.0f : m;
-    a.y = a.y * gm::ex2(a.x - base) + b.y * gm::ex2(b.x - base);
-    a.x = m;
-}
+using gm::join;
 
 // Statistics of stored fp32 outputs y [M, V] (a decode batch, whose outputs
 // the GEMV wrote), kSlice columns per CTA: grid (slices, M).
-__global__ void __launch_bounds__(kThreads) stats_kernel(const float *__restrict__ y, int64_t M, int64_t V,
+__global__ void __launch_bounds__(kThreads) stats_kernel(const float *__restrict__ y, int64_t V,
                                                          const int64_t *__restrict__ targets,
                                                          float2 *__restrict__ part, float *__restrict__ tlogit)
 {
@@ -62,34 +55,31 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const float *__restrict
 #pragma unroll
         for (int w = 1; w < kThreads / 32; ++w)
             join(a, sh[w]);
-        part[(int64_t)blockIdx.x * M + m] = a;
+        part[m * gridDim.x + blockIdx.x] = a;
     }
 }
 
-// lse and loss of 32 rows per CTA from their statistics: a warp takes every
-// eighth slice of the rows (lane = row: whole sectors), then warp 0 joins the
-// eight in a fixed order.  The last steps are in fp64: a few operations per
-// row, and the loss is often a small difference of larger numbers.
+// lse and loss from the statistics, a warp per row: the lanes take every 32nd
+// slice each and are joined in a fixed order.  The last steps are in fp64: a
+// few operations per row, and the loss is often a small difference of larger
+// numbers.
 __global__ void __launch_bounds__(kThreads) loss_kernel(const float2 *__restrict__ part, int64_t slices, int64_t M,
                                                         const int64_t *__restrict__ targets, int64_t ignore, int64_t V,
                                                         const float *__restrict__ tlogit, float *__restrict__ loss,
                                                         float *__restrict__ lse)
 {
-    __shared__ float2 sh[kThreads / 32][32];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t m = 32 * (int64_t)blockIdx.x + lane;
+    const int lane = threadIdx.x & 31;
+    const int64_t m = (kThreads / 32) * (int64_t)blockIdx.x + (threadIdx.x >> 5);
+    if (m >= M)
+        return;
     float2 a = make_float2(__int_as_float(0xFF800000), 0.0f);
-    if (m < M) {
 #pragma unroll 4
-        for (int64_t s = w; s < slices; s += kThreads / 32)
-            join(a, part[s * M + m]);
-    }
-    sh[w][lane] = a;
-    __syncthreads();
-    if (w == 0 && m < M) {
+    for (int64_t s = lane; s < slices; s += 32)
+        join(a, part[m * slices + s]);
 #pragma unroll
-        for (int i = 1; i < kThreads / 32; ++i)
-            join(a, sh[i][lane]);
+    for (int o = 16; o >= 1; o >>= 1)
+        join(a, make_float2(__shfl_xor_sync(0xFFFFFFFFu, a.x, o), __shfl_xor_sync(0xFFFFFFFFu, a.y, o)));
+    if (lane == 0) {
         // the references are in units of the fp32 constant that made them
         const double l = (double)a.x / (double)gm::kLog2e + log((double)a.y);
         lse[m] = (float)l;
@@ -101,12 +91,19 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const float2 *__restrict
     }
 }
 
-// fp32 -> bf16, four elements per thread and step.
-__global__ void __launch_bounds__(kThreads) to_bf16_kernel(const float4 *__restrict__ src, int64_t n4,
-                                                           uint2 *__restrict__ dst)
+// out[m, k] = bf16(sum over s of acc[s, m, k]), four elements per thread and
+// step; the sums are taken in the order of s.
+__global__ void __launch_bounds__(kThreads) sum_to_bf16_kernel(const float4 *__restrict__ acc, int splits,
+                                                               int64_t split_stride4, int64_t n4,
+                                                               uint2 *__restrict__ dst)
 {
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n4; i += (int64_t)gridDim.x * kThreads) {
-        const float4 v = src[i];
+        float4 v = acc[i];
+#pragma unroll 4
+        for (int s = 1; s < splits; ++s) {
+            const float4 u = acc[s * split_stride4 + i];
+            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        }
         dst[i] = make_uint2(to_bf16x2_bits(v.x, v.y), to_bf16x2_bits(v.z, v.w));
     }
 }
@@ -114,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) to_bf16_kernel(const float4 *__restr
 inline cudaError_t launch_stats(const float *y, int64_t M, int64_t V, const int64_t *targets, float2 *part,
                                 float *tlogit, cudaStream_t stream)
 {
-    stats_kernel<<<dim3((unsigned)((V + kSlice - 1) / kSlice), (unsigned)M), kThreads, 0, stream>>>(y, M, V, targets,
+    stats_kernel<<<dim3((unsigned)((V + kSlice - 1) / kSlice), (unsigned)M), kThreads, 0, stream>>>(y, V, targets,
                                                                                                     part, tlogit);
     return cudaGetLastError();
 }
@@ -122,19 +119,21 @@ inline cudaError_t launch_stats(const float *y, int64_t M, int64_t V, const int6
 inline cudaError_t launch_loss(const float2 *part, int64_t slices, int64_t M, const int64_t *targets, int64_t ignore,
                                int64_t V, const float *tlogit, float *loss, float *lse, cudaStream_t stream)
 {
-    loss_kernel<<<(unsigned)((M + 31) / 32), kThreads, 0, stream>>>(part, slices, M, targets, ignore, V, tlogit, loss,
+    loss_kernel<<<(unsigned)((M + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, stream>>>(part, slices, M, targets, ignore, V, tlogit, loss,
                                                                     lse);
     return cudaGetLastError();
 }
 
-inline cudaError_t launch_to_bf16(const float *src, int64_t n, uint16_t *dst, int num_sms, cudaStream_t stream)
+// acc: `splits` blocks of split_rows x K fp32; dst [M, K] bf16.
+inline cudaError_t launch_sum_to_bf16(const float *acc, int splits, int64_t split_rows, int64_t M, int64_t K,
+                                      uint16_t *dst, int num_sms, cudaStream_t stream)
 {
-    const int64_t n4 = n / 4;
+    const int64_t n4 = M * K / 4;
     int64_t grid = (n4 + kThreads - 1) / kThreads;
     if (grid > 8 * (int64_t)num_sms)
         grid = 8 * (int64_t)num_sms;
-    to_bf16_kernel<<<(unsigned)grid, kThreads, 0, stream>>>(reinterpret_cast<const float4 *>(src), n4,
-                                                            reinterpret_cast<uint2 *>(dst));
+    sum_to_bf16_kernel<<<(unsigned)grid, kThreads, 0, stream>>>(reinterpret_cast<const float4 *>(acc), splits,
+                                                                split_rows * K / 4, n4, reinterpret_cast<uint2 *>(dst));
     return cudaGetLastError();
 }
 

@@ -35,13 +35,22 @@ namespace gm {
 enum Mode : int {
     kI8 = 0,         // int8; the layer's outputs (with SwiGLU when asked)
     kBf16 = 1,       // bf16 x bf16 -> fp32; the accumulators are the outputs
-    kBf16Add = 2,    // the same, added to the fp32 outputs already there
+    kBf16RowsAdd = 2,  // bf16; outputs scaled by row and added to the fp32 outputs already there
     kSwigluGrad = 3, // int8; the gradient of interleaved gate/up outputs
     kCeStats = 4,    // int8; softmax statistics of the outputs
-    kCeGrad = 5      // int8; the cross entropy's gradient of the outputs
+    kCeGrad = 5,     // int8; the cross entropy's gradient of the outputs, up to each row's factor
+    kBf16Rows = 6,   // bf16; outputs scaled by row
+    kModes = 7
 };
 
-constexpr bool is_bf16(int mode) { return mode == kBf16 || mode == kBf16Add; }
+constexpr bool is_bf16(int mode) { return mode == kBf16 || mode == kBf16Rows || mode == kBf16RowsAdd; }
+constexpr bool row_factor(int mode) { return mode == kBf16Rows || mode == kBf16RowsAdd; }
+
+// The epilogues that evaluate exponentials per output take eight warps (each
+// 32 rows x 128 columns of a tile) where the others take four (32 x 256): with
+// four, the epilogue of an int8 tile outlasted the tile's own MMAs.
+constexpr int epi_warps(int mode) { return mode == kSwigluGrad || mode == kCeStats || mode == kCeGrad ? 8 : 4; }
+constexpr int threads(int mode) { return 64 + 32 * epi_warps(mode); }
 
 // What the epilogues beyond the layer's own read and write.
 struct EpiArgs {
@@ -49,9 +58,24 @@ struct EpiArgs {
     const int64_t *targets = nullptr;  // kCe*: [M]
     int64_t ignore = 0, V = 0;         // kCe*: the target that has no loss; the whole vocabulary
     int n0 = 0;                        // kCe*: the vocabulary entry of column 0
-    float2 *part = nullptr;            // kCeStats: [tiles, M] (reference in log2, sum)
+    float2 *part = nullptr;            // kCeStats: [M, slices] (reference in log2, sum)
+    int slices = 0;
     float *tlogit = nullptr;           // kCeStats: [M], the target's output
-    const float *lse = nullptr, *dloss = nullptr;  // kCeGrad: [M]
+    const float *lse = nullptr;        // kCeGrad: [M]
+    const float *dloss = nullptr;      // kBf16Rows*: [M], with targets
+    // bf16 modes: the reduction split into so many ranges, each a tile of its
+    // own whose outputs go to rows split * split_rows + row
+    int splits = 1, split_rows = 0;
+
+    // The factor of a row of the cross entropy's gradient: dloss, 0 in ignored
+    // rows, NaN in rows whose target is outside the vocabulary.
+    __device__ __forceinline__ float row_scale(int row) const
+    {
+        const int64_t t = targets[row];
+        if (t == ignore)
+            return 0.0f;
+        return t >= 0 && t < V ? dloss[row] : __int_as_float(0x7FC00000);
+    }
 };
 
 constexpr int BM = 128, BN = 256, BK = 128;  // BK in int8 elements = bytes
@@ -60,7 +84,6 @@ constexpr int kABytes = BM * BK;              // 16 KB
 constexpr int kBBytes = BN * BK;              // 32 KB
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kTmemCols = 2 * BN;             // two accumulators
-constexpr int kThreads = 192;
 constexpr uint32_t kIdesc = idesc_i8(BM, BN);
 
 constexpr int kEpiBytes = 32 * 128;  // one epilogue store unit: 32 rows x 128 bytes
@@ -113,6 +136,29 @@ __device__ __forceinline__ void store_unit_rows(const uint32_t (&p)[32], int uco
     ++units_issued;
 }
 
+// The same for 32 bf16 columns (16 words a lane, 64 bytes a row; `tmOut` has
+// the 64-byte swizzle: chunk c of row r at chunk c ^ ((r / 2) % 4)).
+__device__ __forceinline__ void store_half_unit(const uint32_t (&p)[16], int ucol0, int row0, int lane,
+                                                const CUtensorMap *tmOut, uint8_t *stg, uint32_t &units_issued)
+{
+    if (units_issued >= 1) {
+        if (lane == 0)
+            bulk_wait_read<0>();  // the previous store has read the staging buffer
+        __syncwarp();
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4 *>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16)) =
+            make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_2d(tmOut, ucol0, row0, stg);
+        bulk_commit();
+    }
+    ++units_issued;
+}
+
 // Epilogue of one 128 x 256 accumulator tile for one warp: its 32 TMEM lanes
 // are rows row0 + lane; `tbase` addresses lane 0 of the warp's quarter at the
 // tile's first column; the output columns are col_base + [0, 256).  Fast path
@@ -123,9 +169,9 @@ __device__ __forceinline__ void store_unit_rows(const uint32_t (&p)[32], int uco
 // thread stores its own row.  release() hands the accumulator back once every
 // column is in registers.
 // RAW: the accumulator holds fp32 values that are the outputs themselves
-// (bf16 GEMM); no scales, bias or SwiGLU.  ADD: the fp32 outputs are added to
+// (bf16 GEMM; ROWS: times xm); no channel scales, bias or SwiGLU.  ADD: the fp32 outputs are added to
 // what is there, by the bulk stores' own reduction (tma_out only).
-template <bool RAW, bool ADD, class Release>
+template <bool RAW, bool ROWS, bool ADD, class Release>
 __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_base, int lane, float xm, bool row_ok,
                                               const float *wsv, const float *bsv, bool has_bias, int M, int N,
                                               int out_f32, int swiglu, int tma_out, const CUtensorMap *tmOut,
@@ -143,7 +189,7 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_
             if constexpr (RAW) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    y[e] = __uint_as_float(v[j + e]);
+                    y[e] = ROWS ? __fmul_rn(__uint_as_float(v[j + e]), xm) : __uint_as_float(v[j + e]);
             } else {
                 const float4 w4 = *reinterpret_cast<const float4 *>(wsv + c0 + j);
                 const float4 b4 = *reinterpret_cast<const float4 *>(bsv + c0 + j);
@@ -302,7 +348,9 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_
                     const int n = col0 + j;
                     if (n >= N)
                         break;
-                    const float y = RAW ? __uint_as_float(cur[j]) : epilogue_value((int32_t)cur[j], xm, ws[n], bias, n);
+                    const float y = ROWS  ? __fmul_rn(__uint_as_float(cur[j]), xm)
+                                    : RAW ? __uint_as_float(cur[j])
+                                          : epilogue_value((int32_t)cur[j], xm, ws[n], bias, n);
                     if (out_f32)
                         reinterpret_cast<float *>(out)[base + j] = y;
                     else
@@ -371,45 +419,46 @@ __device__ __forceinline__ void load_dout16(const uint16_t *drow, int f0, int F,
     }
 }
 
-// Epilogue of kSwigluGrad for one warp's 32 rows of a tile: accumulator
-// columns 2f and 2f + 1 are gate and up of output column f; their gradients
-// leave as the same two columns of dz [M, N] bf16.  Each row's 16 values of
-// dout for the next 32 columns are loaded while the current ones are used.
+// The epilogues below take one warp's 32 rows and columns [c_lo, c_lo + 128)
+// of a tile, 32 columns at a time.
+constexpr int kEpiCols = 128;
+
+// Epilogue of kSwigluGrad: accumulator columns 2f and 2f + 1 are gate and up
+// of output column f; their gradients leave as the same two columns of dz
+// [M, N] bf16.  Each row's 16 values of dout for the next 32 columns are loaded
+// while the current ones are used (`dn`: those of the first, loaded by the
+// caller before it waits for the accumulator).
 template <class Release>
-__device__ __forceinline__ void epilogue_swiglu_grad(uint32_t tbase, int row0, int col_base, int lane, float xm,
-                                                     bool row_ok, const float *wsv, const float *bsv, bool has_bias,
-                                                     int N, const EpiArgs &ex, const CUtensorMap *tmOut,
-                                                     uint8_t *stage_buf, uint32_t &units_issued, Release release)
+__device__ __forceinline__ void epilogue_swiglu_grad(uint32_t tbase, int row0, int col_base, int c_lo, int lane,
+                                                     float xm, bool row_ok, const float *wsv, const float *bsv,
+                                                     bool has_bias, int N, const EpiArgs &ex, const CUtensorMap *tmOut,
+                                                     uint8_t *stage_buf, uint32_t &units_issued, uint32_t (&dn)[8],
+                                                     Release release)
 {
-    const int F = N >> 1, f_base = col_base >> 1;
+    const int F = N >> 1;
     const uint16_t *drow = ex.dout + (int64_t)(row0 + lane) * F;
-    uint32_t dn[8], cur[32], packed[32];
-    load_dout16(drow, f_base, F, row_ok, dn);
-    for (int un = 0; un < BN / 64; ++un) {
+#pragma unroll 1
+    for (int c0 = c_lo; c0 < c_lo + kEpiCols; c0 += 32) {
+        uint32_t cur[32], d[8], packed[16];
+        __syncwarp();
+        tmem_ld_32cols(tbase + (uint32_t)c0, cur);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int c0 = 64 * un + 32 * k;
-            __syncwarp();
-            tmem_ld_32cols(tbase + (uint32_t)c0, cur);
-            uint32_t d[8];
+        for (int i = 0; i < 8; ++i)
+            d[i] = dn[i];
+        if (c0 + 32 < c_lo + kEpiCols)
+            load_dout16(drow, (col_base + c0 + 32) >> 1, F, row_ok, dn);
+        tmem_ld_wait();
+        if (c0 + 32 == c_lo + kEpiCols)
+            release();
+        float y[32];
+        outputs32(cur, c0, xm, wsv, bsv, has_bias, y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                d[i] = dn[i];
-            if (c0 + 32 < BN)
-                load_dout16(drow, f_base + (c0 + 32) / 2, F, row_ok, dn);
-            tmem_ld_wait();
-            if (c0 + 32 == BN)
-                release();
-            float y[32];
-            outputs32(cur, c0, xm, wsv, bsv, has_bias, y);
-#pragma unroll
-            for (int p = 0; p < 16; ++p) {
-                const float dv = __uint_as_float((p & 1) ? d[p >> 1] & 0xFFFF0000u : d[p >> 1] << 16);
-                packed[16 * k + p] = swiglu_grad(y[2 * p], y[2 * p + 1], dv);
-            }
+        for (int p = 0; p < 16; ++p) {
+            const float dv = __uint_as_float((p & 1) ? d[p >> 1] & 0xFFFF0000u : d[p >> 1] << 16);
+            packed[p] = swiglu_grad(y[2 * p], y[2 * p + 1], dv);
         }
-        if (col_base + 64 * un < N)
-            store_unit_rows<false>(packed, col_base + 64 * un, row0, lane, tmOut, stage_buf, units_issued);
+        if (col_base + c0 < N)
+            store_half_unit(packed, col_base + c0, row0, lane, tmOut, stage_buf, units_issued);
     }
 }
 
@@ -423,42 +472,53 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// Epilogue of kCeStats for one warp's 32 rows: each row's sum of exponentials
-// over the tile's (at most 256) columns, relative to its maximum there.  The
-// reference is kept in the base-2 domain as the rounded product max * log2(e),
-// and every term is 2^(fma(y, log2 e, -reference)), so the pair (reference,
-// sum) carries no error of the reference's rounding.  Columns past N are left
-// out; -inf outputs (a bias that masks a vocabulary entry) contribute 0, also
-// where a whole tile has nothing else.
+// A row's sum of exponentials as a pair: the reference (its maximum in the
+// base-2 domain) and the sum relative to it.  Joining two rescales the smaller
+// reference's sum.
+__device__ __forceinline__ void join(float2 &a, const float2 b)
+{
+    const float m = fmaxf(a.x, b.x);
+    const float base = m == __int_as_float(0xFF800000) ? 0.0f : m;
+    a.y = a.y * ex2(a.x - base) + b.y * ex2(b.x - base);
+    a.x = m;
+}
+
+// Epilogue of kCeStats: each row's sum of exponentials over the warp's
+// columns, relative to its maximum there.  The reference is kept in the base-2
+// domain as the rounded product max * log2(e), and every term is 2^(fma(y,
+// log2 e, -reference)), so the pair (reference, sum) carries no error of the
+// reference's rounding.  Columns past N are left out; -inf outputs (a bias
+// that masks a vocabulary entry) contribute 0, also where there is nothing
+// else.  The target's output goes to tlogit.
 template <class Release>
-__device__ __forceinline__ void epilogue_ce_stats(uint32_t tbase, int row, int tile_n, int lane, float xm, bool row_ok,
-                                                  const float *wsv, const float *bsv, bool has_bias, int M, int N,
-                                                  const EpiArgs &ex, Release release)
+__device__ __forceinline__ float2 epilogue_ce_stats(uint32_t tbase, int row, int col_base, int c_lo, float xm,
+                                                    bool row_ok, const float *wsv, const float *bsv, bool has_bias,
+                                                    int N, const EpiArgs &ex, Release release)
 {
     const float kNegInf = __int_as_float(0xFF800000);
-    const int col_base = tile_n * BN;
-    const int64_t t = row_ok ? ex.targets[row] : -1, lo = (int64_t)ex.n0 + col_base;
-    const int tcol = (t >= lo && t < lo + BN && t - ex.n0 < N) ? (int)(t - lo) : -1;  // the target in this tile
+    const int64_t t = row_ok ? ex.targets[row] : -1, lo = (int64_t)ex.n0 + col_base + c_lo;
+    const int tcol = (t >= lo && t < lo + kEpiCols && t - ex.n0 < N) ? c_lo + (int)(t - lo) : -1;
     float ref = kNegInf, s0 = 0.0f, s1 = 0.0f, tl = 0.0f;
-    for (int ch = 0; ch < BN / 32; ++ch) {
+#pragma unroll 1
+    for (int c0 = c_lo; c0 < c_lo + kEpiCols; c0 += 32) {
         uint32_t cur[32];
         __syncwarp();
-        tmem_ld_32cols(tbase + (uint32_t)(32 * ch), cur);
+        tmem_ld_32cols(tbase + (uint32_t)c0, cur);
         tmem_ld_wait();
-        if (ch + 1 == BN / 32)
+        if (c0 + 32 == c_lo + kEpiCols)
             release();
         float y[32];
-        outputs32(cur, 32 * ch, xm, wsv, bsv, has_bias, y);
-        if (col_base + 32 * ch + 32 > N) {
+        outputs32(cur, c0, xm, wsv, bsv, has_bias, y);
+        if (col_base + c0 + 32 > N) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (col_base + 32 * ch + j >= N)
+                if (col_base + c0 + j >= N)
                     y[j] = kNegInf;
         }
-        if ((tcol >> 5) == ch) {
+        if (tcol >= c0 && tcol < c0 + 32) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if ((tcol & 31) == j)
+                if (tcol == c0 + j)
                     tl = y[j];
         }
         float m0 = y[0], m1 = y[1];
@@ -479,98 +539,130 @@ __device__ __forceinline__ void epilogue_ce_stats(uint32_t tbase, int row, int t
         }
         ref = next;
     }
-    if (row_ok) {
-        ex.part[(int64_t)(ex.n0 / BN + tile_n) * M + row] = make_float2(ref, s0 + s1);
-        if (tcol >= 0)
-            ex.tlogit[row] = tl;
-    }
+    if (tcol >= 0)
+        ex.tlogit[row] = tl;
+    return make_float2(ref, s0 + s1);
 }
 
-// Epilogue of kCeGrad: dl[m, n] = dloss[m] * (e^(y - lse[m]) - [n = target]),
-// zero for ignored rows, to bf16; columns from N to the buffer's width (a
-// multiple of 8) are written as zeros.  A target outside the vocabulary makes
-// its row NaN.
+// Epilogue of kCeGrad: dl[m, n] = e^(y - lse[m]) - [n = target], zero for
+// ignored rows, to bf16; columns from N to the buffer's width (a multiple of
+// 8) are written as zeros.  The row's factor dloss[m] is applied after the
+// contraction: dl at the target is then -1 rounded by at most the target's
+// probability, where -dloss itself would carry bf16's relative rounding, the
+// same one in every row of a mean (0.4 percent of dx at worst).
 template <class Release>
-__device__ __forceinline__ void epilogue_ce_grad(uint32_t tbase, int row0, int col_base, int lane, float xm,
+__device__ __forceinline__ void epilogue_ce_grad(uint32_t tbase, int row0, int col_base, int c_lo, int lane, float xm,
                                                  bool row_ok, const float *wsv, const float *bsv, bool has_bias,
                                                  int N, const EpiArgs &ex, const CUtensorMap *tmOut,
                                                  uint8_t *stage_buf, uint32_t &units_issued, Release release)
 {
     const int row = row0 + lane;
-    float scale = 0.0f, lse2 = __int_as_float(0x7F800000);  // an ignored row: every exponential 0
+    float lse2 = __int_as_float(0x7F800000);  // an ignored row: every exponential 0
     int tcol = -1;
     if (row_ok) {
         const int64_t t = ex.targets[row];
         if (t != ex.ignore) {
             lse2 = __fmul_rn(ex.lse[row], kLog2e);
-            scale = (t >= 0 && t < ex.V) ? ex.dloss[row] : __int_as_float(0x7FC00000);
             const int64_t lo = (int64_t)ex.n0 + col_base;
             tcol = (t >= lo && t < lo + BN) ? (int)(t - lo) : -1;
         }
     }
-    uint32_t cur[32], packed[32];
-    for (int un = 0; un < BN / 64; ++un) {
+#pragma unroll 1
+    for (int c0 = c_lo; c0 < c_lo + kEpiCols; c0 += 32) {
+        uint32_t cur[32], packed[16];
+        __syncwarp();
+        tmem_ld_32cols(tbase + (uint32_t)c0, cur);
+        tmem_ld_wait();
+        if (c0 + 32 == c_lo + kEpiCols)
+            release();
+        float y[32];
+        outputs32(cur, c0, xm, wsv, bsv, has_bias, y);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int c0 = 64 * un + 32 * k;
-            __syncwarp();
-            tmem_ld_32cols(tbase + (uint32_t)c0, cur);
-            tmem_ld_wait();
-            if (c0 + 32 == BN)
-                release();
-            float y[32];
-            outputs32(cur, c0, xm, wsv, bsv, has_bias, y);
+        for (int j = 0; j < 32; ++j)
+            y[j] = ex2(__fmaf_rn(y[j], kLog2e, -lse2));
+        if (tcol >= c0 && tcol < c0 + 32) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                y[j] = ex2(__fmaf_rn(y[j], kLog2e, -lse2));
-            if ((tcol >> 5) == (c0 >> 5)) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if ((tcol & 31) == j)
-                        y[j] -= 1.0f;
-            }
-            if (col_base + c0 + 32 > N) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (col_base + c0 + j >= N)
-                        y[j] = 0.0f;
-            }
-#pragma unroll
-            for (int p = 0; p < 16; ++p)
-                packed[16 * k + p] = to_bf16x2_bits(y[2 * p] * scale, y[2 * p + 1] * scale);
+                if (tcol == c0 + j)
+                    y[j] -= 1.0f;
         }
-        if (col_base + 64 * un < N)
-            store_unit_rows<false>(packed, col_base + 64 * un, row0, lane, tmOut, stage_buf, units_issued);
+        if (col_base + c0 + 32 > N) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (col_base + c0 + j >= N)
+                    y[j] = 0.0f;
+        }
+#pragma unroll
+        for (int p = 0; p < 16; ++p)
+            packed[p] = to_bf16x2_bits(y[2 * p], y[2 * p + 1]);
+        if (col_base + c0 < N)
+            store_half_unit(packed, col_base + c0, row0, lane, tmOut, stage_buf, units_issued);
     }
 }
 
-// The tile's epilogue for one warp, by mode.
-template <int MODE, class Release>
-__device__ __forceinline__ void epilogue_any(uint32_t tbase, int row0, int tile_n, int lane, float xm, bool row_ok,
-                                             const float *wsv, const float *bsv, bool has_bias, int M, int N,
+// One tile's epilogue for one warp of the CTA's epilogue warps, by mode:
+// `ew` is the warp's number among them, row0 the first of its 32 rows in the
+// output's row numbering (past M only in the padding of a split reduction),
+// row the calling lane's row.  wait() waits for the accumulator and is called
+// after whatever can be loaded before it; it returns false after an abort.
+template <int MODE, class Sh, class Wait, class Release>
+__device__ __forceinline__ void epilogue_any(Sh &sh, int ew, int buf, uint32_t tbase, int row0, int out_row0,
+                                             int tile_n, int lane, const float *xs, bool has_bias, int M, int N,
                                              int out_f32, int swiglu, int tma_out, const CUtensorMap *tmOut,
-                                             uint8_t *stage_buf, uint32_t &units_issued, void *out, int32_t *acc_out,
-                                             const float *ws, const float *bias, const EpiArgs &ex, Release release)
+                                             uint32_t &units_issued, void *out, int32_t *acc_out, const float *ws,
+                                             const float *bias, const EpiArgs &ex, Wait wait, Release release)
 {
-    if constexpr (MODE == kSwigluGrad)
-        epilogue_swiglu_grad(tbase, row0, tile_n * BN, lane, xm, row_ok, wsv, bsv, has_bias, N, ex, tmOut, stage_buf,
-                             units_issued, release);
-    else if constexpr (MODE == kCeStats)
-        epilogue_ce_stats(tbase, row0 + lane, tile_n, lane, xm, row_ok, wsv, bsv, has_bias, M, N, ex, release);
-    else if constexpr (MODE == kCeGrad)
-        epilogue_ce_grad(tbase, row0, tile_n * BN, lane, xm, row_ok, wsv, bsv, has_bias, N, ex, tmOut, stage_buf,
-                         units_issued, release);
-    else
-        epilogue_tile<is_bf16(MODE), MODE == kBf16Add>(tbase, row0, tile_n * BN, lane, xm, row_ok, wsv, bsv, has_bias,
-                                                       M, N, out_f32, swiglu, tma_out, tmOut, stage_buf, units_issued,
-                                                       out, acc_out, ws, bias, release);
+    const int row = row0 + lane;
+    const bool row_ok = row < M;
+    const float *wsv = sh.wsb[buf], *bsv = sh.biasb[buf];
+    if constexpr (epi_warps(MODE) == 4) {
+        if (!wait())
+            return;
+        const float xm = !row_ok ? 0.0f : row_factor(MODE) ? ex.row_scale(row) : is_bf16(MODE) ? 0.0f : xs[row];
+        epilogue_tile<is_bf16(MODE), row_factor(MODE), MODE == kBf16RowsAdd>(
+            tbase, out_row0, tile_n * BN, lane, xm, row_ok, wsv, bsv, has_bias, M, N, out_f32, swiglu, tma_out, tmOut,
+            sh.epi[ew], units_issued, out, acc_out, ws, bias, release);
+    } else {
+        const int c_lo = (ew >> 2) * kEpiCols, col_base = tile_n * BN;
+        uint8_t *stage_buf = &sh.epi[0][0] + ew * (kEpiBytes / 2);
+        const float xm = row_ok ? xs[row] : 0.0f;
+        if constexpr (MODE == kSwigluGrad) {
+            uint32_t dn[8];
+            load_dout16(ex.dout + (int64_t)row * (N >> 1), (col_base + c_lo) >> 1, N >> 1, row_ok, dn);
+            if (!wait())
+                return;
+            epilogue_swiglu_grad(tbase, row0, col_base, c_lo, lane, xm, row_ok, wsv, bsv, has_bias, N, ex, tmOut,
+                                 stage_buf, units_issued, dn, release);
+        } else if constexpr (MODE == kCeGrad) {
+            if (!wait())
+                return;
+            epilogue_ce_grad(tbase, row0, col_base, c_lo, lane, xm, row_ok, wsv, bsv, has_bias, N, ex, tmOut,
+                             stage_buf, units_issued, release);
+        } else {
+            // the two warps of a row join their halves: the upper one's pairs
+            // go through its staging buffer (unused otherwise).  After an abort
+            // both still meet at the barrier.
+            const bool ok = wait();
+            float2 a = make_float2(0.0f, 0.0f);
+            if (ok)
+                a = epilogue_ce_stats(tbase, row, col_base, c_lo, xm, row_ok, wsv, bsv, has_bias, N, ex, release);
+            float2 *half = reinterpret_cast<float2 *>(&sh.epi[0][0]) + 32 * (ew & 3);
+            if (ew >= 4)
+                half[lane] = a;
+            asm volatile("bar.sync 3, 256;" ::: "memory");
+            if (ok && ew < 4 && row_ok) {
+                join(a, half[lane]);
+                ex.part[(int64_t)row * ex.slices + ex.n0 / BN + tile_n] = a;
+            }
+        }
+    }
 }
 
 // BF16 modes: A and B are bf16 (K counted in bf16 elements, 64 per 128-byte
 // stage row), tcgen05.mma kind::f16 into fp32, and the epilogue writes the
 // accumulators as they are (xs, ws, bias, swiglu and acc_out unused).
 template <int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads(MODE), 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmOut, const float *__restrict__ xs,
                 const float *__restrict__ ws, const float *__restrict__ bias, int M, int N, int K, int out_f32,
@@ -582,9 +674,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
-    const int num_tiles = tiles_m * tiles_n;
+    const int splits = BF16 ? ex.splits : 1;  // ranges of the reduction
+    const int mn_tiles = tiles_m * tiles_n, num_tiles = mn_tiles * splits;
     constexpr int BKE = BF16 ? BK / 2 : BK;  // K elements per stage
     const int kblocks = (K + BKE - 1) / BKE;
+    // a tile's place and its range [k0, k1) of the reduction's blocks
+    auto coords = [&](int tile, int &tm, int &tn, int &k0, int &k1) {
+        int split = 0;
+        k0 = 0;
+        k1 = kblocks;
+        if constexpr (BF16) {
+            split = tile / mn_tiles;
+            tile -= split * mn_tiles;
+            k0 = (int)((int64_t)kblocks * split / splits);
+            k1 = (int)((int64_t)kblocks * (split + 1) / splits);
+        }
+        tile_coords(tile, tiles_n, tm, tn);
+        return split;
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -593,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sh.tmem_full[b], 1);
-            mbar_init(&sh.tmem_empty[b], 4);
+            mbar_init(&sh.tmem_empty[b], epi_warps(MODE));
         }
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -622,9 +729,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issued[s] = 0, issued_phase[s] = 0;
             bool ok = true;
             for (int tile = blockIdx.x; ok && tile < num_tiles; tile += gridDim.x) {
-                int tm, tn;
-                tile_coords(tile, tiles_n, tm, tn);
-                for (int kb = 0; kb < kblocks; ++kb) {
+                int tm, tn, k0, k1;
+                coords(tile, tm, tn, k0, k1);
+                for (int kb = k0; kb < k1; ++kb) {
                     if (!mbar_wait_bounded(&sh.empty[stage], phase ^ 1u, abort)) {
                         ok = false;
                         break;
@@ -665,7 +772,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * BN);
-                for (int kb = 0; kb < kblocks; ++kb) {
+                int tm, tn, k0, k1;
+                coords(tile, tm, tn, k0, k1);
+                for (int kb = k0; kb < k1; ++kb) {
                     if (!mbar_wait_bounded(&sh.full[stage], phase, abort)) {
                         ok = false;
                         break;
@@ -678,9 +787,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t ad = sw128_kmajor_desc(a_addr + 32u * kk);
                         const uint64_t bd = sw128_kmajor_desc(b_addr + 32u * kk);
                         if constexpr (BF16)
-                            mma_bf16(d, ad, bd, idesc_bf16(BM, BN), (kb | kk) != 0 ? 1u : 0u);
+                            mma_bf16(d, ad, bd, idesc_bf16(BM, BN), ((kb - k0) | kk) != 0 ? 1u : 0u);
                         else
-                            mma_i8(d, ad, bd, kIdesc, (kb | kk) != 0 ? 1u : 0u);
+                            mma_i8(d, ad, bd, kIdesc, ((kb - k0) | kk) != 0 ? 1u : 0u);
                     }
                     tc_commit(&sh.empty[stage]);
                     if (++stage == kStages) {
@@ -693,9 +802,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        // ------------------------------------------------ epilogue (warps 2..5)
+        // ------------------------------------------------ epilogue (warps 2..5, or 2..9)
         // Warp q owns TMEM lanes 32q..32q+31 = rows 32q.. of the tile.
-        // Per tile: the 128 epilogue threads stage the tile's channel scales
+        // Per tile: the epilogue threads stage the tile's channel scales
         // (and bias) in shared memory before waiting for the accumulator, so
         // that latency hides under the MMAs.  The accumulator is read 32
         // columns at a time, the next chunk's TMEM load in flight while the
@@ -707,33 +816,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The loop never exits early: after an abort every warp still reaches
         // the same named barriers, skipping the work.
         const int q = warp & 3;
-        const int et = threadIdx.x - 64;  // 0..127 among the epilogue threads
+        const int et = threadIdx.x - 64;  // among the epilogue threads
         int local = 0;
         uint32_t units_issued = 0;
         for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++local) {
-            int tm, tn;
-            tile_coords(tile, tiles_n, tm, tn);
+            int tm, tn, k0, k1;
+            const int split = coords(tile, tm, tn, k0, k1);
             const int buf = local & 1;
             const uint32_t use = (uint32_t)(local >> 1) & 1u;
             if constexpr (!BF16) {
-                for (int j = et; j < BN; j += 128) {
+                for (int j = et; j < BN; j += 32 * epi_warps(MODE)) {
                     const int n = tn * BN + j;
                     sh.wsb[buf][j] = n < N ? ws[n] : 0.0f;
                     sh.biasb[buf][j] = (bias != nullptr && n < N) ? bias[n] : 0.0f;
                 }
             }
-            asm volatile("bar.sync 2, 128;" ::: "memory");
-            const bool ok = mbar_wait_bounded_warp(&sh.tmem_full[buf], use, abort);
-            if (!ok)
-                continue;
-            tc_fence_after();
-            const int row = tm * BM + 32 * q + lane;
-            const bool row_ok = row < M;
-            const float xm = (!BF16 && row_ok) ? xs[row] : 0.0f;
+            asm volatile("bar.sync 2, %0;" ::"n"(32 * epi_warps(MODE)) : "memory");
+            auto wait = [&]() {
+                const bool ok = mbar_wait_bounded_warp(&sh.tmem_full[buf], use, abort);
+                tc_fence_after();
+                return ok;
+            };
             const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * BN);
-            epilogue_any<MODE>(tbase, tm * BM + 32 * q, tn, lane, xm, row_ok, sh.wsb[buf], sh.biasb[buf],
-                          bias != nullptr, M, N, out_f32, swiglu, tma_out, &tmOut, sh.epi[q], units_issued, out, acc_out, ws,
-                          bias, ex, [&]() {
+            const int row0 = tm * BM + 32 * q;
+            epilogue_any<MODE>(sh, warp - 2, buf, tbase, row0, split * ex.split_rows + row0, tn, lane, xs,
+                               bias != nullptr, M, N, out_f32, swiglu, tma_out, &tmOut, units_issued, out, acc_out, ws,
+                               bias, ex, wait, [&]() {
                               tc_fence_before();
                               __syncwarp();
                               if (lane == 0)
@@ -788,7 +896,7 @@ constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 
 // BF16 as for gemm_kernel.
 template <int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads(MODE), 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmOut, const float *__restrict__ xs,
                      const float *__restrict__ ws, const float *__restrict__ bias, int M, int N, int K, int out_f32,
@@ -803,9 +911,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool leader = rank == 0;
     const int npairs = gridDim.x >> 1, pair_id = blockIdx.x >> 1;
     const int tiles_m = (M + 255) / 256, tiles_n = (N + BN - 1) / BN;
-    const int num_tiles = tiles_m * tiles_n;
+    const int splits = BF16 ? ex.splits : 1;  // ranges of the reduction
+    const int mn_tiles = tiles_m * tiles_n, num_tiles = mn_tiles * splits;
     constexpr int BKE = BF16 ? BK / 2 : BK;  // K elements per stage
     const int kblocks = (K + BKE - 1) / BKE;
+    // a tile's place and its range [k0, k1) of the reduction's blocks
+    auto coords = [&](int tile, int &tm, int &tn, int &k0, int &k1) {
+        int split = 0;
+        k0 = 0;
+        k1 = kblocks;
+        if constexpr (BF16) {
+            split = tile / mn_tiles;
+            tile -= split * mn_tiles;
+            k0 = (int)((int64_t)kblocks * split / splits);
+            k1 = (int)((int64_t)kblocks * (split + 1) / splits);
+        }
+        tile_coords(tile, tiles_n, tm, tn);
+        return split;
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < pair::kStages; ++s) {
@@ -814,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sh.tmem_full[b], 1);
-            mbar_init(&sh.tmem_empty[b], 8);
+            mbar_init(&sh.tmem_empty[b], 2 * epi_warps(MODE));
         }
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -843,9 +966,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issued[s] = 0, issued_phase[s] = 0;
             bool ok = true;
             for (int tile = pair_id; ok && tile < num_tiles; tile += npairs) {
-                int tm, tn;
-                tile_coords(tile, tiles_n, tm, tn);
-                for (int kb = 0; kb < kblocks; ++kb) {
+                int tm, tn, k0, k1;
+                coords(tile, tm, tn, k0, k1);
+                for (int kb = k0; kb < k1; ++kb) {
                     if (!mbar_wait_bounded(&sh.empty[stage], phase ^ 1u, abort)) {
                         ok = false;
                         break;
@@ -898,7 +1021,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * BN);
-                for (int kb = 0; kb < kblocks; ++kb) {
+                int tm, tn, k0, k1;
+                coords(tile, tm, tn, k0, k1);
+                for (int kb = k0; kb < k1; ++kb) {
                     if (!mbar_wait_bounded(&sh.full[stage], phase, abort)) {
                         ok = false;
                         break;
@@ -911,11 +1036,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if constexpr (BF16)
                             mma_bf16_pair(d, sw128_kmajor_desc(a_addr + 32u * kk),
                                           sw128_kmajor_desc(b_addr + 32u * kk), idesc_bf16(256, BN),
-                                          (kb | kk) != 0 ? 1u : 0u);
+                                          ((kb - k0) | kk) != 0 ? 1u : 0u);
                         else
                             mma_i8_pair(d, sw128_kmajor_desc(a_addr + 32u * kk),
                                         sw128_kmajor_desc(b_addr + 32u * kk), pair::kIdesc,
-                                        (kb | kk) != 0 ? 1u : 0u);
+                                        ((kb - k0) | kk) != 0 ? 1u : 0u);
                     const uint32_t e = smem_u32(&sh.empty[stage]);
                     tc_commit_pair(mapa_shared(e, 0));
                     tc_commit_pair(mapa_shared(e, peer));
@@ -932,35 +1057,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        // ------------------------------------------------ epilogue (warps 2..5, both CTAs)
+        // ------------------------------------------------ epilogue (warps 2..5, or 2..9, both CTAs)
         const int q = warp & 3;
         const int et = threadIdx.x - 64;
         int local = 0;
         uint32_t units_issued = 0;
         for (int tile = pair_id; tile < num_tiles; tile += npairs, ++local) {
-            int tm, tn;
-            tile_coords(tile, tiles_n, tm, tn);
+            int tm, tn, k0, k1;
+            const int split = coords(tile, tm, tn, k0, k1);
             const int buf = local & 1;
             const uint32_t use = (uint32_t)(local >> 1) & 1u;
             if constexpr (!BF16) {
-                for (int j = et; j < BN; j += 128) {
+                for (int j = et; j < BN; j += 32 * epi_warps(MODE)) {
                     const int n = tn * BN + j;
                     sh.wsb[buf][j] = n < N ? ws[n] : 0.0f;
                     sh.biasb[buf][j] = (bias != nullptr && n < N) ? bias[n] : 0.0f;
                 }
             }
-            asm volatile("bar.sync 2, 128;" ::: "memory");
-            const bool ok = mbar_wait_bounded_warp(&sh.tmem_full[buf], use, abort);
-            if (!ok)
-                continue;
-            tc_fence_after();
+            asm volatile("bar.sync 2, %0;" ::"n"(32 * epi_warps(MODE)) : "memory");
+            auto wait = [&]() {
+                const bool ok = mbar_wait_bounded_warp(&sh.tmem_full[buf], use, abort);
+                tc_fence_after();
+                return ok;
+            };
             const int row0 = tm * 256 + (int)rank * 128 + 32 * q;
-            const bool row_ok = row0 + lane < M;
-            const float xm = (!BF16 && row_ok) ? xs[row0 + lane] : 0.0f;
             const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * BN);
             const uint32_t release_addr = mapa_shared(smem_u32(&sh.tmem_empty[buf]), 0);
-            epilogue_any<MODE>(tbase, row0, tn, lane, xm, row_ok, sh.wsb[buf], sh.biasb[buf], bias != nullptr, M,
-                          N, out_f32, swiglu, tma_out, &tmOut, sh.epi[q], units_issued, out, acc_out, ws, bias, ex, [&]() {
+            epilogue_any<MODE>(sh, warp - 2, buf, tbase, row0, split * ex.split_rows + row0, tn, lane, xs,
+                               bias != nullptr, M, N, out_f32, swiglu, tma_out, &tmOut, units_issued, out, acc_out, ws,
+                               bias, ex, wait, [&]() {
                               tc_fence_before();
                               __syncwarp();
                               if (lane == 0)
