@@ -69,6 +69,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """The loaded C library with typed entry points (the raw C ABI)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -147,9 +149,15 @@ def cr_version() -> str:
 
 # ---------------------------------------------------------------- marshalling
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -252,9 +260,17 @@ def _on_stream(fn):
 
     @functools.wraps(fn)
     def wrapper(*args, stream=None, **kwargs):
-        if stream is None:
-            return body(*args, **kwargs)
         torch = _torch()
+        if stream is None:
+            # the usual call, all tensors on the current device, without the wrapper's search
+            here = torch.cuda.current_device()
+            for a in args:
+                if a.__class__ is torch.Tensor and a.get_device() != here:
+                    return body(*args, **kwargs)
+            for a in kwargs.values():
+                if a.__class__ is torch.Tensor and a.get_device() != here:
+                    return body(*args, **kwargs)
+            return fn(*args, **kwargs)
         dev = _cuda_device_of(args, kwargs)
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=dev)
@@ -264,6 +280,13 @@ def _on_stream(fn):
             return body(*args, **kwargs)
 
     return wrapper
+
+
+def _want(t, name, dtype, shape):
+    """_need for one dtype and a known shape: the checks alone where they pass."""
+    if not (t.__class__ is _torch().Tensor and t.dtype == dtype and t.shape == shape and t.is_cuda
+            and t.is_contiguous()):
+        _need(t, name, (dtype,), shape=shape)
 
 
 def gemv_rows(m: int) -> int:
@@ -1013,24 +1036,24 @@ def cr_rmsnorm_quant_act(x, gamma, eps: float = 1e-6, residual=None, mp: Optiona
     code = _gamma(gamma, K)
     MP = M if mp is None else int(mp)
     if residual is not None:
-        _need(residual, "residual", (torch.bfloat16,), shape=(M, K))
+        _want(residual, "residual", torch.bfloat16, (M, K))
         if h is None:
             h = torch.empty_like(x)
-        _need(h, "h", (torch.bfloat16,), shape=(M, K))
+        _want(h, "h", torch.bfloat16, (M, K))
     elif h is not None and h is not x:
         raise ValueError("h is an output of the residual's addition: without a residual it is x")
     if xq is None:
         xq = torch.empty(MP, K, dtype=torch.int8, device=x.device)
     else:
-        _need(xq, "xq", (torch.int8,), shape=(MP, K))
+        _want(xq, "xq", torch.int8, (MP, K))
     if xs is None:
         xs = torch.empty(MP, dtype=torch.float32, device=x.device)
     else:
-        _need(xs, "xs", (torch.float32,), shape=(MP,))
+        _want(xs, "xs", torch.float32, (MP,))
     if rs is None:
         rs = torch.empty(M, dtype=torch.float32, device=x.device)
     else:
-        _need(rs, "rs", (torch.float32,), shape=(M,))
+        _want(rs, "rs", torch.float32, (M,))
     _check(lib().cr_rmsnorm_quant_act(_ptr(x), _ptr(residual), _ptr(gamma), code, float(eps), M, K, MP, int(act_qmax),
                                       _ptr(h) if residual is not None else None, _ptr(xq), _ptr(xs), _ptr(rs),
                                       _stream(None)), "cr_rmsnorm_quant_act")
@@ -1048,20 +1071,20 @@ def cr_rmsnorm_backward(dr, h, gamma, rs, dres=None, dx=None, dgamma=None, work=
     torch = _torch()
     _need(dr, "dr", (torch.bfloat16,), 2)
     M, K = dr.shape
-    _need(h, "h", (torch.bfloat16,), shape=(M, K))
+    _want(h, "h", torch.bfloat16, (M, K))
     code = _gamma(gamma, K)
-    _need(rs, "rs", (torch.float32,), shape=(M,))
+    _want(rs, "rs", torch.float32, (M,))
     if dres is not None:
-        _need(dres, "dres", (torch.bfloat16,), shape=(M, K))
+        _want(dres, "dres", torch.bfloat16, (M, K))
     if dx is None:
         dx = torch.empty(M, K, dtype=torch.bfloat16, device=dr.device)
     else:
-        _need(dx, "dx", (torch.bfloat16,), shape=(M, K))
+        _want(dx, "dx", torch.bfloat16, (M, K))
     if with_dgamma:
         if dgamma is None:
             dgamma = torch.empty(K, dtype=torch.float32, device=dr.device)
         else:
-            _need(dgamma, "dgamma", (torch.float32,), shape=(K,))
+            _want(dgamma, "dgamma", torch.float32, (K,))
         work = _work_buffer(work, lib().cr_rmsnorm_backward_work_bytes(M, K), dr.device)
     elif dgamma is not None:
         raise ValueError("dgamma given with with_dgamma=False")
@@ -1094,7 +1117,7 @@ def cr_rotate(x, out=None):
     if out is None:
         out = torch.empty_like(x)
     else:
-        _need(out, "out", (torch.bfloat16,), shape=x.shape)
+        _want(out, "out", torch.bfloat16, x.shape)
     _check(lib().cr_rotate(_ptr(x), x.shape[0], x.shape[1], _ptr(out), _stream(None)), "cr_rotate")
     return out
 
@@ -1126,11 +1149,11 @@ def cr_w4a8_swiglu_backward(dout, xq, xs, qdata, srel, codebook, s_channel, bias
     if dx is None:
         dx = torch.empty(M, K, dtype=torch.bfloat16, device=dout.device)
     else:
-        _need(dx, "dx", (torch.bfloat16,), shape=(M, K))
+        _want(dx, "dx", torch.bfloat16, (M, K))
     if dz is None:
         dz = torch.empty(M, N, dtype=torch.bfloat16, device=dout.device)
     else:
-        _need(dz, "dz", (torch.bfloat16,), shape=(M, N))
+        _want(dz, "dz", torch.bfloat16, (M, N))
     work = _work_buffer(work, lib().cr_w4a8_swiglu_backward_work_bytes(M, N, K), dout.device)
     _check(lib().cr_w4a8_swiglu_backward(_ptr(dout), _ptr(xq), _ptr(xs), _ptr(qdata), _ptr(srel), _ptr(codebook),
                                          _ptr(s_channel), _ptr(bias), M, N, K, _ptr(dx), _ptr(dz), _ptr(work),
@@ -1153,11 +1176,11 @@ def cr_w4a8_cross_entropy(xq, xs, qdata, srel, codebook, s_channel, targets, bia
     if loss is None:
         loss = torch.empty(M, dtype=torch.float32, device=xq.device)
     else:
-        _need(loss, "loss", (torch.float32,), shape=(M,))
+        _want(loss, "loss", torch.float32, (M,))
     if lse is None:
         lse = torch.empty(M, dtype=torch.float32, device=xq.device)
     else:
-        _need(lse, "lse", (torch.float32,), shape=(M,))
+        _want(lse, "lse", torch.float32, (M,))
     work = _work_buffer(work, lib().cr_w4a8_cross_entropy_work_bytes(M, V, K), xq.device)
     _check(lib().cr_w4a8_cross_entropy(_ptr(xq), _ptr(xs), _ptr(qdata), _ptr(srel), _ptr(codebook), _ptr(s_channel),
                                        _ptr(bias), _ptr(targets), int(ignore_index), M, V, K, _ptr(loss), _ptr(lse),
@@ -1177,12 +1200,12 @@ def cr_w4a8_cross_entropy_backward(xq, xs, qdata, srel, codebook, s_channel, tar
     _need(targets, "targets", (torch.int64,), 1)
     M = targets.shape[0]
     _activations(xq, xs, M, K)
-    _need(lse, "lse", (torch.float32,), shape=(M,))
-    _need(dloss, "dloss", (torch.float32,), shape=(M,))
+    _want(lse, "lse", torch.float32, (M,))
+    _want(dloss, "dloss", torch.float32, (M,))
     if dx is None:
         dx = torch.empty(M, K, dtype=torch.bfloat16, device=xq.device)
     else:
-        _need(dx, "dx", (torch.bfloat16,), shape=(M, K))
+        _want(dx, "dx", torch.bfloat16, (M, K))
     work = _work_buffer(work, lib().cr_w4a8_cross_entropy_backward_work_bytes(M, V, K), xq.device)
     _check(lib().cr_w4a8_cross_entropy_backward(_ptr(xq), _ptr(xs), _ptr(qdata), _ptr(srel), _ptr(codebook),
                                                 _ptr(s_channel), _ptr(bias), _ptr(targets), int(ignore_index),

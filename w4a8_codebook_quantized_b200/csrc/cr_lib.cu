@@ -1223,7 +1223,7 @@ cr_status cr_rotate(const uint16_t *x, int64_t M, int64_t K, uint16_t *out, cr_s
     const cr_status ds = current_device(&d);
     if (ds != CR_OK)
         return ds;
-    return launched(cr::nm::launch_rotate(x, M, K, out, d->num_sms, stream));
+    return launched(cr::nm::launch_rotate(x, M, K, out, stream));
 }
 
 // ---------------------------------------------------------------- gated layer's gradient, cross entropy

@@ -23,6 +23,9 @@
 // (4 with a residual) and 1 (3) out, the backward's 6 (8), the rotation's 4.
 #pragma once
 
+#include <climits>
+#include <initializer_list>
+
 #include "cr_device.cuh"
 #include "k_rotquant.cuh"
 
@@ -33,18 +36,45 @@ namespace nm {
 
 // Sixteen consecutive bf16 values as eight words (element 2i in the low half
 // of word i).  Plain loads: the rows may be written earlier by this kernel.
-__device__ __forceinline__ void load16(const uint16_t *p, uint32_t (&w)[8])
+// wide: every row starts on a 32-byte boundary, and one 256-bit access takes
+// them: a warp's 32 lanes then cover whole lines, where two 128-bit accesses at
+// a stride of 32 bytes each touch every line of the span (measured, 16384 x
+// 8192 forward: 192 -> 168 us).
+__device__ __forceinline__ void load16(const uint16_t *p, bool wide, uint32_t (&w)[8])
 {
+    if (wide) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p)
+                     : "memory");
+        return;
+    }
     const uint4 a = *reinterpret_cast<const uint4 *>(p);
     const uint4 b = *reinterpret_cast<const uint4 *>(p + 8);
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
     w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
 }
 
-__device__ __forceinline__ void store16(uint16_t *p, const uint32_t (&w)[8])
+__device__ __forceinline__ void store16(uint16_t *p, bool wide, const uint32_t (&w)[8])
 {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+        return;
+    }
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4 *>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// Whether every given pointer starts on a 32-byte boundary (rows are multiples
+// of 512 bytes; a null pointer counts as aligned).
+inline bool all_wide(std::initializer_list<const void *> ps)
+{
+    uintptr_t bits = 0;
+    for (const void *p : ps)
+        bits |= reinterpret_cast<uintptr_t>(p);
+    return (bits & 31) == 0;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -87,27 +117,27 @@ __device__ __forceinline__ double squares16(const uint32_t (&w)[8])
 }
 
 // rs of the row, from every thread's share of the sum of squares: the warps'
-// sums in shared memory, then one thread adds them and takes the root (the
-// fp64 division and root are some hundred instructions: one warp spends them).
+// sums in shared memory, then every thread adds them in the same order and
+// takes the root (some twenty fp64 instructions a warp; one warp doing it for
+// all costs a second barrier).
 template <int THREADS>
-__device__ __forceinline__ float row_rs(double ss, int64_t K, double eps, double *warp_ss, float *rs_out)
+__device__ __forceinline__ float row_rs(double ss, double inv_k, double eps, double *warp_ss)
 {
-    const int tid = threadIdx.x;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1)
         ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-    if ((tid & 31) == 0)
-        warp_ss[tid >> 5] = ss;
+    if ((threadIdx.x & 31) == 0)
+        warp_ss[threadIdx.x >> 5] = ss;
     __syncthreads();
-    if (tid == 0) {
-        double t = warp_ss[0];
+    double t[THREADS / 32];
 #pragma unroll
-        for (int w = 1; w < THREADS / 32; ++w)
-            t += warp_ss[w];
-        *rs_out = (float)(1.0 / sqrt(t / (double)K + eps));
-    }
-    __syncthreads();
-    return *rs_out;
+    for (int w = 0; w < THREADS / 32; ++w)
+        t[w] = warp_ss[w];
+    double sum = t[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 32; ++w)
+        sum += t[w];
+    return (float)rsqrt(fma(sum, inv_k, eps));
 }
 
 // Sixteen consecutive weights as fp32 (GBF16: stored as bf16).
@@ -132,6 +162,22 @@ __device__ __forceinline__ void load_gamma16(const void *gamma, int64_t k, float
         }
     }
 }
+
+// The same as eight fp32 pairs.
+template <bool GBF16>
+__device__ __forceinline__ void load_gamma_pairs(const void *gamma, int64_t k, uint64_t (&g)[8])
+{
+    float f[16];
+    load_gamma16<GBF16>(gamma, k, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        g[i] = rq::pk(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]));
+}
+
+// Both bf16 values of a word as an fp32 pair.
+__device__ __forceinline__ uint64_t pair_of(uint32_t w) { return rq::pk(w << 16, w & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint64_t pair_both(float v) { return rq::pk(__float_as_uint(v), __float_as_uint(v)); }
 
 // The maximum over the CTA of a non-negative, NaN-free value.
 template <int THREADS>
@@ -166,9 +212,10 @@ struct RowScale {
 struct FwdArgs {
     const uint16_t *x, *res;
     const void *gamma;
-    double eps;
+    double eps, inv_k;
     int64_t M, K;
     int qmax;
+    bool wide;      // x, res and h on 32-byte boundaries
     uint16_t *h;
     int8_t *xq;
     float *xs, *rs;
@@ -201,7 +248,6 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_rows_kernel(const FwdArgs a)
     __shared__ __align__(16) uint8_t tb_all[kHalfWarps][272];
     __shared__ double warp_ss[THREADS / 32];
     __shared__ float warp_max[THREADS / 32];
-    __shared__ float rs_sh;
 
     asm volatile("griddepcontrol.launch_dependents;" :::);
     if (threadIdx.x == 0 && (int64_t)blockIdx.x < a.M) {
@@ -229,12 +275,12 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_rows_kernel(const FwdArgs a)
     uint32_t w[kHeld][8];
     double ss = 0.0;
     auto load_h = [&](int b, uint32_t (&wj)[8]) {
-        load16(xrow + 256 * b + 16 * L, wj);
+        load16(xrow + 256 * b + 16 * L, a.wide, wj);
         if (rrow != nullptr) {
             uint32_t r[8];
-            load16(rrow + 256 * b + 16 * L, r);
+            load16(rrow + 256 * b + 16 * L, a.wide, r);
             add16(wj, r);
-            store16(hrow + 256 * b + 16 * L, wj);
+            store16(hrow + 256 * b + 16 * L, a.wide, wj);
         }
         ss += squares16(wj);
     };
@@ -247,7 +293,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_rows_kernel(const FwdArgs a)
         for (int b = hw; b < NB; b += kHalfWarps)
             load_h(b, w[0]);
     }
-    const float rs = row_rs<THREADS>(ss, a.K, a.eps, warp_ss, &rs_sh);
+    const float rs = row_rs<THREADS>(ss, a.inv_k, a.eps, warp_ss);
 
     float v[kHeld][16];
     auto rotate = [&](int b, const uint32_t (&wj)[8], float (&vj)[16]) {
@@ -271,7 +317,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_rows_kernel(const FwdArgs a)
             }
     } else {
         for (int b = hw; b < NB; b += kHalfWarps) {
-            load16(again + 256 * b + 16 * L, w[0]);
+            load16(again + 256 * b + 16 * L, a.wide, w[0]);
             rotate(b, w[0], v[0]);
             amax = fmaxf(amax, rq::max_abs16(v[0]));
         }
@@ -285,7 +331,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_rows_kernel(const FwdArgs a)
                                    qrow + 256 * (hw + kHalfWarps * j));
     } else {
         for (int b = hw; b < NB; b += kHalfWarps) {
-            load16(again + 256 * b + 16 * L, w[0]);
+            load16(again + 256 * b + 16 * L, a.wide, w[0]);
             rotate(b, w[0], v[0]);
             rq::quantise_store(v[0], s.scale, s.inv16, a.qmax, s.exact_row, L, tb, hmask, qrow + 256 * b);
         }
@@ -310,7 +356,6 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_pairs_kernel(const FwdArgs a)
     extern __shared__ __align__(16) uint64_t nm_smem[];
     __shared__ double warp_ss[THREADS / 32];
     __shared__ float warp_max[THREADS / 32];
-    __shared__ float rs_sh;
 
     asm volatile("griddepcontrol.launch_dependents;" :::);
     if (threadIdx.x == 0 && (int64_t)blockIdx.x < a.M) {
@@ -341,22 +386,22 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_pairs_kernel(const FwdArgs a)
     auto load_h = [&](int p, uint32_t (&u0)[8], uint32_t (&u1)[8]) {
         const int64_t k0 = 512 * (int64_t)p + 16 * L;
         const bool two = 2 * p + 1 < NB;
-        load16(xrow + k0, u0);
+        load16(xrow + k0, a.wide, u0);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             u1[i] = 0u;
         if (two)
-            load16(xrow + k0 + 256, u1);
+            load16(xrow + k0 + 256, a.wide, u1);
         if (rrow != nullptr) {
             uint32_t r0[8], r1[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-            load16(rrow + k0, r0);
+            load16(rrow + k0, a.wide, r0);
             if (two)
-                load16(rrow + k0 + 256, r1);
+                load16(rrow + k0 + 256, a.wide, r1);
             add16(u0, r0);
             add16(u1, r1);
-            store16(hrow + k0, u0);
+            store16(hrow + k0, a.wide, u0);
             if (two)
-                store16(hrow + k0 + 256, u1);
+                store16(hrow + k0 + 256, a.wide, u1);
         }
         ss += squares16(u0);
         if (two)
@@ -371,7 +416,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_pairs_kernel(const FwdArgs a)
         for (int p = hw; p < NP; p += kHalfWarps)
             load_h(p, w0[0], w1[0]);
     }
-    const float rs = row_rs<THREADS>(ss, a.K, a.eps, warp_ss, &rs_sh);
+    const float rs = row_rs<THREADS>(ss, a.inv_k, a.eps, warp_ss);
     const uint64_t rs2 = rq::pk(__float_as_uint(rs), __float_as_uint(rs));
 
     uint64_t v[kHeld][16];
@@ -398,9 +443,9 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_pairs_kernel(const FwdArgs a)
     };
     auto reload = [&](int p) {  // this thread's values of h again
         const uint16_t *src = (rrow != nullptr ? hrow : xrow) + 512 * (int64_t)p + 16 * L;
-        load16(src, w0[0]);
+        load16(src, a.wide, w0[0]);
         if (2 * p + 1 < NB)
-            load16(src + 256, w1[0]);
+            load16(src + 256, a.wide, w1[0]);
         else
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -523,73 +568,141 @@ inline cudaError_t launch_fwd_t(const FwdArgs &a, int64_t MP, cudaStream_t strea
 // Short batches take the scalar form, 512 threads for K >= 8192 and 256 below;
 // longer ones the packed form with one half-warp per block pair where that fits
 // in 512 threads (K <= 16384), and the re-reading form beyond.
-inline cudaError_t launch_fwd(const FwdArgs &a, int64_t MP, bool gamma_bf16, cudaStream_t stream)
+inline cudaError_t launch_fwd(FwdArgs a, int64_t MP, bool gamma_bf16, cudaStream_t stream)
 {
+    a.inv_k = 1.0 / (double)a.K;
+    a.wide = all_wide({a.x, a.res, a.h});
     return gamma_bf16 ? launch_fwd_t<true>(a, MP, stream) : launch_fwd_t<false>(a, MP, stream);
 }
 
 // ---------------------------------------------------------------- the rotation back in row order
 
-// Rotate one block held in row order (v[b] = element 16L + b) and return it in
-// row order, scaled: v[b] = rotated element 16L + b.  A second transpose
-// through `tr` after rotate_regs: column L goes out as 16 scalar stores, row L
-// comes back as four 16-byte loads; chunk c of row a lives at chunk position
-// c ^ ((a >> 1) & 3), as in rotate_regs.
-__device__ __forceinline__ void rotate_rows(int L, float *tr, unsigned hmask, float (&v)[16])
+// Rotate one block held in row order, v[i] = elements 16L + 2i (low half) and
+// 16L + 2i + 1, and return 16 times the result in row order.  The digits whose
+// stride is a multiple of 4 places work on both elements of a pair at once.
+// Two transposes through `tr`: chunk c of row a lives at chunk position
+// c ^ ((a >> 1) & 3), which makes the 16-byte and the scalar side conflict-free.
+__device__ __forceinline__ void rotate_rows16(int L, float *tr, unsigned hmask, uint64_t (&v)[8])
 {
-    rq::rotate_regs(L, tr, hmask, v);
+    auto digits = [](uint64_t (&u)[8]) {  // stride 1, then stride 4, of the places 0..15
 #pragma unroll
-    for (int a = 0; a < 16; ++a)
-        tr[16 * a + 4 * ((L >> 2) ^ ((a >> 1) & 3)) + (L & 3)] = __fmul_rn(v[a], 0.0625f);
-    __syncwarp(hmask);
-    const float4 *rowp = reinterpret_cast<const float4 *>(tr + 16 * L);
+        for (int q = 0; q < 4; ++q) {
+            uint32_t a0, a1, a2, a3;
+            rq::unpk(u[2 * q], a0, a1);
+            rq::unpk(u[2 * q + 1], a2, a3);
+            float f0 = __uint_as_float(a0), f1 = __uint_as_float(a1), f2 = __uint_as_float(a2),
+                  f3 = __uint_as_float(a3);
+            rq::h4_quad(f0, f1, f2, f3);
+            u[2 * q] = rq::pk(__float_as_uint(f0), __float_as_uint(f1));
+            u[2 * q + 1] = rq::pk(__float_as_uint(f2), __float_as_uint(f3));
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            rq::h4_quad2(u[q], u[q + 2], u[q + 4], u[q + 6]);
+    };
+    digits(v);
+    uint4 *rowp = reinterpret_cast<uint4 *>(tr + 16 * L);
     const int sw = (L >> 1) & 3;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        const float4 t = rowp[c ^ sw];
-        v[4 * c] = t.x, v[4 * c + 1] = t.y, v[4 * c + 2] = t.z, v[4 * c + 3] = t.w;
+        uint32_t a0, a1, b0, b1;
+        rq::unpk(v[2 * c], a0, a1);
+        rq::unpk(v[2 * c + 1], b0, b1);
+        rowp[c ^ sw] = make_uint4(a0, a1, b0, b1);
+    }
+    __syncwarp(hmask);
+    uint32_t *col[4];  // this lane's column in rows whose (a >> 1) & 3 is k
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        col[k] = reinterpret_cast<uint32_t *>(tr) + 4 * ((L >> 2) ^ k) + (L & 3);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = rq::pk(col[i & 3][32 * i], col[i & 3][32 * i + 16]);
+    digits(v);
+    // a lane's column is its own: it goes back to the places it came from
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t lo, hi;
+        rq::unpk(v[i], lo, hi);
+        col[i & 3][32 * i] = lo;
+        col[i & 3][32 * i + 16] = hi;
+    }
+    __syncwarp(hmask);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint4 t = rowp[c ^ sw];
+        v[2 * c] = rq::pk(t.x, t.y);
+        v[2 * c + 1] = rq::pk(t.z, t.w);
     }
     __syncwarp(hmask);
 }
 
+// out = bf16(x rotated): a half-warp per pair of blocks, counted over all rows
+// (the loop is for more than fit one grid), in the packed arithmetic of the
+// many-row forward.  On the way back the two blocks' values of a place share a
+// word, so that transpose moves half the bytes of an fp32 one; the row's words
+// are then taken apart by byte permutes.  out may be x: a block is read and
+// written by the same half-warp.
 constexpr int kRotThreads = 256;
 
-// out = bf16(x rotated): a half-warp per block, grid-stride over all blocks of
-// all rows.  out may be x: a block is read and written by the same half-warp.
-__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const uint16_t *x, int64_t blocks, uint16_t *out)
+__global__ void __launch_bounds__(kRotThreads, 4) rotate_kernel(const uint16_t *x, int64_t blocks, uint16_t *out,
+                                                               bool wide)
 {
-    __shared__ __align__(16) float tr_all[kRotThreads / 16][16 * 16 + 16];
+    __shared__ __align__(16) uint64_t tr_all[kRotThreads / 16][16 * 16];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int hw = threadIdx.x >> 4, L = threadIdx.x & 15;
     const unsigned hmask = 0xFFFFu << (16 * (hw & 1));
-    float *tr = tr_all[hw];
-    for (int64_t b = (int64_t)blockIdx.x * (kRotThreads / 16) + hw; b < blocks;
-         b += (int64_t)gridDim.x * (kRotThreads / 16)) {
-        uint32_t w[8];
-        load16(x + 256 * b + 16 * L, w);
-        float v[16];
+    uint64_t *tr = tr_all[hw];
+    // 64 bytes in for the odd half-warp: the word stores of a warp's two halves
+    // fall in different banks
+    uint32_t *tw = reinterpret_cast<uint32_t *>(tr) + 16 * (hw & 1);
+    for (int64_t p = (int64_t)blockIdx.x * (kRotThreads / 16) + hw; 2 * p < blocks;
+         p += (int64_t)gridDim.x * (kRotThreads / 16)) {
+        const bool two = 2 * p + 1 < blocks;
+        uint32_t w0[8], w1[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        load16(x + 512 * p + 16 * L, wide, w0);
+        if (two)
+            load16(x + 512 * p + 256 + 16 * L, wide, w1);
+        uint64_t v[16];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[2 * i] = bf16_lo(w[i]);
-            v[2 * i + 1] = bf16_hi(w[i]);
+            v[2 * i] = rq::pk(w0[i] << 16, w1[i] << 16);
+            v[2 * i + 1] = rq::pk(w0[i] & 0xFFFF0000u, w1[i] & 0xFFFF0000u);
         }
-        rotate_rows(L, tr, hmask, v);
+        rq::rotate_pair_regs(L, tr, hmask, v);
+        // column L out: word (a, L) at chunk (L / 4) ^ ((a / 2) % 4) of row a
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w[i] = to_bf16x2_bits(v[2 * i], v[2 * i + 1]);
-        store16(out + 256 * b + 16 * L, w);
+        for (int a = 0; a < 16; ++a) {
+            uint32_t lo, hi;
+            rq::unpk(rq::mul2(v[a], 0x3D8000003D800000ull), lo, hi);  // times 1/16
+            tw[16 * a + 4 * ((L >> 2) ^ ((a >> 1) & 3)) + (L & 3)] =
+                to_bf16x2_bits(__uint_as_float(lo), __uint_as_float(hi));
+        }
+        __syncwarp(hmask);
+        const uint4 *rowp = reinterpret_cast<const uint4 *>(tw + 16 * L);
+        const int sw = (L >> 1) & 3;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint4 t = rowp[c ^ sw];
+            w0[2 * c] = prmt(t.x, t.y, 0x5410u);
+            w1[2 * c] = prmt(t.x, t.y, 0x7632u);
+            w0[2 * c + 1] = prmt(t.z, t.w, 0x5410u);
+            w1[2 * c + 1] = prmt(t.z, t.w, 0x7632u);
+        }
+        __syncwarp(hmask);
+        store16(out + 512 * p + 16 * L, wide, w0);
+        if (two)
+            store16(out + 512 * p + 256 + 16 * L, wide, w1);
     }
 }
 
-inline cudaError_t launch_rotate(const uint16_t *x, int64_t M, int64_t K, uint16_t *out, int num_sms,
-                                 cudaStream_t stream)
+inline cudaError_t launch_rotate(const uint16_t *x, int64_t M, int64_t K, uint16_t *out, cudaStream_t stream)
 {
     const int64_t blocks = M * (K / 256);
-    int64_t grid = (blocks + kRotThreads / 16 - 1) / (kRotThreads / 16);
-    const int64_t cap = 8 * (int64_t)num_sms;
-    if (grid > cap)
-        grid = cap;
-    return launch_dependent(rotate_kernel, grid, kRotThreads, 0, stream, x, blocks, out);
+    int64_t grid = (blocks + kRotThreads / 8 - 1) / (kRotThreads / 8);
+    if (grid > INT_MAX)
+        grid = INT_MAX;
+    return launch_dependent(rotate_kernel, grid, kRotThreads, 0, stream, x, blocks, out, all_wide({x, out}));
 }
 
 // ---------------------------------------------------------------- backward
@@ -608,6 +721,7 @@ struct BwdArgs {
     int64_t M, K;
     uint16_t *dx;
     float *part;  // [gridDim.x, K], or null: no dgamma
+    bool wide;    // dr, h, dres and dx on 32-byte boundaries
 };
 
 // Sum over the CTA; `slot` alternates between two rows of warp sums, so one
@@ -644,113 +758,164 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(const BwdArgs
     float *tr = tr_all[hw];
     float *prow = a.part != nullptr ? a.part + (int64_t)blockIdx.x * a.K : nullptr;
     constexpr int kHeld = kWide ? 1 : J;
-    float acc[kHeld][16];
+    uint64_t acc[kHeld][8];
 #pragma unroll
     for (int j = 0; j < kHeld; ++j)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            acc[j][i] = 0.0f;
+        for (int i = 0; i < 8; ++i)
+            acc[j][i] = 0ull;
 
-    // dv of one block, and h packed
-    auto load_dv = [&](int64_t row, int b, float (&dv)[16], uint32_t (&hw8)[8]) {
-        uint32_t w[8];
-        load16(a.dr + row + 256 * b + 16 * L, w);
-        load16(a.h + row + 256 * b + 16 * L, hw8);
+    // Packed pairs of neighbouring elements throughout.  V = 16 dv comes out of
+    // the rotation; the 1/16 (exact) sits in rs16 = rs / 16: with
+    //   g' = V * gamma,  xh' = h * rs16:  V * xh' = dv * xh,  g' * xh' = g * xh,
+    //   dx = g' * rs16 + (h * (-rs * rs * c) + dres).
+    auto rotated = [&](const uint32_t (&w)[8], uint64_t (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            dv[2 * i] = bf16_lo(w[i]);
-            dv[2 * i + 1] = bf16_hi(w[i]);
-        }
-        rotate_rows(L, tr, hmask, dv);
+        for (int i = 0; i < 8; ++i)
+            v[i] = pair_of(w[i]);
+        rotate_rows16(L, tr, hmask, v);
     };
-    auto finish = [&](int64_t row, int b, const float (&g)[16], const uint32_t (&hw8)[8], float rs, float c) {
-        uint32_t r[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u}, o[8];
-        if (a.dres != nullptr)
-            load16(a.dres + row + 256 * b + 16 * L, r);
+    auto finish = [&](int64_t at, const uint64_t (&g)[8], const uint32_t (&hp)[8], const uint32_t (&r)[8], float rs,
+                      float c) {
+        const uint64_t rs16 = pair_both(rs * 0.0625f), k = pair_both(-(rs * rs) * c);
+        uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float lo = rs * (g[2 * i] - bf16_lo(hw8[i]) * rs * c) + bf16_lo(r[i]);
-            const float hi = rs * (g[2 * i + 1] - bf16_hi(hw8[i]) * rs * c) + bf16_hi(r[i]);
-            o[i] = to_bf16x2_bits(lo, hi);
+            uint32_t lo, hi;
+            rq::unpk(rq::fma2(g[i], rs16, rq::fma2(pair_of(hp[i]), k, pair_of(r[i]))), lo, hi);
+            o[i] = to_bf16x2_bits(__uint_as_float(lo), __uint_as_float(hi));
         }
-        store16(a.dx + row + 256 * b + 16 * L, o);
+        store16(a.dx + at, a.wide, o);
+    };
+    auto sum_pair = [](uint64_t v) {
+        uint32_t lo, hi;
+        rq::unpk(v, lo, hi);
+        return __uint_as_float(lo) + __uint_as_float(hi);
     };
 
     int slot = 0;
-    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, slot ^= 1) {
-        const int64_t row = m * a.K;
-        const float rs = a.rs[m];
-        float s = 0.0f;
-        if constexpr (!kWide) {
-            float g[J][16];
-            uint32_t hp[J][8];
+    if constexpr (!kWide) {
+        // the next row's values are loaded while the current row is worked on
+        uint32_t nd[J][8], nh[J][8], nr[J][8];
+        float nrs = 0.0f;
+        auto fetch = [&](int64_t m) {
+            if (m >= a.M)
+                return;
+            nrs = a.rs[m];
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const int b = hw + kHalfWarps * j;
                 if (b < NB) {
-                    load_dv(row, b, g[j], hp[j]);
-                    float gm[16];
-                    load_gamma16<GBF16>(a.gamma, 256 * b + 16 * L, gm);
+                    const int64_t at = m * a.K + 256 * b + 16 * L;
+                    load16(a.dr + at, a.wide, nd[j]);
+                    load16(a.h + at, a.wide, nh[j]);
+                    if (a.dres != nullptr) {
+                        load16(a.dres + at, a.wide, nr[j]);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float xh = (i & 1 ? bf16_hi(hp[j][i >> 1]) : bf16_lo(hp[j][i >> 1])) * rs;
-                        acc[j][i] += g[j][i] * xh;
-                        g[j][i] *= gm[i];
-                        s += g[j][i] * xh;
+                        for (int i = 0; i < 8; ++i)
+                            nr[j][i] = 0u;
                     }
                 }
             }
-            const float c = block_sum<THREADS>(s, warp_sum, slot) * inv_k;
+        };
+        constexpr bool kAhead = J == 1;  // two blocks a half-warp leave no registers for it
+        if (kAhead)
+            fetch(blockIdx.x);
+        for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, slot ^= 1) {
+            if (!kAhead)
+                fetch(m);
+            const float rs = nrs;
+            const uint64_t rs16 = pair_both(rs * 0.0625f);
+            uint64_t s = 0ull, g[J][8];
+            uint32_t hp[J][8], r[J][8], d[J][8];
 #pragma unroll
             for (int j = 0; j < J; ++j)
-                if (hw + kHalfWarps * j < NB)
-                    finish(row, hw + kHalfWarps * j, g[j], hp[j], rs, c);
-        } else {
-            float g[16], gm[16];
-            uint32_t hp[8];
-            for (int b = hw; b < NB; b += kHalfWarps) {
-                load_dv(row, b, g, hp);
-                load_gamma16<GBF16>(a.gamma, 256 * b + 16 * L, gm);
-                float4 *pp = reinterpret_cast<float4 *>(prow + 256 * b + 16 * L);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float d[4];
+                for (int i = 0; i < 8; ++i) {
+                    d[j][i] = nd[j][i];
+                    hp[j][i] = nh[j][i];
+                    r[j][i] = nr[j][i];
+                }
+            if (kAhead)
+                fetch(m + gridDim.x);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int i = 4 * q + e;
-                        const float xh = (i & 1 ? bf16_hi(hp[i >> 1]) : bf16_lo(hp[i >> 1])) * rs;
-                        d[e] = g[i] * xh;
-                        s += g[i] * gm[i] * xh;
-                    }
-                    if (prow != nullptr) {
-                        float4 t = m == blockIdx.x ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : pp[q];
-                        t.x += d[0], t.y += d[1], t.z += d[2], t.w += d[3];
-                        pp[q] = t;
+            for (int j = 0; j < J; ++j) {
+                const int b = hw + kHalfWarps * j;
+                if (b < NB) {
+                    rotated(d[j], g[j]);
+                    uint64_t gm[8];
+                    load_gamma_pairs<GBF16>(a.gamma, 256 * b + 16 * L, gm);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint64_t xh = rq::mul2(pair_of(hp[j][i]), rs16);
+                        acc[j][i] = rq::fma2(g[j][i], xh, acc[j][i]);
+                        g[j][i] = rq::mul2(g[j][i], gm[i]);
+                        s = rq::fma2(g[j][i], xh, s);
                     }
                 }
             }
-            const float c = block_sum<THREADS>(s, warp_sum, slot) * inv_k;
-            for (int b = hw; b < NB; b += kHalfWarps) {
-                load_dv(row, b, g, hp);
-                load_gamma16<GBF16>(a.gamma, 256 * b + 16 * L, gm);
+            const float c = block_sum<THREADS>(sum_pair(s), warp_sum, slot) * inv_k;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    g[i] *= gm[i];
-                finish(row, b, g, hp, rs, c);
+            for (int j = 0; j < J; ++j) {
+                const int b = hw + kHalfWarps * j;
+                if (b < NB)
+                    finish(m * a.K + 256 * b + 16 * L, g[j], hp[j], r[j], rs, c);
             }
         }
-    }
-    if constexpr (!kWide) {
         if (prow != nullptr) {
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const int b = hw + kHalfWarps * j;
                 if (b < NB) {
-                    float4 *pp = reinterpret_cast<float4 *>(prow + 256 * b + 16 * L);
+                    ulonglong2 *pp = reinterpret_cast<ulonglong2 *>(prow + 256 * b + 16 * L);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        pp[q] = make_float4(acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]);
+                        pp[q] = make_ulonglong2(acc[j][2 * q], acc[j][2 * q + 1]);
                 }
+            }
+        }
+    } else {
+        for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, slot ^= 1) {
+            const float rs = a.rs[m];
+            const uint64_t rs16 = pair_both(rs * 0.0625f);
+            uint64_t s = 0ull, g[8], gm[8];
+            uint32_t hp[8], d[8];
+            for (int b = hw; b < NB; b += kHalfWarps) {
+                const int64_t at = m * a.K + 256 * b + 16 * L;
+                load16(a.dr + at, a.wide, d);
+                load16(a.h + at, a.wide, hp);
+                rotated(d, g);
+                load_gamma_pairs<GBF16>(a.gamma, 256 * b + 16 * L, gm);
+                ulonglong2 *pp = reinterpret_cast<ulonglong2 *>(prow + 256 * b + 16 * L);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint64_t xh[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        xh[e] = rq::mul2(pair_of(hp[2 * q + e]), rs16);
+                        s = rq::fma2(rq::mul2(g[2 * q + e], gm[2 * q + e]), xh[e], s);
+                    }
+                    if (prow != nullptr) {
+                        const ulonglong2 t = m == blockIdx.x ? make_ulonglong2(0ull, 0ull) : pp[q];
+                        pp[q] = make_ulonglong2(rq::fma2(g[2 * q], xh[0], t.x), rq::fma2(g[2 * q + 1], xh[1], t.y));
+                    }
+                }
+            }
+            const float c = block_sum<THREADS>(sum_pair(s), warp_sum, slot) * inv_k;
+            for (int b = hw; b < NB; b += kHalfWarps) {
+                const int64_t at = m * a.K + 256 * b + 16 * L;
+                uint32_t r[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                load16(a.dr + at, a.wide, d);
+                load16(a.h + at, a.wide, hp);
+                if (a.dres != nullptr)
+                    load16(a.dres + at, a.wide, r);
+                rotated(d, g);
+                load_gamma_pairs<GBF16>(a.gamma, 256 * b + 16 * L, gm);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    g[i] = rq::mul2(g[i], gm[i]);
+                finish(at, g, hp, r, rs, c);
             }
         }
     }
@@ -810,8 +975,9 @@ inline cudaError_t launch_bwd_t(const BwdArgs &a, float *dgamma, cudaStream_t st
     return launch_dependent(dgamma_kernel, a.K / 32, 256, 0, stream, (const float *)a.part, (int)P, a.K, dgamma);
 }
 
-inline cudaError_t launch_bwd(const BwdArgs &a, bool gamma_bf16, float *dgamma, cudaStream_t stream)
+inline cudaError_t launch_bwd(BwdArgs a, bool gamma_bf16, float *dgamma, cudaStream_t stream)
 {
+    a.wide = all_wide({a.dr, a.h, a.dres, a.dx});
     return gamma_bf16 ? launch_bwd_t<true>(a, dgamma, stream) : launch_bwd_t<false>(a, dgamma, stream);
 }
 
