@@ -578,6 +578,22 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr)
     return d;
 }
 
+// Shared-memory matrix descriptor for an MN-major operand tile of 16-bit
+// elements in the 128-byte-swizzled canonical layout: rows of 64 consecutive
+// MN elements (128 bytes), one row per K index, 8-row atoms of 1024 bytes
+// stacked along K (stride-dimension byte offset 1024), the next 64 MN elements
+// `mn_stride` bytes on (leading-dimension byte offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t mn_stride)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(mn_stride >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
 // Instruction descriptor for kind::i8: s32 accumulator, signed A and B, both
 // K-major, shape M x N.
 __host__ __device__ constexpr uint32_t idesc_i8(int M, int N)
@@ -590,13 +606,15 @@ __host__ __device__ constexpr uint32_t idesc_i8(int M, int N)
 }
 
 // Instruction descriptor for kind::f16 with bf16 A and B and an fp32
-// accumulator, both operands K-major: D format 1 (f32) in bits 4-5, A and B
-// format 1 (bf16) in bits 7-9 and 10-12, N / 8 in bits 17-22, M / 16 in 24-28.
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N)
+// accumulator: D format 1 (f32) in bits 4-5, A and B format 1 (bf16) in bits
+// 7-9 and 10-12, N / 8 in bits 17-22, M / 16 in 24-28; A is K-major, B K-major
+// or (bit 16) MN-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major = false)
 {
     return (1u << 4)                        // D format: f32
            | (1u << 7)                      // A: bf16
            | (1u << 10)                     // B: bf16
+           | ((b_mn_major ? 1u : 0u) << 16)
            | ((uint32_t)(N >> 3) << 17)     // N / 8
            | ((uint32_t)(M >> 4) << 24);    // M / 16
 }

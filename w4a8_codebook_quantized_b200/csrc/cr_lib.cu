@@ -456,8 +456,8 @@ cr_status side_stream(DeviceState &d)
     return CR_OK;
 }
 
-// A tcgen05 GEMM over A [M, K] and B [N, K] (both int8 or both bf16, by
-// MODE), `to` the output's tensor map (any map when nothing leaves through it):
+// A tcgen05 GEMM over A [M, K] and B [N, K], or [K, N] (both int8 or both
+// bf16, by MODE), `to` the output's tensor map (any map when nothing leaves through it):
 // CTA pairs (256 x 256 tiles) when there is at least one tile per SM pair,
 // otherwise one CTA per 128 x 256 tile.
 struct GemmEpilogue {
@@ -465,6 +465,7 @@ struct GemmEpilogue {
     int out_f32 = 0, swiglu = 0, tma_out = 1;
     void *out = nullptr;
     int32_t *acc_out = nullptr;
+    int64_t b_rows = 0;  // rows that a B given as [K, N] has, where K counts padding of A past them (0: K)
     cr::gm::EpiArgs ex;
 };
 
@@ -491,7 +492,9 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
     const int splits = gm::is_bf16(MODE) ? e.ex.splits : 1;
     const bool use_pair = splits > 1 ? M > gm::BM : pair_tiles >= d.num_sms / 2;
     CUtensorMap ta, tb;
-    if (!map(&ta, A, M, (uint32_t)gm::BM) || !map(&tb, B, N, use_pair ? 128u : (uint32_t)gm::BN))
+    if (!map(&ta, A, M, (uint32_t)gm::BM) ||
+        !(gm::b_is_kn(MODE) ? make_tmap_bf16(&tb, B, (uint64_t)N, (uint64_t)(e.b_rows ? e.b_rows : K), 64u, 64u)
+                            : map(&tb, B, N, use_pair ? 128u : (uint32_t)gm::BN)))
         return CR_ERR_CUDA;
     const CUtensorMap &tm_out = to ? *to : ta;  // placeholder when the output does not go through TMA
     if (use_pair) {
@@ -1015,8 +1018,8 @@ cr_status cr_w4a8_dequant_t_bf16(const uint8_t *qdata, const uint8_t *srel, cons
     st = current_device(&d);
     if (st != CR_OK)
         return st;
-    return launched(cr::ew::launch_dequant_t_bf16(qdata, srel, codebook, s_channel, (int)N, (int)K, (int)N, wt,
-                                                  d->num_sms, stream));
+    return launched(cr::ew::launch_dequant_t_bf16(qdata, srel, codebook, s_channel, (int)N, (int)K, wt, d->num_sms,
+                                                  stream));
 }
 
 namespace {
@@ -1057,8 +1060,7 @@ cr_status ste_backward_impl(const uint16_t *grad, const uint8_t *qdata, const ui
         cudaGetLastError();
         return CR_ERR_CUDA;
     }
-    st = launched(ew::launch_dequant_t_bf16(qdata, srel, codebook, s_channel, (int)N, (int)K, (int)N, wt, d->num_sms,
-                                            stream));
+    st = launched(ew::launch_dequant_t_bf16(qdata, srel, codebook, s_channel, (int)N, (int)K, wt, d->num_sms, stream));
     // dx [M, K] = grad [M, N] x wt [K, N]^T: the GEMM's rows are M, its columns K, its reduction N
     CUtensorMap to;
     if (st == CR_OK && !make_tmap_out(&to, dx, M, K, false))
@@ -1231,14 +1233,15 @@ cr_status cr_rotate(const uint16_t *x, int64_t M, int64_t K, uint16_t *out, cr_s
 namespace {
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-// A work buffer handed out in 256-byte aligned parts.
+// A work buffer handed out in 256-byte aligned parts; 256 bytes of its size
+// are for a buffer that is itself aligned to 16 bytes only.
 struct Parts {
-    uint8_t *base;
-    int64_t used = 0;
-    explicit Parts(void *p) : base(static_cast<uint8_t *>(p)) {}
+    uintptr_t base;
+    int64_t used = 256;
+    explicit Parts(void *p) : base((reinterpret_cast<uintptr_t>(p) + 255) / 256 * 256) {}
     void *take(int64_t bytes)
     {
-        void *p = base ? base + used : nullptr;
+        void *p = reinterpret_cast<void *>(base + (uintptr_t)(used - 256));
         used += round_up(bytes, 256);
         return p;
     }
@@ -1267,15 +1270,15 @@ struct SplitPlan {
 
 struct SwigluWork {
     int8_t *w8;
-    uint16_t *wt;
-    float *acc;  // the split reduction's copies (null: not split)
+    uint16_t *w;  // the gradient's bf16 weight
+    float *acc;   // the split reduction's copies (null: not split)
     SplitPlan split;
     int64_t bytes;
     SwigluWork(void *work, int64_t M, int64_t N, int64_t K) : split(M, K, N)
     {
         Parts p(work);
         w8 = static_cast<int8_t *>(p.take(N * K));
-        wt = static_cast<uint16_t *>(p.take(2 * N * K));
+        w = static_cast<uint16_t *>(p.take(2 * N * K));
         acc = split.n > 1 ? static_cast<float *>(p.take(4 * split.n * split.rows * K)) : nullptr;
         bytes = p.used;
     }
@@ -1328,7 +1331,7 @@ struct CeFwdWork {
 struct CeBwdWork {
     int64_t rows, piece;
     int8_t *w8;
-    uint16_t *wt, *dl;
+    uint16_t *w, *dl;
     float *acc;  // fp32 sums over the pieces, per range of a split reduction (null: one piece, not split)
     SplitPlan split;
     int64_t bytes;
@@ -1339,7 +1342,7 @@ struct CeBwdWork {
         Parts p(work);
         const int64_t most = piece < V ? piece : round_up(V, 8);
         w8 = static_cast<int8_t *>(p.take(most * K));
-        wt = static_cast<uint16_t *>(p.take(2 * most * K));
+        w = static_cast<uint16_t *>(p.take(2 * most * K));
         dl = static_cast<uint16_t *>(p.take(2 * most * rows));
         acc = piece < V || split.n > 1 ? static_cast<float *>(p.take(4 * split.n * split.rows * K)) : nullptr;
         bytes = p.used;
@@ -1415,7 +1418,7 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
     if (!make_tmap_out(&tz, dz, M, N, false, /*half=*/true) ||
         !(w.acc ? make_tmap_out(&tx, w.acc, w.split.n * w.split.rows, K, true) : make_tmap_out(&tx, dx, M, K, false)))
         return CR_ERR_CUDA;
-    st = launched(ew::launch_decode(qdata, srel, codebook, N, K, w.w8, d->num_sms, stream));
+    st = launched(ew::launch_decode_both(qdata, srel, codebook, s_channel, N, K, w.w8, w.w, d->num_sms, stream));
     if (st != CR_OK)
         return st;
     GemmEpilogue e;
@@ -1426,15 +1429,11 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
     st = launch_gemm<gm::kSwigluGrad>(*d, xq, w.w8, &tz, M, N, K, e, stream);
     if (st != CR_OK)
         return st;
-    st = launched(ew::launch_dequant_t_bf16(qdata, srel, codebook, s_channel, (int)N, (int)K, (int)N, w.wt, d->num_sms,
-                                            stream));
-    if (st != CR_OK)
-        return st;
     GemmEpilogue g;
     g.out_f32 = w.acc != nullptr;
     g.ex.splits = w.split.n;
     g.ex.split_rows = (int)w.split.rows;
-    st = launch_gemm<gm::kBf16>(*d, dz, w.wt, &tx, M, K, N, g, stream);
+    st = launch_gemm<gm::kBf16Nt>(*d, dz, w.w, &tx, M, K, N, g, stream);
     if (st == CR_OK && w.acc)
         st = launched(ce::launch_sum_to_bf16(w.acc, w.split.n, w.split.rows, M, K, dx, d->num_sms, stream));
     return st;
@@ -1531,7 +1530,7 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
         for (int64_t n0 = 0; n0 < V; n0 += w.piece) {
             const int64_t n = V - n0 < w.piece ? V - n0 : w.piece, np = round_up(n, 8);
             const uint8_t *q = qdata + n0 * (K / 2), *s = srel + n0 * (K / 16);
-            st = launched(ew::launch_decode(q, s, codebook, n, K, w.w8, d->num_sms, stream));
+            st = launched(ew::launch_decode_both(q, s, codebook, s_channel + n0, n, K, w.w8, w.w, d->num_sms, stream));
             if (st != CR_OK)
                 return st;
             // dl [rows, np]: the gradient of the piece's outputs
@@ -1552,12 +1551,9 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
             st = launch_gemm<gm::kCeGrad>(*d, xq + m0 * K, w.w8, &tl, rows, n, K, e, stream);
             if (st != CR_OK)
                 return st;
-            st = launched(ew::launch_dequant_t_bf16(q, s, codebook, s_channel + n0, (int)n, (int)K, (int)np, w.wt,
-                                                    d->num_sms, stream));
-            if (st != CR_OK)
-                return st;
             GemmEpilogue g;
             g.out_f32 = w.acc != nullptr;
+            g.b_rows = n;
             // a short last piece has fewer blocks of terms than ranges: every range keeps one
             g.ex.splits = (int)((np + 63) / 64 < w.split.n ? (np + 63) / 64 : w.split.n);
             g.ex.split_rows = (int)w.split.rows;
@@ -1565,8 +1561,8 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
             g.ex.ignore = ignore_index;
             g.ex.V = V;
             g.ex.dloss = dloss + m0;
-            st = w.acc && n0 > 0 ? launch_gemm<gm::kBf16RowsAdd>(*d, w.dl, w.wt, &tx, rows, K, np, g, stream)
-                                 : launch_gemm<gm::kBf16Rows>(*d, w.dl, w.wt, &tx, rows, K, np, g, stream);
+            st = w.acc && n0 > 0 ? launch_gemm<gm::kBf16RowsAdd>(*d, w.dl, w.w, &tx, rows, K, np, g, stream)
+                                 : launch_gemm<gm::kBf16Rows>(*d, w.dl, w.w, &tx, rows, K, np, g, stream);
             if (st != CR_OK)
                 return st;
         }

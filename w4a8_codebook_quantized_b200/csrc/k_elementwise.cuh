@@ -199,15 +199,14 @@ inline cudaError_t launch_interleave_rows(const void *src, void *dst, int64_t ro
 // the 16 bf16 pairs (row 2p, row 2p + 1) of those columns into a shared tile
 // of 4-byte pairs [128 k][36] (lanes on consecutive pairs: no bank
 // conflicts); the tile then leaves as 128 rows of 64 bf16 (16-byte stores, 8
-// lanes per 128-byte row).  wt has NP columns, NP a multiple of 8, N <= NP;
-// columns N .. NP - 1 are zeros.  K must be a multiple of 128.
+// lanes per 128-byte row).  N must be a multiple of 8 and K of 128.
 constexpr int kTN = 64, kTK = 128, kTPairs = 36;  // 32 row pairs + 4 of padding (16-byte aligned rows)
 
 __global__ void __launch_bounds__(kThreads) dequant_t_bf16_kernel(const uint8_t *__restrict__ qdata,
                                                                   const uint8_t *__restrict__ srel,
                                                                   const float *__restrict__ codebook,
                                                                   const float *__restrict__ s_channel, int N, int K,
-                                                                  int NP, uint16_t *__restrict__ wt)
+                                                                  uint16_t *__restrict__ wt)
 {
     __shared__ __align__(16) uint32_t tile[kTK][kTPairs];
     __shared__ uint4 lut[256];
@@ -217,7 +216,7 @@ __global__ void __launch_bounds__(kThreads) dequant_t_bf16_kernel(const uint8_t 
     __syncthreads();
     lut[threadIdx.x] = lut_entry(threadIdx.x, cb);  // kThreads == 256 scale bytes
     __syncthreads();
-    const int tiles_k = K / kTK, tiles_n = (NP + kTN - 1) / kTN;
+    const int tiles_k = K / kTK, tiles_n = (N + kTN - 1) / kTN;
     const int p = threadIdx.x & 31, g = threadIdx.x >> 5;
     // n fastest: CTAs running together write neighbouring 128-byte strips of
     // the same 128 rows of wt (whole rows between them), not one strip each
@@ -225,20 +224,15 @@ __global__ void __launch_bounds__(kThreads) dequant_t_bf16_kernel(const uint8_t 
     for (int t = blockIdx.x; t < tiles_k * tiles_n; t += gridDim.x) {
         const int tk = t / tiles_n, tn = t - tk * tiles_n;
         const int n0 = tn * kTN, k0 = tk * kTK, n = n0 + 2 * p;
-        if (n < NP) {
+        if (n < N) {  // N % 8 == 0: both rows of the pair exist
             const int kg = k0 / 16 + g;  // this thread's group
             uint32_t lo[4], hi[4];
             float sch[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                uint32_t *w = r ? hi : lo;
-                if (n + r >= N) {
-                    w[0] = w[1] = w[2] = w[3] = 0u;
-                    sch[r] = 0.0f;
-                    continue;
-                }
                 const uint2 c = *reinterpret_cast<const uint2 *>(qdata + (int64_t)(n + r) * (K / 2) + 8 * kg);
                 const uint4 T = lut[srel[(int64_t)(n + r) * (K / 16) + kg]];
+                uint32_t *w = r ? hi : lo;
                 decode8(c.x, T, w[0], w[1]);
                 decode8(c.y, T, w[2], w[3]);
                 sch[r] = __bfloat162float(__float2bfloat16_rn(s_channel[n + r]));
@@ -261,8 +255,8 @@ __global__ void __launch_bounds__(kThreads) dequant_t_bf16_kernel(const uint8_t 
         __syncthreads();
         for (int i = threadIdx.x; i < kTK * (kTN / 8); i += kThreads) {
             const int kr = i >> 3, ch = i & 7, nn = n0 + 8 * ch;
-            if (nn < NP)  // NP % 8 == 0: a 16-byte chunk is wholly inside or outside
-                *reinterpret_cast<uint4 *>(wt + (int64_t)(k0 + kr) * NP + nn) =
+            if (nn < N)  // N % 8 == 0: a 16-byte chunk is wholly inside or outside
+                *reinterpret_cast<uint4 *>(wt + (int64_t)(k0 + kr) * N + nn) =
                     *reinterpret_cast<const uint4 *>(&tile[kr][4 * ch]);
         }
         __syncthreads();
@@ -270,14 +264,103 @@ __global__ void __launch_bounds__(kThreads) dequant_t_bf16_kernel(const uint8_t 
 }
 
 inline cudaError_t launch_dequant_t_bf16(const uint8_t *qdata, const uint8_t *srel, const float *codebook,
-                                         const float *s_channel, int N, int K, int NP, uint16_t *wt, int num_sms,
+                                         const float *s_channel, int N, int K, uint16_t *wt, int num_sms,
                                          cudaStream_t stream)
 {
-    const int64_t tiles = (int64_t)(K / kTK) * ((NP + kTN - 1) / kTN);
+    const int64_t tiles = (int64_t)(K / kTK) * ((N + kTN - 1) / kTN);
     const int64_t cap = (int64_t)num_sms * 8;
     const int grid = (int)(tiles < cap ? tiles : cap);
-    dequant_t_bf16_kernel<<<grid < 1 ? 1 : grid, kThreads, 0, stream>>>(qdata, srel, codebook, s_channel, N, K, NP,
-                                                                        wt);
+    dequant_t_bf16_kernel<<<grid < 1 ? 1 : grid, kThreads, 0, stream>>>(qdata, srel, codebook, s_channel, N, K, wt);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- both weights of a gradient
+//
+// What a gradient that recomputes its forward needs of a weight, from one
+// reading of the packed codes: the int8 grid w8 [N, K] (decode_int8_kernel) and
+// the straight-through backward's w = bf16(w8 * bf16(s_channel)) [N, K]
+// (dequant_t_bf16_kernel's values, in the weight's own order: the contraction
+// takes it as an MN-major operand).  HBM traffic per weight: 0.5625 bytes in, 3
+// out.  As in decode_int8_kernel a thread takes one group of 16 weights; its
+// bf16 values leave as one 32-byte store, so a warp writes 512 and 1024
+// contiguous bytes.
+constexpr int kBothUnroll = 4;
+
+__global__ void __launch_bounds__(kThreads) decode_both_kernel(const uint8_t *__restrict__ qdata,
+                                                               const uint8_t *__restrict__ srel,
+                                                               const float *__restrict__ codebook,
+                                                               const float *__restrict__ s_channel, int64_t N,
+                                                               int64_t K, int8_t *__restrict__ w8,
+                                                               uint16_t *__restrict__ w)
+{
+    __shared__ uint4 lut[256 * kDecodeLutCopies];
+    __shared__ float cb[16];
+    if (threadIdx.x < 16)
+        cb[threadIdx.x] = codebook[threadIdx.x];
+    __syncthreads();
+    for (int s = threadIdx.x; s < 256; s += kThreads) {
+        const uint4 e = lut_entry((uint32_t)s, cb);
+#pragma unroll
+        for (int c = 0; c < kDecodeLutCopies; ++c)
+            lut[s * kDecodeLutCopies + c] = e;
+    }
+    __syncthreads();
+    const uint4 *lutc = lut + (threadIdx.x & (kDecodeLutCopies - 1));
+    const uint32_t per_row = (uint32_t)(K / 16);
+    const int64_t total = N * (K / 16), stride = (int64_t)gridDim.x * kThreads;
+    for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += kBothUnroll * stride) {
+        uint2 c[kBothUnroll];
+        uint32_t sb[kBothUnroll];
+        float sch[kBothUnroll];
+#pragma unroll
+        for (int u = 0; u < kBothUnroll; ++u) {
+            const int64_t i = i0 + u * stride;
+            if (i < total) {
+                c[u] = ldg_stream8(qdata + 8 * i);
+                sb[u] = __ldg(srel + i);
+                sch[u] = __ldg(s_channel + (total <= 0xFFFFFFFFll ? (uint32_t)i / per_row : i / per_row));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kBothUnroll; ++u) {
+            const int64_t i = i0 + u * stride;
+            if (i < total) {
+                const uint4 T = lutc[kDecodeLutCopies * sb[u]];
+                uint32_t o[4];
+                decode8(c[u].x, T, o[0], o[1]);
+                decode8(c[u].y, T, o[2], o[3]);
+                *reinterpret_cast<uint4 *>(w8 + 16 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+                // int8 -> fp32 through the low mantissa byte of 2^23, as in dequant_t_bf16_kernel
+                const float sc = __bfloat162float(__float2bfloat16_rn(sch[u]));
+                uint32_t b[8];
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    const uint32_t x = o[j >> 2] ^ 0x80808080u;
+                    const float f0 = __fsub_rn(
+                        __uint_as_float(prmt(x, 0x4B000000u, 0x7650u | (uint32_t)(j & 3))), 8388736.0f);
+                    const float f1 = __fsub_rn(
+                        __uint_as_float(prmt(x, 0x4B000000u, 0x7650u | (uint32_t)((j + 1) & 3))), 8388736.0f);
+                    b[j >> 1] = to_bf16x2_bits(__fmul_rn(f0, sc), __fmul_rn(f1, sc));
+                }
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(w + 16 * i), "r"(b[0]),
+                             "r"(b[1]), "r"(b[2]), "r"(b[3]), "r"(b[4]), "r"(b[5]), "r"(b[6]), "r"(b[7])
+                             : "memory");
+            }
+        }
+    }
+}
+
+// w must start on a 32-byte boundary.
+inline cudaError_t launch_decode_both(const uint8_t *qdata, const uint8_t *srel, const float *codebook,
+                                      const float *s_channel, int64_t N, int64_t K, int8_t *w8, uint16_t *w,
+                                      int num_sms, cudaStream_t stream)
+{
+    const int64_t total = N * (K / 16);
+    int64_t blocks = (total + (int64_t)kThreads * kBothUnroll - 1) / ((int64_t)kThreads * kBothUnroll);
+    const int64_t cap = (int64_t)num_sms * 8;
+    if (blocks > cap)
+        blocks = cap;
+    decode_both_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(qdata, srel, codebook, s_channel, N, K, w8, w);
     return cudaGetLastError();
 }
 

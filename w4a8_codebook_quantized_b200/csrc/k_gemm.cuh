@@ -40,10 +40,17 @@ enum Mode : int {
     kCeStats = 4,    // int8; softmax statistics of the outputs
     kCeGrad = 5,     // int8; the cross entropy's gradient of the outputs, up to each row's factor
     kBf16Rows = 6,   // bf16; outputs scaled by row
-    kModes = 7
+    kBf16Nt = 7,     // bf16; as kBf16, with B as below
+    kModes = 8
 };
 
-constexpr bool is_bf16(int mode) { return mode == kBf16 || mode == kBf16Rows || mode == kBf16RowsAdd; }
+constexpr bool is_bf16(int mode)
+{
+    return mode == kBf16 || mode == kBf16Nt || mode == kBf16Rows || mode == kBf16RowsAdd;
+}
+// B is given as [K, N] (N contiguous: an MN-major operand), not as [N, K]: a
+// weight [outputs, inputs] is the B of its input gradient as it stands.
+constexpr bool b_is_kn(int mode) { return mode == kBf16Nt || mode == kBf16Rows || mode == kBf16RowsAdd; }
 constexpr bool row_factor(int mode) { return mode == kBf16Rows || mode == kBf16RowsAdd; }
 
 // The epilogues that evaluate exponentials per output take eight warps (each
@@ -83,6 +90,7 @@ constexpr int kStages = 4;
 constexpr int kABytes = BM * BK;              // 16 KB
 constexpr int kBBytes = BN * BK;              // 32 KB
 constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kKnBytes = 64 * 128;            // 8 KB: 64 terms x 64 columns of a B given as [K, N]
 constexpr int kTmemCols = 2 * BN;             // two accumulators
 constexpr uint32_t kIdesc = idesc_i8(BM, BN);
 
@@ -738,7 +746,14 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                     }
                     mbar_arrive_expect_tx(&sh.full[stage], kStageBytes);
                     tma_load_2d(sh.stage[stage], &tmA, kb * BKE, tm * BM, &sh.full[stage]);
-                    tma_load_2d(sh.stage[stage] + kABytes, &tmB, kb * BKE, tn * BN, &sh.full[stage]);
+                    if constexpr (b_is_kn(MODE)) {
+#pragma unroll
+                        for (int i = 0; i < BN / 64; ++i)  // boxes of 64 columns x 64 terms
+                            tma_load_2d(sh.stage[stage] + kABytes + i * kKnBytes, &tmB, tn * BN + 64 * i, kb * BKE,
+                                        &sh.full[stage]);
+                    } else {
+                        tma_load_2d(sh.stage[stage] + kABytes, &tmB, kb * BKE, tn * BN, &sh.full[stage]);
+                    }
                     issued[stage] = 1;
                     issued_phase[stage] = phase;
                     if (++stage == kStages) {
@@ -785,9 +800,11 @@ __global__ void __launch_bounds__(threads(MODE), 1)
 #pragma unroll
                     for (int kk = 0; kk < BK / 32; ++kk) {
                         const uint64_t ad = sw128_kmajor_desc(a_addr + 32u * kk);
-                        const uint64_t bd = sw128_kmajor_desc(b_addr + 32u * kk);
+                        // 16 terms: 32 bytes along a K-major row, 16 rows of an MN-major box
+                        const uint64_t bd = b_is_kn(MODE) ? sw128_mnmajor_desc(b_addr + 2048u * kk, kKnBytes)
+                                                          : sw128_kmajor_desc(b_addr + 32u * kk);
                         if constexpr (BF16)
-                            mma_bf16(d, ad, bd, idesc_bf16(BM, BN), ((kb - k0) | kk) != 0 ? 1u : 0u);
+                            mma_bf16(d, ad, bd, idesc_bf16(BM, BN, b_is_kn(MODE)), ((kb - k0) | kk) != 0 ? 1u : 0u);
                         else
                             mma_i8(d, ad, bd, kIdesc, ((kb - k0) | kk) != 0 ? 1u : 0u);
                     }
@@ -977,8 +994,15 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                     if (leader)
                         mbar_arrive_expect_tx(&sh.full[stage], 2 * pair::kStageBytes);
                     tma_load_2d_pair(sh.stage[stage], &tmA, kb * BKE, tm * 256 + (int)rank * 128, full_leader);
-                    tma_load_2d_pair(sh.stage[stage] + pair::kHalfBytes, &tmB, kb * BKE, tn * BN + (int)rank * 128,
-                                     full_leader);
+                    if constexpr (b_is_kn(MODE)) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)  // this CTA's 128 columns, in boxes of 64 columns x 64 terms
+                            tma_load_2d_pair(sh.stage[stage] + pair::kHalfBytes + i * kKnBytes, &tmB,
+                                             tn * BN + (int)rank * 128 + 64 * i, kb * BKE, full_leader);
+                    } else {
+                        tma_load_2d_pair(sh.stage[stage] + pair::kHalfBytes, &tmB, kb * BKE,
+                                         tn * BN + (int)rank * 128, full_leader);
+                    }
                     issued[stage] = 1;
                     issued_phase[stage] = phase;
                     if (++stage == pair::kStages) {
@@ -1035,7 +1059,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                     for (int kk = 0; kk < BK / 32; ++kk)
                         if constexpr (BF16)
                             mma_bf16_pair(d, sw128_kmajor_desc(a_addr + 32u * kk),
-                                          sw128_kmajor_desc(b_addr + 32u * kk), idesc_bf16(256, BN),
+                                          b_is_kn(MODE) ? sw128_mnmajor_desc(b_addr + 2048u * kk, kKnBytes)
+                                                        : sw128_kmajor_desc(b_addr + 32u * kk),
+                                          idesc_bf16(256, BN, b_is_kn(MODE)),
                                           ((kb - k0) | kk) != 0 ? 1u : 0u);
                         else
                             mma_i8_pair(d, sw128_kmajor_desc(a_addr + 32u * kk),
