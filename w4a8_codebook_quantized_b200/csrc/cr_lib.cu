@@ -507,13 +507,15 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
         cfg.blockDim = dim3(gm::threads(MODE));
         cfg.dynamicSmemBytes = gm::pair::kSmemBytes;
         cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = gm::dependent(MODE) ? 2 : 1;
         return launched(cudaLaunchKernelEx(&cfg, gm::gemm_pair_kernel<MODE>, ta, tb, tm_out, e.xs, e.ws, e.bias, (int)M,
                                            (int)N, (int)K, e.out_f32, e.swiglu, e.tma_out, e.out, e.acc_out, e.ex));
     }
@@ -521,10 +523,18 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
         return CR_ERR_CUDA;
     const int64_t tiles = ((M + gm::BM - 1) / gm::BM) * ((N + gm::BN - 1) / gm::BN) * splits;
     const int grid = (int)(tiles < d.num_sms ? tiles : d.num_sms);
-    gm::gemm_kernel<MODE><<<grid, gm::threads(MODE), gm::kSmemBytes, stream>>>(ta, tb, tm_out, e.xs, e.ws, e.bias, (int)M,
-                                                                         (int)N, (int)K, e.out_f32, e.swiglu, e.tma_out,
-                                                                         e.out, e.acc_out, e.ex);
-    return launched(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(gm::threads(MODE));
+    cfg.dynamicSmemBytes = gm::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = gm::dependent(MODE) ? 1 : 0;
+    return launched(cudaLaunchKernelEx(&cfg, gm::gemm_kernel<MODE>, ta, tb, tm_out, e.xs, e.ws, e.bias, (int)M, (int)N,
+                                       (int)K, e.out_f32, e.swiglu, e.tma_out, e.out, e.acc_out, e.ex));
 }
 
 // The tensor map of a row-major output [M, cols] leaving in boxes of 32 rows x

@@ -25,6 +25,8 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const float *__restrict
                                                          const int64_t *__restrict__ targets,
                                                          float2 *__restrict__ part, float *__restrict__ tlogit)
 {
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const float kNegInf = __int_as_float(0xFF800000);
     __shared__ float2 sh[kThreads / 32];
     const int64_t m = blockIdx.y, n0 = (int64_t)blockIdx.x * kSlice;
@@ -68,6 +70,8 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const float2 *__restrict
                                                         const float *__restrict__ tlogit, float *__restrict__ loss,
                                                         float *__restrict__ lse)
 {
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
     const int64_t m = (kThreads / 32) * (int64_t)blockIdx.x + (threadIdx.x >> 5);
     if (m >= M)
@@ -97,6 +101,8 @@ __global__ void __launch_bounds__(kThreads) sum_to_bf16_kernel(const float4 *__r
                                                                int64_t split_stride4, int64_t n4,
                                                                uint2 *__restrict__ dst)
 {
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n4; i += (int64_t)gridDim.x * kThreads) {
         float4 v = acc[i];
 #pragma unroll 4
@@ -111,17 +117,15 @@ __global__ void __launch_bounds__(kThreads) sum_to_bf16_kernel(const float4 *__r
 inline cudaError_t launch_stats(const float *y, int64_t M, int64_t V, const int64_t *targets, float2 *part,
                                 float *tlogit, cudaStream_t stream)
 {
-    stats_kernel<<<dim3((unsigned)((V + kSlice - 1) / kSlice), (unsigned)M), kThreads, 0, stream>>>(y, V, targets,
-                                                                                                    part, tlogit);
-    return cudaGetLastError();
+    return launch_dependent(stats_kernel, dim3((unsigned)((V + kSlice - 1) / kSlice), (unsigned)M), kThreads, 0,
+                            stream, y, V, targets, part, tlogit);
 }
 
 inline cudaError_t launch_loss(const float2 *part, int64_t slices, int64_t M, const int64_t *targets, int64_t ignore,
                                int64_t V, const float *tlogit, float *loss, float *lse, cudaStream_t stream)
 {
-    loss_kernel<<<(unsigned)((M + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, stream>>>(part, slices, M, targets, ignore, V, tlogit, loss,
-                                                                    lse);
-    return cudaGetLastError();
+    return launch_dependent(loss_kernel, dim3((unsigned)((M + kThreads / 32 - 1) / (kThreads / 32))), kThreads, 0,
+                            stream, part, slices, M, targets, ignore, V, tlogit, loss, lse);
 }
 
 // acc: `splits` blocks of split_rows x K fp32; dst [M, K] bf16.
@@ -132,9 +136,9 @@ inline cudaError_t launch_sum_to_bf16(const float *acc, int splits, int64_t spli
     int64_t grid = (n4 + kThreads - 1) / kThreads;
     if (grid > 8 * (int64_t)num_sms)
         grid = 8 * (int64_t)num_sms;
-    sum_to_bf16_kernel<<<(unsigned)grid, kThreads, 0, stream>>>(reinterpret_cast<const float4 *>(acc), splits,
-                                                                split_rows * K / 4, n4, reinterpret_cast<uint2 *>(dst));
-    return cudaGetLastError();
+    return launch_dependent(sum_to_bf16_kernel, dim3((unsigned)grid), kThreads, 0, stream,
+                            reinterpret_cast<const float4 *>(acc), splits, split_rows * K / 4, n4,
+                            reinterpret_cast<uint2 *>(dst));
 }
 
 }  // namespace ce

@@ -295,6 +295,8 @@ __global__ void __launch_bounds__(kThreads) decode_both_kernel(const uint8_t *__
 {
     __shared__ uint4 lut[256 * kDecodeLutCopies];
     __shared__ float cb[16];
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x < 16)
         cb[threadIdx.x] = codebook[threadIdx.x];
     __syncthreads();
@@ -360,8 +362,8 @@ inline cudaError_t launch_decode_both(const uint8_t *qdata, const uint8_t *srel,
     const int64_t cap = (int64_t)num_sms * 8;
     if (blocks > cap)
         blocks = cap;
-    decode_both_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(qdata, srel, codebook, s_channel, N, K, w8, w);
-    return cudaGetLastError();
+    return launch_dependent(decode_both_kernel, dim3((unsigned)blocks), kThreads, 0, stream, qdata, srel, codebook,
+                            s_channel, N, K, w8, w);
 }
 
 // ---------------------------------------------------------------- failure-path self-test

@@ -53,6 +53,12 @@ constexpr bool is_bf16(int mode)
 constexpr bool b_is_kn(int mode) { return mode == kBf16Nt || mode == kBf16Rows || mode == kBf16RowsAdd; }
 constexpr bool row_factor(int mode) { return mode == kBf16Rows || mode == kBf16RowsAdd; }
 
+// The modes whose kernels follow one another in one call (decode -> int8
+// contraction -> bf16 contraction -> sum) are launched as programmatic
+// dependents: a kernel's launch and set-up overlap its predecessor's tail, and
+// it waits for the predecessor before it reads or writes anything.
+constexpr bool dependent(int mode) { return mode != kI8 && mode != kBf16; }
+
 // The epilogues that evaluate exponentials per output take eight warps (each
 // 32 rows x 128 columns of a tile) where the others take four (32 x 256): with
 // four, the epilogue of an int8 tile outlasted the tile's own MMAs.
@@ -721,6 +727,10 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if constexpr (dependent(MODE)) {
+        asm volatile("griddepcontrol.launch_dependents;" :::);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
     const uint32_t tmem = sh.tmem_base;
     volatile int *abort = &sh.abort;
 
@@ -967,6 +977,10 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     tc_fence_before();
     cluster_sync();  // both CTAs' barriers exist before anyone signals them
     tc_fence_after();
+    if constexpr (dependent(MODE)) {
+        asm volatile("griddepcontrol.launch_dependents;" :::);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
     const uint32_t tmem = sh.tmem_base;
     volatile int *abort = &sh.abort;
 

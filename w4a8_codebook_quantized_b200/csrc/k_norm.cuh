@@ -493,24 +493,6 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_pairs_kernel(const FwdArgs a)
     }
 }
 
-// A launch as a programmatic dependent of the previous kernel on the stream.
-template <class... Args>
-inline cudaError_t launch_dependent(void (*kern)(Args...), int64_t grid, int threads, int smem, cudaStream_t stream,
-                                    Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <bool GBF16, int THREADS>
 inline cudaError_t launch_fwd_rows(const FwdArgs &a, int64_t MP, cudaStream_t stream)
 {
@@ -519,7 +501,7 @@ inline cudaError_t launch_fwd_rows(const FwdArgs &a, int64_t MP, cudaStream_t st
     void (*kern)(FwdArgs) = per_hw <= 1   ? rmsnorm_rows_kernel<1, false, THREADS, GBF16>
                             : per_hw == 2 ? rmsnorm_rows_kernel<2, false, THREADS, GBF16>
                                           : rmsnorm_rows_kernel<1, true, THREADS, GBF16>;
-    return launch_dependent(kern, MP, THREADS, 0, stream, a);
+    return launch_dependent(kern, dim3((unsigned)(MP)), THREADS, 0, stream, a);
 }
 
 // Opt the 384- and 512-thread CTAs of the packed form into their transpose
@@ -553,16 +535,16 @@ inline cudaError_t launch_fwd_t(const FwdArgs &a, int64_t MP, cudaStream_t strea
         return a.K >= 8192 ? launch_fwd_rows<GBF16, 512>(a, MP, stream) : launch_fwd_rows<GBF16, 256>(a, MP, stream);
     const int64_t pairs = (a.K / 256 + 1) / 2;
     if (pairs <= 4)
-        return launch_dependent(rmsnorm_pairs_kernel<1, false, 64, GBF16>, MP, 64, rq::smem_bytes<64>(), stream, a);
+        return launch_dependent(rmsnorm_pairs_kernel<1, false, 64, GBF16>, dim3((unsigned)(MP)), 64, rq::smem_bytes<64>(), stream, a);
     if (pairs <= 8)
-        return launch_dependent(rmsnorm_pairs_kernel<1, false, 128, GBF16>, MP, 128, rq::smem_bytes<128>(), stream, a);
+        return launch_dependent(rmsnorm_pairs_kernel<1, false, 128, GBF16>, dim3((unsigned)(MP)), 128, rq::smem_bytes<128>(), stream, a);
     if (pairs <= 16)
-        return launch_dependent(rmsnorm_pairs_kernel<1, false, 256, GBF16>, MP, 256, rq::smem_bytes<256>(), stream, a);
+        return launch_dependent(rmsnorm_pairs_kernel<1, false, 256, GBF16>, dim3((unsigned)(MP)), 256, rq::smem_bytes<256>(), stream, a);
     if (pairs <= 24)
-        return launch_dependent(rmsnorm_pairs_kernel<1, false, 384, GBF16>, MP, 384, rq::smem_bytes<384>(), stream, a);
+        return launch_dependent(rmsnorm_pairs_kernel<1, false, 384, GBF16>, dim3((unsigned)(MP)), 384, rq::smem_bytes<384>(), stream, a);
     if (pairs <= 32)
-        return launch_dependent(rmsnorm_pairs_kernel<1, false, 512, GBF16>, MP, 512, rq::smem_bytes<512>(), stream, a);
-    return launch_dependent(rmsnorm_pairs_kernel<1, true, 512, GBF16>, MP, 512, rq::smem_bytes<512>(), stream, a);
+        return launch_dependent(rmsnorm_pairs_kernel<1, false, 512, GBF16>, dim3((unsigned)(MP)), 512, rq::smem_bytes<512>(), stream, a);
+    return launch_dependent(rmsnorm_pairs_kernel<1, true, 512, GBF16>, dim3((unsigned)(MP)), 512, rq::smem_bytes<512>(), stream, a);
 }
 
 // Short batches take the scalar form, 512 threads for K >= 8192 and 256 below;
@@ -702,7 +684,7 @@ inline cudaError_t launch_rotate(const uint16_t *x, int64_t M, int64_t K, uint16
     int64_t grid = (blocks + kRotThreads / 8 - 1) / (kRotThreads / 8);
     if (grid > INT_MAX)
         grid = INT_MAX;
-    return launch_dependent(rotate_kernel, grid, kRotThreads, 0, stream, x, blocks, out, all_wide({x, out}));
+    return launch_dependent(rotate_kernel, dim3((unsigned)(grid)), kRotThreads, 0, stream, x, blocks, out, all_wide({x, out}));
 }
 
 // ---------------------------------------------------------------- backward
@@ -959,20 +941,20 @@ inline cudaError_t launch_bwd_t(const BwdArgs &a, float *dgamma, cudaStream_t st
     const int64_t P = backward_ctas(a.M, a.K);
     cudaError_t e;
     if (a.K <= 1024)
-        e = launch_dependent(rmsnorm_backward_kernel<1, false, 64, GBF16>, P, 64, 0, stream, a);
+        e = launch_dependent(rmsnorm_backward_kernel<1, false, 64, GBF16>, dim3((unsigned)(P)), 64, 0, stream, a);
     else if (a.K <= 2048)
-        e = launch_dependent(rmsnorm_backward_kernel<1, false, 128, GBF16>, P, 128, 0, stream, a);
+        e = launch_dependent(rmsnorm_backward_kernel<1, false, 128, GBF16>, dim3((unsigned)(P)), 128, 0, stream, a);
     else if (a.K <= 4096)
-        e = launch_dependent(rmsnorm_backward_kernel<1, false, 256, GBF16>, P, 256, 0, stream, a);
+        e = launch_dependent(rmsnorm_backward_kernel<1, false, 256, GBF16>, dim3((unsigned)(P)), 256, 0, stream, a);
     else if (a.K <= 8192)
-        e = launch_dependent(rmsnorm_backward_kernel<1, false, 512, GBF16>, P, 512, 0, stream, a);
+        e = launch_dependent(rmsnorm_backward_kernel<1, false, 512, GBF16>, dim3((unsigned)(P)), 512, 0, stream, a);
     else if (a.K <= 16384)
-        e = launch_dependent(rmsnorm_backward_kernel<2, false, 512, GBF16>, P, 512, 0, stream, a);
+        e = launch_dependent(rmsnorm_backward_kernel<2, false, 512, GBF16>, dim3((unsigned)(P)), 512, 0, stream, a);
     else
-        e = launch_dependent(rmsnorm_backward_kernel<1, true, 512, GBF16>, P, 512, 0, stream, a);
+        e = launch_dependent(rmsnorm_backward_kernel<1, true, 512, GBF16>, dim3((unsigned)(P)), 512, 0, stream, a);
     if (e != cudaSuccess || dgamma == nullptr)
         return e;
-    return launch_dependent(dgamma_kernel, a.K / 32, 256, 0, stream, (const float *)a.part, (int)P, a.K, dgamma);
+    return launch_dependent(dgamma_kernel, dim3((unsigned)(a.K / 32)), 256, 0, stream, (const float *)a.part, (int)P, a.K, dgamma);
 }
 
 inline cudaError_t launch_bwd(BwdArgs a, bool gamma_bf16, float *dgamma, cudaStream_t stream)
