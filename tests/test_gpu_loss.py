@@ -48,10 +48,12 @@ def _work(name, *shape):
 
 @pytest.mark.parametrize("M,N,K,bias", [(1, 8, 256, False), (1, 264, 512, True), (8, 520, 256, False),
                                         (37, 1000, 768, True), (128, 256, 256, False), (129, 2824, 1280, True),
-                                        (257, 512, 1024, False), (700, 6400, 256, True)])
+                                        (257, 512, 1024, False), (700, 6400, 256, True), (2500, 512, 1024, False),
+                                        (3900, 3200, 1280, False)])
 def test_swiglu_backward(M, N, K, bias):
     """One row to several tiles, ragged rows and columns (N / 2 a multiple of
-    4 only), both GEMM forms."""
+    4 only), both GEMM forms; the reduction split for few tiles, and for the
+    last partial wave of more than one wave of tiles."""
     ly = inputs.layer(N, K, M + N, with_bias=bias)
     xq, xs, xq_d, xs_d = _quantised(M, K, 3, rows=M + 3)
     dout = to_bf16(np.random.default_rng([M, N]).standard_normal((M, N // 2)))
@@ -199,7 +201,7 @@ def test_cross_entropy_of_masked_entries(M):
     assert (f64(lse) == -np.inf).all()
 
 
-@pytest.mark.parametrize("M", [5, 30])
+@pytest.mark.parametrize("M", [5, 30, 300])
 def test_cross_entropy_of_invalid_targets(M):
     """A target outside the vocabulary: NaN in its row alone; another
     ignore_index; all rows ignored."""
@@ -287,6 +289,45 @@ def test_cross_entropy_split_reduction_over_pieces():
     rx, ex = cross_entropy_backward(ly, xq, xs, t, f64(lse), dloss.astype(np.float64))
     assert_bf16_near(dx.tensor, rx, 0.0, "dx", extra=ex)
     assert torch.equal(dx.tensor, cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(t), lse, dev(dloss)))
+
+
+@pytest.mark.parametrize("ignored", ["none", "third", "most", "all"])
+def test_cross_entropy_of_many_rows(ignored):
+    """More than one wave of tiles, of which the ignored rows leave fewer: the
+    rows that take part are gathered, their number is known on the device only,
+    and rows of NaN scale (a padded batch) do not matter where ignored."""
+    M, V, K = 4100, 3300, 1280
+    ly = inputs.layer(V, K, 21)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 22)
+    t = _targets(M, V, 23, ignored=False)
+    rng = np.random.default_rng(24)
+    gone = {"none": np.zeros(M, bool), "third": rng.random(M) < 1 / 3, "most": rng.random(M) < 0.99,
+            "all": np.ones(M, bool)}[ignored]
+    t[gone] = -100
+    w, _ = _layer_dev(ly)
+    _, r_lse, _ = cross_entropy(ly, xq, xs, t)
+    lse = r_lse.astype(np.float32)
+    lse_d = lse.copy()
+    lse_d[gone] = np.nan
+    dloss = rng.uniform(-1, 1, M).astype(np.float32)
+    dx = Guarded((M, K), torch.bfloat16)
+    work = _work("cr_w4a8_cross_entropy_backward", M, V, K)
+    work.tensor.fill_(0xFF)
+    cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(t), dev(lse_d), dev(dloss), dx=dx.tensor, work=work.tensor)
+    torch.cuda.synchronize()
+    assert dx.intact() and work.intact()
+    rx, ex = cross_entropy_backward(ly, xq, xs, t, lse.astype(np.float64), dloss.astype(np.float64))
+    assert_bf16_near(dx.tensor, rx, 0.0, "dx", extra=ex)
+    assert (f64(dx.tensor)[gone] == 0).all()
+    again = cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(t), dev(lse_d), dev(dloss))
+    assert torch.equal(again, dx.tensor)
+    # a target outside the vocabulary: NaN in its row alone
+    bad = np.flatnonzero(~gone)[3::7][:5]
+    t[bad] = V + np.arange(len(bad))
+    again = cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(t), dev(lse_d), dev(dloss))
+    keep = np.ones(M, bool)
+    keep[bad] = False
+    assert torch.isnan(again[dev(bad)]).all() and torch.equal(again[dev(keep)], dx.tensor[dev(keep)])
 
 
 def test_cross_entropy_row_blocks():

@@ -465,6 +465,8 @@ struct GemmEpilogue {
     int out_f32 = 0, swiglu = 0, tma_out = 1;
     void *out = nullptr;
     int32_t *acc_out = nullptr;
+    bool pair = false;                  // B as [K, N]: one tile per SM pair (the plan's choice)
+    const CUtensorMap *copies = nullptr;  // and where split tiles go
     int64_t b_rows = 0;  // rows that a B given as [K, N] has, where K counts padding of A past them (0: K)
     cr::gm::EpiArgs ex;
 };
@@ -489,18 +491,18 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
         return true;
     };
     const int64_t pair_tiles = ((M + 255) / 256) * ((N + gm::BN - 1) / gm::BN);
-    const int splits = gm::is_bf16(MODE) ? e.ex.splits : 1;
-    const bool use_pair = splits > 1 ? M > gm::BM : pair_tiles >= d.num_sms / 2;
+    const bool use_pair = gm::b_is_kn(MODE) ? e.pair : pair_tiles >= d.num_sms / 2;
     CUtensorMap ta, tb;
     if (!map(&ta, A, M, (uint32_t)gm::BM) ||
         !(gm::b_is_kn(MODE) ? make_tmap_bf16(&tb, B, (uint64_t)N, (uint64_t)(e.b_rows ? e.b_rows : K), 64u, 64u)
                             : map(&tb, B, N, use_pair ? 128u : (uint32_t)gm::BN)))
         return CR_ERR_CUDA;
-    const CUtensorMap &tm_out = to ? *to : ta;  // placeholder when the output does not go through TMA
+    const CUtensorMap &tm_out = to ? *to : ta;  // placeholders where nothing leaves through them
+    const CUtensorMap &tm_copy = e.copies ? *e.copies : ta;
     if (use_pair) {
         if (!opt_in(d.gemm_pair_attr_set[MODE], (const void *)gm::gemm_pair_kernel<MODE>, gm::pair::kSmemBytes))
             return CR_ERR_CUDA;
-        const int64_t units = pair_tiles * splits;
+        const int64_t units = gm::b_is_kn(MODE) ? e.ex.slots : pair_tiles;
         const int64_t pairs = units < d.num_sms / 2 ? units : d.num_sms / 2;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(2 * pairs));
@@ -516,12 +518,12 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
         attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = gm::dependent(MODE) ? 2 : 1;
-        return launched(cudaLaunchKernelEx(&cfg, gm::gemm_pair_kernel<MODE>, ta, tb, tm_out, e.xs, e.ws, e.bias, (int)M,
+        return launched(cudaLaunchKernelEx(&cfg, gm::gemm_pair_kernel<MODE>, ta, tb, tm_out, tm_copy, e.xs, e.ws, e.bias, (int)M,
                                            (int)N, (int)K, e.out_f32, e.swiglu, e.tma_out, e.out, e.acc_out, e.ex));
     }
     if (!opt_in(d.gemm_attr_set[MODE], (const void *)gm::gemm_kernel<MODE>, gm::kSmemBytes))
         return CR_ERR_CUDA;
-    const int64_t tiles = ((M + gm::BM - 1) / gm::BM) * ((N + gm::BN - 1) / gm::BN) * splits;
+    const int64_t tiles = gm::b_is_kn(MODE) ? e.ex.slots : ((M + gm::BM - 1) / gm::BM) * ((N + gm::BN - 1) / gm::BN);
     const int grid = (int)(tiles < d.num_sms ? tiles : d.num_sms);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -533,7 +535,7 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = gm::dependent(MODE) ? 1 : 0;
-    return launched(cudaLaunchKernelEx(&cfg, gm::gemm_kernel<MODE>, ta, tb, tm_out, e.xs, e.ws, e.bias, (int)M, (int)N,
+    return launched(cudaLaunchKernelEx(&cfg, gm::gemm_kernel<MODE>, ta, tb, tm_out, tm_copy, e.xs, e.ws, e.bias, (int)M, (int)N,
                                        (int)K, e.out_f32, e.swiglu, e.tma_out, e.out, e.acc_out, e.ex));
 }
 
@@ -1257,39 +1259,76 @@ struct Parts {
     }
 };
 
-// How a bf16 contraction [M, K] over `red` terms is spread over the SMs when
-// it has too few tiles to fill them: the reduction in `n` ranges, each with its
-// own fp32 copy of the outputs (`rows` rows, so that no tile's store reaches the
-// next copy), added up afterwards in a fixed order.  One SM pair works a 256 x
-// 256 tile, one SM a 128 x 256 tile when M <= 128; a range keeps at least 8
-// blocks of 64 terms.  148 SMs: the caller's buffers may not depend on more
-// than the shape.
-struct SplitPlan {
-    int n = 1;
-    int64_t rows = 0;
-    SplitPlan(int64_t M, int64_t K, int64_t red)
+// How a bf16 contraction [M, K] over `red` terms is spread over the SMs
+// (gm::Tiling): 256 x 256 tiles on SM pairs, or 128 x 256 tiles on single SMs
+// where M has one such tile or the pairs' tiles would fill more than half of
+// one wave but not all of it.  A split tile's ranges keep at least 8 blocks of
+// 64 terms; the last partial wave is split where a tile is long enough (48
+// blocks, some 20 us) for the joining to cost less than the half wave it saves.
+// The slots count 148 SMs: the caller's buffers may depend on the shape alone.
+struct KnPlan {
+    bool pair;
+    int bm, slots, max_splits, split_tail;
+    int64_t copies;  // fp32 copies of tiles at most
+    KnPlan(int64_t M, int64_t K, int64_t red)
     {
-        const int64_t bm = M <= cr::gm::BM ? cr::gm::BM : 2 * cr::gm::BM, slots = M <= cr::gm::BM ? 148 : 74;
-        const int64_t tiles = (M + bm - 1) / bm * ((K + cr::gm::BN - 1) / cr::gm::BN), blocks = (red + 63) / 64;
-        int64_t s = slots / tiles < blocks / 8 ? slots / tiles : blocks / 8;
-        if (s > 1)
-            n = (int)(s < 32 ? s : 32);
-        rows = n > 1 ? round_up(M, bm) : M;
+        const int64_t tiles_n = (K + cr::gm::BN - 1) / cr::gm::BN, pair_tiles = (M + 255) / 256 * tiles_n;
+        pair = M > cr::gm::BM && (pair_tiles <= 37 || pair_tiles >= 74);
+        bm = pair ? 256 : 128;
+        slots = pair ? 74 : 148;
+        const int64_t blocks = (red + 63) / 64, tiles = (M + bm - 1) / bm * tiles_n;
+        max_splits = (int)(blocks / 8 < 1 ? 1 : blocks / 8 < 32 ? blocks / 8 : 32);
+        split_tail = blocks >= 48;
+        copies = max_splits < 2 || (tiles >= slots && !split_tail) ? 0
+                 : tiles * max_splits < slots                       ? tiles * max_splits
+                                                                    : slots;
+    }
+    int64_t copy_bytes() const { return copies * bm * cr::gm::BN * 4; }
+    // the kernel's arguments for a launch with this plan
+    void put(GemmEpilogue &e) const
+    {
+        e.pair = pair;
+        e.ex.slots = slots;
+        e.ex.max_splits = copies ? max_splits : 1;
+        e.ex.split_tail = split_tail;
+    }
+    cr::ce::SumArgs sum(const float *acc, const float *cp, int64_t M, int64_t K, int64_t red, uint16_t *dst) const
+    {
+        cr::ce::SumArgs a = {};
+        a.acc = acc;
+        a.copies = cp;
+        a.M = (int)M;
+        a.K = (int)K;
+        a.bm = bm;
+        a.kblocks = (int)((red + 63) / 64);
+        a.slots = slots;
+        a.max_splits = copies ? max_splits : 1;
+        a.split_tail = split_tail;
+        a.dst = dst;
+        return a;
+    }
+    // Whether the contraction has split tiles for every row count up to M.
+    bool splits(int64_t M, int64_t K) const
+    {
+        if (!copies)
+            return false;
+        const cr::gm::Tiling t((int)M, (int)K, 8 * max_splits, bm, slots, max_splits, split_tail);
+        return t.units > t.full;
     }
 };
 
 struct SwigluWork {
     int8_t *w8;
-    uint16_t *w;  // the gradient's bf16 weight
-    float *acc;   // the split reduction's copies (null: not split)
-    SplitPlan split;
+    uint16_t *w;    // the gradient's bf16 weight
+    float *copies;  // of split tiles
+    KnPlan plan;
     int64_t bytes;
-    SwigluWork(void *work, int64_t M, int64_t N, int64_t K) : split(M, K, N)
+    SwigluWork(void *work, int64_t M, int64_t N, int64_t K) : plan(M, K, N)
     {
         Parts p(work);
         w8 = static_cast<int8_t *>(p.take(N * K));
         w = static_cast<uint16_t *>(p.take(2 * N * K));
-        acc = split.n > 1 ? static_cast<float *>(p.take(4 * split.n * split.rows * K)) : nullptr;
+        copies = static_cast<float *>(p.take(plan.copy_bytes()));
         bytes = p.used;
     }
 };
@@ -1338,23 +1377,39 @@ struct CeFwdWork {
     }
 };
 
+// Rows are gathered from 2^34 products on: there the two contractions take
+// some 30 us, and a tenth of the rows ignored pays for the gathering's 4 us
+// (4096 x 65536 x 4096, 10 percent ignored: 2671 -> 2385 us with the split
+// last wave; 500 x 10007 x 1024, half ignored: 43.2 -> 44.8 us, so not there).
 struct CeBwdWork {
     int64_t rows, piece;
     int8_t *w8;
     uint16_t *w, *dl;
-    float *acc;  // fp32 sums over the pieces, per range of a split reduction (null: one piece, not split)
-    SplitPlan split;
+    float *acc, *copies;  // fp32 sums over the pieces: whole tiles, and the copies of split ones
+    bool compact;         // gather the rows that take part
+    cr::ce::CompactArgs c = {};
+    KnPlan plan;
     int64_t bytes;
     CeBwdWork(void *work, int64_t M, int64_t V, int64_t K)
-        : rows(M < kBwdRows ? M : kBwdRows), piece(ce_piece(V, rows > K ? rows : K)),
-          split(rows, K, piece < V ? piece : V)
+        : rows(M < kBwdRows ? M : kBwdRows), piece(ce_piece(V, rows > K ? rows : K)), compact(M > 256 && (double)M * (double)V * (double)K >= 17179869184.0),
+          plan(rows, K, piece < V ? piece : V)
     {
         Parts p(work);
         const int64_t most = piece < V ? piece : round_up(V, 8);
         w8 = static_cast<int8_t *>(p.take(most * K));
         w = static_cast<uint16_t *>(p.take(2 * most * K));
         dl = static_cast<uint16_t *>(p.take(2 * most * rows));
-        acc = piece < V || split.n > 1 ? static_cast<float *>(p.take(4 * split.n * split.rows * K)) : nullptr;
+        acc = static_cast<float *>(p.take(4 * rows * K));
+        copies = static_cast<float *>(p.take(plan.copy_bytes()));
+        if (compact) {
+            c.c_xq = static_cast<int8_t *>(p.take(rows * K));
+            c.c_xs = static_cast<float *>(p.take(4 * rows));
+            c.c_lse = static_cast<float *>(p.take(4 * rows));
+            c.c_dloss = static_cast<float *>(p.take(4 * rows));
+            c.c_targets = static_cast<int64_t *>(p.take(8 * rows));
+            c.rows = static_cast<int *>(p.take(4 * rows));
+            c.count = static_cast<int *>(p.take(4));
+        }
         bytes = p.used;
     }
 };
@@ -1424,9 +1479,9 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
     if (st != CR_OK)
         return st;
     using namespace cr;
-    CUtensorMap tz, tx;
-    if (!make_tmap_out(&tz, dz, M, N, false, /*half=*/true) ||
-        !(w.acc ? make_tmap_out(&tx, w.acc, w.split.n * w.split.rows, K, true) : make_tmap_out(&tx, dx, M, K, false)))
+    CUtensorMap tz, tx, tc;
+    if (!make_tmap_out(&tz, dz, M, N, false, /*half=*/true) || !make_tmap_out(&tx, dx, M, K, false) ||
+        (w.plan.copies && !make_tmap_out(&tc, w.copies, w.plan.copies * w.plan.bm, gm::BN, true)))
         return CR_ERR_CUDA;
     st = launched(ew::launch_decode_both(qdata, srel, codebook, s_channel, N, K, w.w8, w.w, d->num_sms, stream));
     if (st != CR_OK)
@@ -1440,12 +1495,11 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
     if (st != CR_OK)
         return st;
     GemmEpilogue g;
-    g.out_f32 = w.acc != nullptr;
-    g.ex.splits = w.split.n;
-    g.ex.split_rows = (int)w.split.rows;
+    w.plan.put(g);
+    g.copies = w.plan.copies ? &tc : nullptr;
     st = launch_gemm<gm::kBf16Nt>(*d, dz, w.w, &tx, M, K, N, g, stream);
-    if (st == CR_OK && w.acc)
-        st = launched(ce::launch_sum_to_bf16(w.acc, w.split.n, w.split.rows, M, K, dx, d->num_sms, stream));
+    if (st == CR_OK && w.plan.splits(M, K))
+        st = launched(ce::launch_split_sum(w.plan.sum(nullptr, w.copies, M, K, N, dx), d->num_sms, stream));
     return st;
 }
 
@@ -1535,8 +1589,36 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
     if (st != CR_OK)
         return st;
     using namespace cr;
+    const int64_t red = w.piece < V ? w.piece : V;
+    CUtensorMap tc;
+    if (w.plan.copies && !make_tmap_out(&tc, w.copies, w.plan.copies * w.plan.bm, gm::BN, true))
+        return CR_ERR_CUDA;
     for (int64_t m0 = 0; m0 < M; m0 += w.rows) {
         const int64_t rows = M - m0 < w.rows ? M - m0 : w.rows;
+        // the block's rows, or those of them that take part
+        ce::CompactArgs c = w.c;
+        c.targets = targets + m0;
+        c.ignore = ignore_index;
+        c.xq = xq + m0 * K;
+        c.xs = xs + m0;
+        c.lse = lse + m0;
+        c.dloss = dloss + m0;
+        c.M = rows;
+        c.K = K;
+        c.dx = dx + m0 * K;
+        if (w.compact) {
+            st = launched(ce::launch_compact(c, stream));
+            if (st != CR_OK)
+                return st;
+        }
+        gm::EpiArgs ex;
+        ex.targets = w.compact ? c.c_targets : c.targets;
+        ex.ignore = ignore_index;
+        ex.V = V;
+        ex.lse = w.compact ? c.c_lse : c.lse;
+        ex.dloss = w.compact ? c.c_dloss : c.dloss;
+        ex.count = w.compact ? c.count : nullptr;
+        const int8_t *bxq = w.compact ? c.c_xq : c.xq;
         for (int64_t n0 = 0; n0 < V; n0 += w.piece) {
             const int64_t n = V - n0 < w.piece ? V - n0 : w.piece, np = round_up(n, 8);
             const uint8_t *q = qdata + n0 * (K / 2), *s = srel + n0 * (K / 16);
@@ -1545,43 +1627,34 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
                 return st;
             // dl [rows, np]: the gradient of the piece's outputs
             CUtensorMap tl, tx;
-            if (!make_tmap_out(&tl, w.dl, rows, np, false, /*half=*/true) ||
-                !(w.acc ? make_tmap_out(&tx, w.acc, w.split.n > 1 ? w.split.n * w.split.rows : rows, K, true)
-                        : make_tmap_out(&tx, dx + m0 * K, rows, K, false)))
+            if (!make_tmap_out(&tl, w.dl, rows, np, false, /*half=*/true) || !make_tmap_out(&tx, w.acc, rows, K, true))
                 return CR_ERR_CUDA;
             GemmEpilogue e;
-            e.xs = xs + m0;
+            e.xs = w.compact ? c.c_xs : c.xs;
             e.ws = s_channel + n0;
             e.bias = bias ? bias + n0 : nullptr;
-            e.ex.targets = targets + m0;
-            e.ex.ignore = ignore_index;
-            e.ex.V = V;
+            e.ex = ex;
             e.ex.n0 = (int)n0;
-            e.ex.lse = lse + m0;
-            st = launch_gemm<gm::kCeGrad>(*d, xq + m0 * K, w.w8, &tl, rows, n, K, e, stream);
+            st = launch_gemm<gm::kCeGrad>(*d, bxq, w.w8, &tl, rows, n, K, e, stream);
             if (st != CR_OK)
                 return st;
             GemmEpilogue g;
-            g.out_f32 = w.acc != nullptr;
+            g.out_f32 = 1;
             g.b_rows = n;
-            // a short last piece has fewer blocks of terms than ranges: every range keeps one
-            g.ex.splits = (int)((np + 63) / 64 < w.split.n ? (np + 63) / 64 : w.split.n);
-            g.ex.split_rows = (int)w.split.rows;
-            g.ex.targets = targets + m0;
-            g.ex.ignore = ignore_index;
-            g.ex.V = V;
-            g.ex.dloss = dloss + m0;
-            st = w.acc && n0 > 0 ? launch_gemm<gm::kBf16RowsAdd>(*d, w.dl, w.w, &tx, rows, K, np, g, stream)
-                                 : launch_gemm<gm::kBf16Rows>(*d, w.dl, w.w, &tx, rows, K, np, g, stream);
+            g.ex = ex;
+            w.plan.put(g);
+            g.copies = w.plan.copies ? &tc : nullptr;
+            st = n0 > 0 ? launch_gemm<gm::kBf16RowsAdd>(*d, w.dl, w.w, &tx, rows, K, np, g, stream)
+                        : launch_gemm<gm::kBf16Rows>(*d, w.dl, w.w, &tx, rows, K, np, g, stream);
             if (st != CR_OK)
                 return st;
         }
-        if (w.acc) {
-            st = launched(ce::launch_sum_to_bf16(w.acc, w.split.n, w.split.rows, rows, K, dx + m0 * K, d->num_sms,
-                                                 stream));
-            if (st != CR_OK)
-                return st;
-        }
+        ce::SumArgs sum = w.plan.sum(w.acc, w.copies, rows, K, red, c.dx);
+        sum.count = ex.count;
+        sum.rows = w.compact ? c.rows : nullptr;
+        st = launched(ce::launch_split_sum(sum, d->num_sms, stream));
+        if (st != CR_OK)
+            return st;
     }
     return CR_OK;
 }

@@ -95,22 +95,120 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const float2 *__restrict
     }
 }
 
-// out[m, k] = bf16(sum over s of acc[s, m, k]), four elements per thread and
-// step; the sums are taken in the order of s.
-__global__ void __launch_bounds__(kThreads) sum_to_bf16_kernel(const float4 *__restrict__ acc, int splits,
-                                                               int64_t split_stride4, int64_t n4,
-                                                               uint2 *__restrict__ dst)
+// The rows that take part in the loss, gathered: every row's index, quantised
+// activations, scale, target, lse and dloss in order, their number in *count,
+// and zeros in dx for the others.  A gradient is zero where the target is
+// ignored, and a batch of prompts and padding is ignored for a good part: the
+// contractions then run over `count` rows.  A CTA takes 32 rows and counts the
+// valid ones before them itself (at most 64 KB of targets, from L2).
+struct CompactArgs {
+    const int64_t *targets;
+    int64_t ignore;
+    const int8_t *xq;
+    const float *xs, *lse, *dloss;
+    int64_t M, K;
+    int8_t *c_xq;
+    float *c_xs, *c_lse, *c_dloss;
+    int64_t *c_targets;
+    int *rows, *count;
+    uint16_t *dx;
+};
+
+__global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a)
+{
+    __shared__ int warp_count[kThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t m0 = 32 * (int64_t)blockIdx.x;
+    int n = 0;
+#pragma unroll 4
+    for (int64_t m = threadIdx.x; m < m0; m += kThreads)
+        n += a.targets[m] != a.ignore ? 1 : 0;
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (lane == 0)
+        warp_count[w] = n;
+    __syncthreads();
+    int base = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i)
+        base += warp_count[i];
+    const int64_t t = m0 + lane < a.M ? a.targets[m0 + lane] : a.ignore;
+    const uint32_t valid = __ballot_sync(0xFFFFFFFFu, t != a.ignore);
+    if (w == 0) {
+        if ((valid >> lane) & 1u) {
+            const int at = base + __popc(valid & ((1u << lane) - 1u));
+            const int64_t m = m0 + lane;
+            a.rows[at] = (int)m;
+            a.c_targets[at] = t;
+            a.c_xs[at] = a.xs[m];
+            a.c_lse[at] = a.lse[m];
+            a.c_dloss[at] = a.dloss[m];
+        }
+        if (lane == 0 && m0 + 32 >= a.M)
+            *a.count = base + __popc(valid);
+    }
+    for (int r = w; r < 32 && m0 + r < a.M; r += kThreads / 32) {
+        const int64_t m = m0 + r;
+        if ((valid >> r) & 1u) {
+            const int64_t at = base + __popc(valid & ((1u << r) - 1u));
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.xq + m * a.K);
+            uint4 *dst = reinterpret_cast<uint4 *>(a.c_xq + at * a.K);
+#pragma unroll 4
+            for (int64_t i = lane; i < a.K / 16; i += 32)
+                dst[i] = src[i];
+        } else {
+            uint4 *dst = reinterpret_cast<uint4 *>(a.dx + m * a.K);
+            for (int64_t i = lane; i < a.K / 8; i += 32)
+                dst[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+}
+
+// The last step of a split contraction: bf16 outputs from the fp32 copies of
+// the split tiles, added in order, and (acc given) from the fp32 sums of the
+// whole ones; without acc the whole tiles' outputs are in dst already, and only
+// the split tiles are visited.  Output row `rows[m]` (m without rows).
+struct SumArgs {
+    const float *acc;     // [M, K], or null
+    const float *copies;  // [copies][bm][256]
+    int M, K, bm, kblocks, slots, max_splits, split_tail;
+    const int *count, *rows;
+    uint16_t *dst;
+};
+
+__global__ void __launch_bounds__(kThreads) split_sum_kernel(const SumArgs a)
 {
     asm volatile("griddepcontrol.launch_dependents;" :::);
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int M = a.count != nullptr ? min(a.M, __ldcg(a.count)) : a.M;
+    const gm::Tiling t(M, a.K, a.kblocks, a.bm, a.slots, a.max_splits, a.split_tail);
+    // rows from the first split tile's group on; the whole tiles there are skipped below
+    const int first = a.acc != nullptr ? 0 : t.full / (gm::kGroup * t.tiles_n) * gm::kGroup * a.bm;
+    const int per_row = a.K / 4;
+    const int64_t n4 = (int64_t)(M - first) * per_row;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n4; i += (int64_t)gridDim.x * kThreads) {
-        float4 v = acc[i];
+        const int m = first + (int)(i / per_row), k = 4 * (int)(i % per_row);
+        const int tm = m / a.bm, tile = gm::tile_number(tm, k / gm::kSlotCols, t.tiles_m, t.tiles_n);
+        float4 v;
+        if (tile < t.full) {
+            if (a.acc == nullptr)
+                continue;
+            v = *reinterpret_cast<const float4 *>(a.acc + (int64_t)m * a.K + k);
+        } else {
+            const int64_t copy0 = (int64_t)(tile - t.full) * t.splits;
+            const float *p = a.copies + (copy0 * a.bm + (m - tm * a.bm)) * gm::kSlotCols + k % gm::kSlotCols;
+            const int64_t stride = (int64_t)a.bm * gm::kSlotCols;
+            v = *reinterpret_cast<const float4 *>(p);
 #pragma unroll 4
-        for (int s = 1; s < splits; ++s) {
-            const float4 u = acc[s * split_stride4 + i];
-            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+            for (int s = 1; s < t.splits; ++s) {
+                const float4 u = *reinterpret_cast<const float4 *>(p + s * stride);
+                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+            }
         }
-        dst[i] = make_uint2(to_bf16x2_bits(v.x, v.y), to_bf16x2_bits(v.z, v.w));
+        const int64_t row = a.rows != nullptr ? a.rows[m] : m;
+        *reinterpret_cast<uint2 *>(a.dst + row * a.K + k) =
+            make_uint2(to_bf16x2_bits(v.x, v.y), to_bf16x2_bits(v.z, v.w));
     }
 }
 
@@ -128,17 +226,17 @@ inline cudaError_t launch_loss(const float2 *part, int64_t slices, int64_t M, co
                             stream, part, slices, M, targets, ignore, V, tlogit, loss, lse);
 }
 
-// acc: `splits` blocks of split_rows x K fp32; dst [M, K] bf16.
-inline cudaError_t launch_sum_to_bf16(const float *acc, int splits, int64_t split_rows, int64_t M, int64_t K,
-                                      uint16_t *dst, int num_sms, cudaStream_t stream)
+inline cudaError_t launch_compact(const CompactArgs &a, cudaStream_t stream)
 {
-    const int64_t n4 = M * K / 4;
-    int64_t grid = (n4 + kThreads - 1) / kThreads;
+    return launch_dependent(compact_kernel, dim3((unsigned)((a.M + 31) / 32)), kThreads, 0, stream, a);
+}
+
+inline cudaError_t launch_split_sum(const SumArgs &a, int num_sms, cudaStream_t stream)
+{
+    int64_t grid = ((int64_t)a.M * a.K / 4 + kThreads - 1) / kThreads;
     if (grid > 8 * (int64_t)num_sms)
         grid = 8 * (int64_t)num_sms;
-    return launch_dependent(sum_to_bf16_kernel, dim3((unsigned)grid), kThreads, 0, stream,
-                            reinterpret_cast<const float4 *>(acc), splits, split_rows * K / 4, n4,
-                            reinterpret_cast<uint2 *>(dst));
+    return launch_dependent(split_sum_kernel, dim3((unsigned)grid), kThreads, 0, stream, a);
 }
 
 }  // namespace ce

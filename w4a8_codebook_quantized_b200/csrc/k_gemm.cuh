@@ -76,9 +76,9 @@ struct EpiArgs {
     float *tlogit = nullptr;           // kCeStats: [M], the target's output
     const float *lse = nullptr;        // kCeGrad: [M]
     const float *dloss = nullptr;      // kBf16Rows*: [M], with targets
-    // bf16 modes: the reduction split into so many ranges, each a tile of its
-    // own whose outputs go to rows split * split_rows + row
-    int splits = 1, split_rows = 0;
+    // modes with B as [K, N]: how tiles are spread over the SMs (Tiling)
+    int slots = 1, max_splits = 1, split_tail = 0;
+    const int *count = nullptr;        // the number of rows where it is known on the device only
 
     // The factor of a row of the cross entropy's gradient: dloss, 0 in ignored
     // rows, NaN in rows whose target is outside the vocabulary.
@@ -88,6 +88,72 @@ struct EpiArgs {
         if (t == ignore)
             return 0.0f;
         return t >= 0 && t < V ? dloss[row] : __int_as_float(0x7FC00000);
+    }
+};
+
+constexpr int kSlotCols = 256;  // = BN
+
+// The order of tiles: kGroup tile rows at a time, column by column, so that
+// the tiles in flight (one wave) form a block of about kGroup x 9 tiles and
+// every operand line is wanted by several SMs at about the same time.  Measured
+// against row by row (1): 4096 x 65536 x 4096 cross-entropy gradient 2735 ->
+// 2675 us, the others within 1 percent; 4 and 16 were slower on the gated layer.
+constexpr int kGroup = 8;
+
+__host__ __device__ __forceinline__ void tile_place(int tile, int tiles_m, int tiles_n, int &tm, int &tn)
+{
+    const int per_group = kGroup * tiles_n, g = tile / per_group, r = tile - g * per_group;
+    const int rows = tiles_m - g * kGroup < kGroup ? tiles_m - g * kGroup : kGroup;
+    tn = r / rows;
+    tm = g * kGroup + r - tn * rows;
+}
+
+__host__ __device__ __forceinline__ int tile_number(int tm, int tn, int tiles_m, int tiles_n)
+{
+    const int g = tm / kGroup, rows = tiles_m - g * kGroup < kGroup ? tiles_m - g * kGroup : kGroup;
+    return g * kGroup * tiles_n + tn * rows + tm - g * kGroup;
+}
+
+// The units of work of a contraction with B as [K, N].  A unit is a tile, or
+// one of `splits` ranges of the reduction of a tile of the last, partial wave
+// (all tiles, where they do not fill one wave of `slots` SMs or SM pairs): those
+// ranges run beside one another, each into an fp32 copy of the tile of its own,
+// and split_sum_kernel adds them up in order.  A range of a short last piece of
+// the reduction may be empty.
+struct Tiling {
+    int tiles_m, tiles_n, kblocks, full, splits, units;
+
+    __host__ __device__ Tiling(int M, int N, int kb, int bm, int slots, int max_splits, int split_tail)
+    {
+        tiles_n = (N + kSlotCols - 1) / kSlotCols;
+        kblocks = kb;
+        tiles_m = (M + bm - 1) / bm;
+        const int tiles = tiles_m * tiles_n;
+        const int tail = tiles < slots || split_tail ? tiles % slots : 0;
+        splits = tail ? slots / tail : 1;
+        if (splits > max_splits)
+            splits = max_splits;
+        full = splits > 1 ? tiles - tail : tiles;
+        units = full + (tiles - full) * splits;
+    }
+
+    // A unit's tile and its range [k0, k1) of the reduction's blocks; `copy` is
+    // its fp32 copy's number, -1 for a whole tile.  False: an empty range.
+    __device__ __forceinline__ bool at(int unit, int &tm, int &tn, int &k0, int &k1, int &copy) const
+    {
+        int tile = unit;
+        k0 = 0;
+        k1 = kblocks;
+        copy = -1;
+        if (unit >= full) {
+            copy = unit - full;
+            const int t = copy / splits, s = copy - t * splits;
+            tile = full + t;
+            k0 = (int)((int64_t)kblocks * s / splits);
+            k1 = (int)((int64_t)kblocks * (s + 1) / splits);
+        }
+        tile_place(tile, tiles_m, tiles_n, tm, tn);
+        return k0 < k1;
     }
 };
 
@@ -116,6 +182,8 @@ struct __align__(1024) Smem {
 };
 
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;  // + slack to align the base
+
+static_assert(BN == kSlotCols, "tile width of Tiling");
 
 __device__ __forceinline__ void tile_coords(int tile, int tiles_n, int &tm, int &tn)
 {
@@ -615,13 +683,13 @@ __device__ __forceinline__ void epilogue_ce_grad(uint32_t tbase, int row0, int c
 }
 
 // One tile's epilogue for one warp of the CTA's epilogue warps, by mode:
-// `ew` is the warp's number among them, row0 the first of its 32 rows in the
-// output's row numbering (past M only in the padding of a split reduction),
-// row the calling lane's row.  wait() waits for the accumulator and is called
+// `ew` is the warp's number among them, row0 the first of its 32 rows; out_row0
+// and out_col are where the tile's outputs go (bf16 modes: a split tile's copy
+// has its own place and type).  wait() waits for the accumulator and is called
 // after whatever can be loaded before it; it returns false after an abort.
 template <int MODE, class Sh, class Wait, class Release>
 __device__ __forceinline__ void epilogue_any(Sh &sh, int ew, int buf, uint32_t tbase, int row0, int out_row0,
-                                             int tile_n, int lane, const float *xs, bool has_bias, int M, int N,
+                                             int tile_n, int out_col, int lane, const float *xs, bool has_bias, int M, int N,
                                              int out_f32, int swiglu, int tma_out, const CUtensorMap *tmOut,
                                              uint32_t &units_issued, void *out, int32_t *acc_out, const float *ws,
                                              const float *bias, const EpiArgs &ex, Wait wait, Release release)
@@ -634,7 +702,7 @@ __device__ __forceinline__ void epilogue_any(Sh &sh, int ew, int buf, uint32_t t
             return;
         const float xm = !row_ok ? 0.0f : row_factor(MODE) ? ex.row_scale(row) : is_bf16(MODE) ? 0.0f : xs[row];
         epilogue_tile<is_bf16(MODE), row_factor(MODE), MODE == kBf16RowsAdd>(
-            tbase, out_row0, tile_n * BN, lane, xm, row_ok, wsv, bsv, has_bias, M, N, out_f32, swiglu, tma_out, tmOut,
+            tbase, out_row0, out_col, lane, xm, row_ok, wsv, bsv, has_bias, M, N, out_f32, swiglu, tma_out, tmOut,
             sh.epi[ew], units_issued, out, acc_out, ws, bias, release);
     } else {
         const int c_lo = (ew >> 2) * kEpiCols, col_base = tile_n * BN;
@@ -678,8 +746,9 @@ __device__ __forceinline__ void epilogue_any(Sh &sh, int ew, int buf, uint32_t t
 template <int MODE>
 __global__ void __launch_bounds__(threads(MODE), 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                const __grid_constant__ CUtensorMap tmOut, const float *__restrict__ xs,
-                const float *__restrict__ ws, const float *__restrict__ bias, int M, int N, int K, int out_f32,
+                const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmCopy,
+                const float *__restrict__ xs,
+                const float *__restrict__ ws, const float *__restrict__ bias, int max_rows, int N, int K, int out_f32,
                 int swiglu, int tma_out, void *__restrict__ out, int32_t *__restrict__ acc_out, const EpiArgs ex)
 {
     constexpr bool BF16 = is_bf16(MODE);
@@ -687,26 +756,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     Smem &sh = smem_aligned_1024<Smem>(smem_raw);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
-    const int splits = BF16 ? ex.splits : 1;  // ranges of the reduction
-    const int mn_tiles = tiles_m * tiles_n, num_tiles = mn_tiles * splits;
     constexpr int BKE = BF16 ? BK / 2 : BK;  // K elements per stage
     const int kblocks = (K + BKE - 1) / BKE;
-    // a tile's place and its range [k0, k1) of the reduction's blocks
-    auto coords = [&](int tile, int &tm, int &tn, int &k0, int &k1) {
-        int split = 0;
-        k0 = 0;
-        k1 = kblocks;
-        if constexpr (BF16) {
-            split = tile / mn_tiles;
-            tile -= split * mn_tiles;
-            k0 = (int)((int64_t)kblocks * split / splits);
-            k1 = (int)((int64_t)kblocks * (split + 1) / splits);
-        }
-        tile_coords(tile, tiles_n, tm, tn);
-        return split;
-    };
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sh.full[s], 1);
@@ -731,6 +782,29 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         asm volatile("griddepcontrol.launch_dependents;" :::);
         asm volatile("griddepcontrol.wait;" ::: "memory");
     }
+    // the rows, known on the device only where ex.count is given
+    int M = max_rows;
+    if constexpr (dependent(MODE)) {
+        if (ex.count != nullptr)
+            M = min(M, __ldcg(ex.count));
+    }
+    const Tiling tiling(M, N, kblocks, BM, b_is_kn(MODE) ? ex.slots : 1, b_is_kn(MODE) ? ex.max_splits : 1,
+                        b_is_kn(MODE) ? ex.split_tail : 0);
+    const int num_tiles = tiling.units;
+    auto coords = [&](int unit, int &tm, int &tn, int &k0, int &k1, int &copy) {
+        if constexpr (b_is_kn(MODE)) {
+            return tiling.at(unit, tm, tn, k0, k1, copy);
+        } else {
+            if constexpr (dependent(MODE))
+                tile_place(unit, tiling.tiles_m, tiling.tiles_n, tm, tn);
+            else
+                tile_coords(unit, tiling.tiles_n, tm, tn);
+            k0 = 0;
+            k1 = kblocks;
+            copy = -1;
+            return true;
+        }
+    };
     const uint32_t tmem = sh.tmem_base;
     volatile int *abort = &sh.abort;
 
@@ -747,8 +821,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                 issued[s] = 0, issued_phase[s] = 0;
             bool ok = true;
             for (int tile = blockIdx.x; ok && tile < num_tiles; tile += gridDim.x) {
-                int tm, tn, k0, k1;
-                coords(tile, tm, tn, k0, k1);
+                int tm, tn, k0, k1, copy;
+                if (!coords(tile, tm, tn, k0, k1, copy))
+                    continue;
                 for (int kb = k0; kb < k1; ++kb) {
                     if (!mbar_wait_bounded(&sh.empty[stage], phase ^ 1u, abort)) {
                         ok = false;
@@ -788,7 +863,10 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             uint32_t phase = 0;
             int local = 0;
             bool ok = true;
-            for (int tile = blockIdx.x; ok && tile < num_tiles; tile += gridDim.x, ++local) {
+            for (int tile = blockIdx.x; ok && tile < num_tiles; tile += gridDim.x) {
+                int tm, tn, k0, k1, copy;
+                if (!coords(tile, tm, tn, k0, k1, copy))
+                    continue;
                 const int buf = local & 1;
                 const uint32_t use = (uint32_t)(local >> 1) & 1u;
                 if (!mbar_wait_bounded(&sh.tmem_empty[buf], use ^ 1u, abort)) {
@@ -797,8 +875,6 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * BN);
-                int tm, tn, k0, k1;
-                coords(tile, tm, tn, k0, k1);
                 for (int kb = k0; kb < k1; ++kb) {
                     if (!mbar_wait_bounded(&sh.full[stage], phase, abort)) {
                         ok = false;
@@ -826,6 +902,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                 }
                 if (ok)
                     tc_commit(&sh.tmem_full[buf]);
+                ++local;
             }
         }
     } else {
@@ -846,11 +923,13 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         const int et = threadIdx.x - 64;  // among the epilogue threads
         int local = 0;
         uint32_t units_issued = 0;
-        for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++local) {
-            int tm, tn, k0, k1;
-            const int split = coords(tile, tm, tn, k0, k1);
+        for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
+            int tm, tn, k0, k1, copy;
+            if (!coords(tile, tm, tn, k0, k1, copy))
+                continue;
             const int buf = local & 1;
             const uint32_t use = (uint32_t)(local >> 1) & 1u;
+            ++local;
             if constexpr (!BF16) {
                 for (int j = et; j < BN; j += 32 * epi_warps(MODE)) {
                     const int n = tn * BN + j;
@@ -866,9 +945,10 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             };
             const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * BN);
             const int row0 = tm * BM + 32 * q;
-            epilogue_any<MODE>(sh, warp - 2, buf, tbase, row0, split * ex.split_rows + row0, tn, lane, xs,
-                               bias != nullptr, M, N, out_f32, swiglu, tma_out, &tmOut, units_issued, out, acc_out, ws,
-                               bias, ex, wait, [&]() {
+            const bool whole = copy < 0;  // a whole tile: its outputs have their own place
+            epilogue_any<MODE>(sh, warp - 2, buf, tbase, row0, whole ? row0 : copy * BM + 32 * q, tn,
+                               whole ? tn * BN : 0, lane, xs, bias != nullptr, M, N, whole ? out_f32 : 1, swiglu,
+                               tma_out, whole ? &tmOut : &tmCopy, units_issued, out, acc_out, ws, bias, ex, wait, [&]() {
                               tc_fence_before();
                               __syncwarp();
                               if (lane == 0)
@@ -925,8 +1005,9 @@ constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 template <int MODE>
 __global__ void __launch_bounds__(threads(MODE), 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ CUtensorMap tmOut, const float *__restrict__ xs,
-                     const float *__restrict__ ws, const float *__restrict__ bias, int M, int N, int K, int out_f32,
+                     const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmCopy,
+                const float *__restrict__ xs,
+                     const float *__restrict__ ws, const float *__restrict__ bias, int max_rows, int N, int K, int out_f32,
                      int swiglu, int tma_out, void *__restrict__ out, int32_t *__restrict__ acc_out, const EpiArgs ex)
 {
     constexpr bool BF16 = is_bf16(MODE);
@@ -937,26 +1018,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int npairs = gridDim.x >> 1, pair_id = blockIdx.x >> 1;
-    const int tiles_m = (M + 255) / 256, tiles_n = (N + BN - 1) / BN;
-    const int splits = BF16 ? ex.splits : 1;  // ranges of the reduction
-    const int mn_tiles = tiles_m * tiles_n, num_tiles = mn_tiles * splits;
     constexpr int BKE = BF16 ? BK / 2 : BK;  // K elements per stage
     const int kblocks = (K + BKE - 1) / BKE;
-    // a tile's place and its range [k0, k1) of the reduction's blocks
-    auto coords = [&](int tile, int &tm, int &tn, int &k0, int &k1) {
-        int split = 0;
-        k0 = 0;
-        k1 = kblocks;
-        if constexpr (BF16) {
-            split = tile / mn_tiles;
-            tile -= split * mn_tiles;
-            k0 = (int)((int64_t)kblocks * split / splits);
-            k1 = (int)((int64_t)kblocks * (split + 1) / splits);
-        }
-        tile_coords(tile, tiles_n, tm, tn);
-        return split;
-    };
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < pair::kStages; ++s) {
             mbar_init(&sh.full[s], 1);
@@ -981,6 +1044,29 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         asm volatile("griddepcontrol.launch_dependents;" :::);
         asm volatile("griddepcontrol.wait;" ::: "memory");
     }
+    // the rows, known on the device only where ex.count is given
+    int M = max_rows;
+    if constexpr (dependent(MODE)) {
+        if (ex.count != nullptr)
+            M = min(M, __ldcg(ex.count));
+    }
+    const Tiling tiling(M, N, kblocks, 256, b_is_kn(MODE) ? ex.slots : 1, b_is_kn(MODE) ? ex.max_splits : 1,
+                        b_is_kn(MODE) ? ex.split_tail : 0);
+    const int num_tiles = tiling.units;
+    auto coords = [&](int unit, int &tm, int &tn, int &k0, int &k1, int &copy) {
+        if constexpr (b_is_kn(MODE)) {
+            return tiling.at(unit, tm, tn, k0, k1, copy);
+        } else {
+            if constexpr (dependent(MODE))
+                tile_place(unit, tiling.tiles_m, tiling.tiles_n, tm, tn);
+            else
+                tile_coords(unit, tiling.tiles_n, tm, tn);
+            k0 = 0;
+            k1 = kblocks;
+            copy = -1;
+            return true;
+        }
+    };
     const uint32_t tmem = sh.tmem_base;
     volatile int *abort = &sh.abort;
 
@@ -997,8 +1083,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                 issued[s] = 0, issued_phase[s] = 0;
             bool ok = true;
             for (int tile = pair_id; ok && tile < num_tiles; tile += npairs) {
-                int tm, tn, k0, k1;
-                coords(tile, tm, tn, k0, k1);
+                int tm, tn, k0, k1, copy;
+                if (!coords(tile, tm, tn, k0, k1, copy))
+                    continue;
                 for (int kb = k0; kb < k1; ++kb) {
                     if (!mbar_wait_bounded(&sh.empty[stage], phase ^ 1u, abort)) {
                         ok = false;
@@ -1050,7 +1137,10 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             int local = 0;
             bool ok = true;
             const uint32_t peer = 1;
-            for (int tile = pair_id; ok && tile < num_tiles; tile += npairs, ++local) {
+            for (int tile = pair_id; ok && tile < num_tiles; tile += npairs) {
+                int tm, tn, k0, k1, copy;
+                if (!coords(tile, tm, tn, k0, k1, copy))
+                    continue;
                 const int buf = local & 1;
                 const uint32_t use = (uint32_t)(local >> 1) & 1u;
                 if (!mbar_wait_bounded(&sh.tmem_empty[buf], use ^ 1u, abort)) {
@@ -1059,8 +1149,6 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * BN);
-                int tm, tn, k0, k1;
-                coords(tile, tm, tn, k0, k1);
                 for (int kb = k0; kb < k1; ++kb) {
                     if (!mbar_wait_bounded(&sh.full[stage], phase, abort)) {
                         ok = false;
@@ -1094,6 +1182,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                     tc_commit_pair(mapa_shared(f, 0));
                     tc_commit_pair(mapa_shared(f, peer));
                 }
+                ++local;
             }
         }
     } else {
@@ -1102,11 +1191,13 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         const int et = threadIdx.x - 64;
         int local = 0;
         uint32_t units_issued = 0;
-        for (int tile = pair_id; tile < num_tiles; tile += npairs, ++local) {
-            int tm, tn, k0, k1;
-            const int split = coords(tile, tm, tn, k0, k1);
+        for (int tile = pair_id; tile < num_tiles; tile += npairs) {
+            int tm, tn, k0, k1, copy;
+            if (!coords(tile, tm, tn, k0, k1, copy))
+                continue;
             const int buf = local & 1;
             const uint32_t use = (uint32_t)(local >> 1) & 1u;
+            ++local;
             if constexpr (!BF16) {
                 for (int j = et; j < BN; j += 32 * epi_warps(MODE)) {
                     const int n = tn * BN + j;
@@ -1123,9 +1214,10 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             const int row0 = tm * 256 + (int)rank * 128 + 32 * q;
             const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * BN);
             const uint32_t release_addr = mapa_shared(smem_u32(&sh.tmem_empty[buf]), 0);
-            epilogue_any<MODE>(sh, warp - 2, buf, tbase, row0, split * ex.split_rows + row0, tn, lane, xs,
-                               bias != nullptr, M, N, out_f32, swiglu, tma_out, &tmOut, units_issued, out, acc_out, ws,
-                               bias, ex, wait, [&]() {
+            const bool whole = copy < 0;  // a whole tile: its outputs have their own place
+            epilogue_any<MODE>(sh, warp - 2, buf, tbase, row0, whole ? row0 : copy * 256 + (int)rank * 128 + 32 * q, tn,
+                               whole ? tn * BN : 0, lane, xs, bias != nullptr, M, N, whole ? out_f32 : 1, swiglu,
+                               tma_out, whole ? &tmOut : &tmCopy, units_issued, out, acc_out, ws, bias, ex, wait, [&]() {
                               tc_fence_before();
                               __syncwarp();
                               if (lane == 0)
