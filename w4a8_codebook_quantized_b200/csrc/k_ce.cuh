@@ -183,21 +183,32 @@ __global__ void __launch_bounds__(kThreads) split_sum_kernel(const SumArgs a)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int M = a.count != nullptr ? min(a.M, __ldcg(a.count)) : a.M;
     const gm::Tiling t(M, a.K, a.kblocks, a.bm, a.slots, a.max_splits, a.split_tail);
-    // rows from the first split tile's group on; the whole tiles there are skipped below
-    const int first = a.acc != nullptr ? 0 : t.full / (gm::kGroup * t.tiles_n) * gm::kGroup * a.bm;
+    constexpr int kTileQuads = gm::kSlotCols / 4;  // float4s of a copy's row
     const int per_row = a.K / 4;
-    const int64_t n4 = (int64_t)(M - first) * per_row;
+    const int64_t n4 = a.acc != nullptr ? (int64_t)M * per_row
+                                        : (int64_t)(t.units - t.full) / t.splits * a.bm * kTileQuads;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n4; i += (int64_t)gridDim.x * kThreads) {
-        const int m = first + (int)(i / per_row), k = 4 * (int)(i % per_row);
-        const int tm = m / a.bm, tile = gm::tile_number(tm, k / gm::kSlotCols, t.tiles_m, t.tiles_n);
+        int m, k, tile;
+        if (a.acc != nullptr) {
+            m = (int)(i / per_row);
+            k = 4 * (int)(i - (int64_t)m * per_row);
+            tile = gm::tile_number(m / a.bm, k / gm::kSlotCols, t.tiles_m, t.tiles_n);
+        } else {
+            int tm, tn;
+            const int r = (int)(i / kTileQuads);  // row among the split tiles' rows
+            tile = t.full + r / a.bm;
+            gm::tile_place(tile, t.tiles_m, t.tiles_n, tm, tn);
+            m = tm * a.bm + r % a.bm;
+            k = tn * gm::kSlotCols + 4 * (int)(i % kTileQuads);
+            if (m >= M)
+                continue;
+        }
         float4 v;
         if (tile < t.full) {
-            if (a.acc == nullptr)
-                continue;
             v = *reinterpret_cast<const float4 *>(a.acc + (int64_t)m * a.K + k);
         } else {
             const int64_t copy0 = (int64_t)(tile - t.full) * t.splits;
-            const float *p = a.copies + (copy0 * a.bm + (m - tm * a.bm)) * gm::kSlotCols + k % gm::kSlotCols;
+            const float *p = a.copies + (copy0 * a.bm + m % a.bm) * gm::kSlotCols + k % gm::kSlotCols;
             const int64_t stride = (int64_t)a.bm * gm::kSlotCols;
             v = *reinterpret_cast<const float4 *>(p);
 #pragma unroll 4
