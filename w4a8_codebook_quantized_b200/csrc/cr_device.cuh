@@ -558,6 +558,17 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t cluster_addr)
                  : "memory");
 }
 
+// The same on the barrier at this offset in both CTAs of the pair, in one
+// instruction.
+__device__ __forceinline__ void tc_commit_both(uint32_t cta_addr)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            cta_addr),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
 // D[tmem] (+)= A x B^T over the CTA pair: M = 256 (128 rows of A from each
 // CTA's shared memory at the descriptor's offset), B split the same way.
 __device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -600,20 +611,27 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr)
     return d;
 }
 
-// Shared-memory matrix descriptor for an MN-major operand tile of 16-bit
-// elements in the 128-byte-swizzled canonical layout: rows of 64 consecutive
-// MN elements (128 bytes), one row per K index, 8-row atoms of 1024 bytes
-// stacked along K (stride-dimension byte offset 1024), the next 64 MN elements
-// `mn_stride` bytes on (leading-dimension byte offset).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t mn_stride)
+// A shared-memory matrix descriptor from its low word (start address, leading
+// byte offset; sw128_kmajor_desc has the fields), to which an offset of n bytes inside the tile adds n / 16:
+// the high word is the same for every tile (stride 1024, version 1, 128-byte
+// swizzle).  The issuing thread has some 500 cycles for a block of four MMAs and
+// shares its scheduler with the epilogue, so it builds no descriptor from parts.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t lo)
 {
-    uint64_t d = 0;
-    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(mn_stride >> 4) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"((1024u >> 4) | (1u << 14) | (2u << 29)));
     return d;
+}
+
+// K-major, as sw128_kmajor_desc; an address below 256 KB fits the field.
+__device__ __forceinline__ uint32_t sw128_kmajor_lo(uint32_t smem_addr) { return (smem_addr >> 4) | (1u << 16); }
+
+// MN-major, 16-bit elements: rows of 64 consecutive MN elements (128 bytes),
+// one row per K index, 8-row atoms of 1024 bytes stacked along K (the stride
+// offset), the next 64 MN elements `mn_stride` bytes on (the leading offset).
+__device__ __forceinline__ uint32_t sw128_mnmajor_lo(uint32_t smem_addr, uint32_t mn_stride)
+{
+    return (smem_addr >> 4) | ((mn_stride >> 4) << 16);
 }
 
 // Instruction descriptor for kind::i8: s32 accumulator, signed A and B, both

@@ -815,10 +815,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             prefetch_tmap(&tmB);
             int stage = 0;
             uint32_t phase = 0;
-            int issued[kStages];
-            uint32_t issued_phase[kStages];
-            for (int s = 0; s < kStages; ++s)
-                issued[s] = 0, issued_phase[s] = 0;
+            uint32_t issued = 0;  // stages filled so far
             bool ok = true;
             for (int tile = blockIdx.x; ok && tile < num_tiles; tile += gridDim.x) {
                 int tm, tn, k0, k1, copy;
@@ -839,8 +836,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                     } else {
                         tma_load_2d(sh.stage[stage] + kABytes, &tmB, kb * BKE, tn * BN, &sh.full[stage]);
                     }
-                    issued[stage] = 1;
-                    issued_phase[stage] = phase;
+                    ++issued;
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -849,11 +845,10 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             }
             if (!ok) {
                 // Let copies already in flight land before the CTA goes away.
-                for (int s = 0; s < kStages; ++s)
-                    if (issued[s]) {
-                        volatile int no_abort = 0;
-                        mbar_wait_bounded(&sh.full[s], issued_phase[s], &no_abort, 20000000ull);
-                    }
+                for (uint32_t s = 0; s < kStages && s < issued; ++s) {
+                    volatile int no_abort = 0;
+                    mbar_wait_bounded(&sh.full[s], ((issued - 1 - s) / kStages) & 1u, &no_abort, 20000000ull);
+                }
             }
         }
     } else if (warp == 1) {
@@ -863,6 +858,12 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             uint32_t phase = 0;
             int local = 0;
             bool ok = true;
+            // descriptors of stage 0; 16 terms (32 bytes of a K-major row, 16 rows
+            // of an MN-major box) on per MMA
+            const uint32_t a_lo = sw128_kmajor_lo(smem_u32(sh.stage[0]));
+            const uint32_t b_addr = smem_u32(sh.stage[0]) + kABytes;
+            const uint32_t b_lo = b_is_kn(MODE) ? sw128_mnmajor_lo(b_addr, kKnBytes) : sw128_kmajor_lo(b_addr);
+            constexpr uint32_t kBStep = b_is_kn(MODE) ? 2048 >> 4 : 32 >> 4;
             for (int tile = blockIdx.x; ok && tile < num_tiles; tile += gridDim.x) {
                 int tm, tn, k0, k1, copy;
                 if (!coords(tile, tm, tn, k0, k1, copy))
@@ -881,18 +882,15 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(sh.stage[stage]);
-                    const uint32_t b_addr = a_addr + kABytes;
+                    const uint32_t st = (uint32_t)stage * (kStageBytes >> 4);
 #pragma unroll
                     for (int kk = 0; kk < BK / 32; ++kk) {
-                        const uint64_t ad = sw128_kmajor_desc(a_addr + 32u * kk);
-                        // 16 terms: 32 bytes along a K-major row, 16 rows of an MN-major box
-                        const uint64_t bd = b_is_kn(MODE) ? sw128_mnmajor_desc(b_addr + 2048u * kk, kKnBytes)
-                                                          : sw128_kmajor_desc(b_addr + 32u * kk);
+                        const uint64_t ad = sw128_desc(a_lo + st + 2u * kk);
+                        const uint64_t bd = sw128_desc(b_lo + st + kBStep * kk);
                         if constexpr (BF16)
-                            mma_bf16(d, ad, bd, idesc_bf16(BM, BN, b_is_kn(MODE)), ((kb - k0) | kk) != 0 ? 1u : 0u);
+                            mma_bf16(d, ad, bd, idesc_bf16(BM, BN, b_is_kn(MODE)), kk == 0 ? kb != k0 : 1u);
                         else
-                            mma_i8(d, ad, bd, kIdesc, ((kb - k0) | kk) != 0 ? 1u : 0u);
+                            mma_i8(d, ad, bd, kIdesc, kk == 0 ? kb != k0 : 1u);
                     }
                     tc_commit(&sh.empty[stage]);
                     if (++stage == kStages) {
@@ -1075,12 +1073,10 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         if (lane == 0) {
             prefetch_tmap(&tmA);
             prefetch_tmap(&tmB);
+            const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0);  // the leader's
             int stage = 0;
             uint32_t phase = 0;
-            int issued[pair::kStages];
-            uint32_t issued_phase[pair::kStages];
-            for (int s = 0; s < pair::kStages; ++s)
-                issued[s] = 0, issued_phase[s] = 0;
+            uint32_t issued = 0;  // stages filled so far
             bool ok = true;
             for (int tile = pair_id; ok && tile < num_tiles; tile += npairs) {
                 int tm, tn, k0, k1, copy;
@@ -1091,7 +1087,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                         ok = false;
                         break;
                     }
-                    const uint32_t full_leader = mapa_shared(smem_u32(&sh.full[stage]), 0);
+                    const uint32_t full_leader = full0 + 8u * (uint32_t)stage;
                     if (leader)
                         mbar_arrive_expect_tx(&sh.full[stage], 2 * pair::kStageBytes);
                     tma_load_2d_pair(sh.stage[stage], &tmA, kb * BKE, tm * 256 + (int)rank * 128, full_leader);
@@ -1104,8 +1100,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                         tma_load_2d_pair(sh.stage[stage] + pair::kHalfBytes, &tmB, kb * BKE,
                                          tn * BN + (int)rank * 128, full_leader);
                     }
-                    issued[stage] = 1;
-                    issued_phase[stage] = phase;
+                    ++issued;
                     if (++stage == pair::kStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -1117,11 +1112,11 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                 // waits on its barriers (bounded); the partner, whose copies
                 // signal the leader, waits a fixed 100 us
                 if (leader) {
-                    for (int s = 0; s < pair::kStages; ++s)
-                        if (issued[s]) {
-                            volatile int no_abort = 0;
-                            mbar_wait_bounded(&sh.full[s], issued_phase[s], &no_abort, 20000000ull);
-                        }
+                    for (uint32_t s = 0; s < pair::kStages && s < issued; ++s) {
+                        volatile int no_abort = 0;
+                        mbar_wait_bounded(&sh.full[s], ((issued - 1 - s) / pair::kStages) & 1u, &no_abort,
+                                          20000000ull);
+                    }
                 } else {
                     const uint64_t t0 = globaltimer_ns();
                     while (globaltimer_ns() - t0 < 100000ull) {
@@ -1136,7 +1131,12 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             uint32_t phase = 0;
             int local = 0;
             bool ok = true;
-            const uint32_t peer = 1;
+            // descriptors of stage 0; 16 terms (32 bytes of a K-major row, 16 rows
+            // of an MN-major box) on per MMA
+            const uint32_t a_lo = sw128_kmajor_lo(smem_u32(sh.stage[0]));
+            const uint32_t b_addr = smem_u32(sh.stage[0]) + pair::kHalfBytes;
+            const uint32_t b_lo = b_is_kn(MODE) ? sw128_mnmajor_lo(b_addr, kKnBytes) : sw128_kmajor_lo(b_addr);
+            constexpr uint32_t kBStep = b_is_kn(MODE) ? 2048 >> 4 : 32 >> 4;
             for (int tile = pair_id; ok && tile < num_tiles; tile += npairs) {
                 int tm, tn, k0, k1, copy;
                 if (!coords(tile, tm, tn, k0, k1, copy))
@@ -1155,33 +1155,24 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(sh.stage[stage]);
-                    const uint32_t b_addr = a_addr + pair::kHalfBytes;
+                    const uint32_t st = (uint32_t)stage * (pair::kStageBytes >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < BK / 32; ++kk)
+                    for (int kk = 0; kk < BK / 32; ++kk) {
+                        const uint64_t ad = sw128_desc(a_lo + st + 2u * kk);
+                        const uint64_t bd = sw128_desc(b_lo + st + kBStep * kk);
                         if constexpr (BF16)
-                            mma_bf16_pair(d, sw128_kmajor_desc(a_addr + 32u * kk),
-                                          b_is_kn(MODE) ? sw128_mnmajor_desc(b_addr + 2048u * kk, kKnBytes)
-                                                        : sw128_kmajor_desc(b_addr + 32u * kk),
-                                          idesc_bf16(256, BN, b_is_kn(MODE)),
-                                          ((kb - k0) | kk) != 0 ? 1u : 0u);
+                            mma_bf16_pair(d, ad, bd, idesc_bf16(256, BN, b_is_kn(MODE)), kk == 0 ? kb != k0 : 1u);
                         else
-                            mma_i8_pair(d, sw128_kmajor_desc(a_addr + 32u * kk),
-                                        sw128_kmajor_desc(b_addr + 32u * kk), pair::kIdesc,
-                                        ((kb - k0) | kk) != 0 ? 1u : 0u);
-                    const uint32_t e = smem_u32(&sh.empty[stage]);
-                    tc_commit_pair(mapa_shared(e, 0));
-                    tc_commit_pair(mapa_shared(e, peer));
+                            mma_i8_pair(d, ad, bd, pair::kIdesc, kk == 0 ? kb != k0 : 1u);
+                    }
+                    tc_commit_both(smem_u32(&sh.empty[0]) + 8u * (uint32_t)stage);
                     if (++stage == pair::kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                if (ok) {
-                    const uint32_t f = smem_u32(&sh.tmem_full[buf]);
-                    tc_commit_pair(mapa_shared(f, 0));
-                    tc_commit_pair(mapa_shared(f, peer));
-                }
+                if (ok)
+                    tc_commit_both(smem_u32(&sh.tmem_full[buf]));
                 ++local;
             }
         }
