@@ -65,6 +65,14 @@ constexpr bool dependent(int mode) { return mode != kI8 && mode != kBf16; }
 constexpr int epi_warps(int mode) { return mode == kSwigluGrad || mode == kCeStats || mode == kCeGrad ? 8 : 4; }
 constexpr int threads(int mode) { return 64 + 32 * epi_warps(mode); }
 
+// Where a tile's column j has its scale and bias in shared memory: for the
+// gated gradient in the order gate, gate, up, up of two pairs of columns.
+template <int MODE>
+__device__ __forceinline__ int stage_column(int j)
+{
+    return MODE == kSwigluGrad && ((j & 3) == 1 || (j & 3) == 2) ? j ^ 3 : j;
+}
+
 // What the epilogues beyond the layer's own read and write.
 struct EpiArgs {
     const uint16_t *dout = nullptr;    // kSwigluGrad: [M, N / 2] bf16
@@ -451,39 +459,74 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_
     }
 }
 
-// The 32 fp32 outputs of accumulator columns [c0, c0 + 32) of one row, as the
-// layer's epilogue computes them (wsv, bsv: the tile's channel scales and bias).
-__device__ __forceinline__ void outputs32(const uint32_t (&v)[32], int c0, float xm, const float *wsv,
-                                          const float *bsv, bool has_bias, float (&y)[32])
+// The epilogues beyond the layer's own work on pairs of values in packed fp32x2
+// arithmetic (each half rounded as the scalar instruction rounds it): their
+// warps share the schedulers with the thread that issues the MMAs, and what
+// they do not issue, it can.
+
+// Two fp32 outputs of a row as the layer's epilogue computes them, from their
+// accumulators and the channels' scales (and bias).
+__device__ __forceinline__ uint64_t output_pair(uint32_t a, uint32_t b, uint64_t xm2, uint64_t w2, uint64_t b2,
+                                                bool has_bias)
+{
+    const uint64_t acc = pack2(__float_as_uint(__int2float_rn((int32_t)a)), __float_as_uint(__int2float_rn((int32_t)b)));
+    const uint64_t y = mul2(acc, mul2(xm2, w2));
+    return has_bias ? add2(y, b2) : y;
+}
+
+// The 32 outputs of accumulator columns [c0, c0 + 32) of one row, neighbours
+// paired (wsv, bsv: the tile's channel scales and bias).
+__device__ __forceinline__ void outputs32(const uint32_t (&v)[32], int c0, uint64_t xm2, const float *wsv,
+                                          const float *bsv, bool has_bias, uint64_t (&y)[16])
 {
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        const float4 w4 = *reinterpret_cast<const float4 *>(wsv + c0 + j);
-        const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            y[j + e] = __fmul_rn(__int2float_rn((int32_t)v[j + e]), __fmul_rn(xm, wv[e]));
-        if (has_bias) {
-            const float4 b4 = *reinterpret_cast<const float4 *>(bsv + c0 + j);
-            const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                y[j + e] = __fadd_rn(y[j + e], bv[e]);
-        }
+    for (int j = 0; j < 8; ++j) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(wsv + c0 + 4 * j);
+        ulonglong2 b = make_ulonglong2(0ull, 0ull);
+        if (has_bias)
+            b = *reinterpret_cast<const ulonglong2 *>(bsv + c0 + 4 * j);
+        y[2 * j] = output_pair(v[4 * j], v[4 * j + 1], xm2, w.x, b.x, has_bias);
+        y[2 * j + 1] = output_pair(v[4 * j + 2], v[4 * j + 3], xm2, w.y, b.y, has_bias);
     }
 }
 
-// Gradient of silu(g) * u with respect to g and u, for the gradient d of the
-// product: with s = sigmoid(g), du = d g s and dg = d u s (1 + g (1 - s)).
-// t = e^-|g| lies in (0, 1], so the divisor of the fast division lies in
-// [1, 2] (at most 2 ulp), as in swiglu_value.
-__device__ __forceinline__ uint32_t swiglu_grad(float g, float u, float d)
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x by the special-function unit (2 ulp; 0 for x = -inf, inf for +inf).
+__device__ __forceinline__ float ex2(float x)
 {
-    const float t = expf(-fabsf(g));
-    const float r = __fdividef(1.0f, 1.0f + t), q = t * r;
-    const float s = g >= 0.0f ? r : q, os = g >= 0.0f ? q : r;  // sigmoid and 1 - sigmoid
-    const float ds = d * s;
-    return to_bf16x2_bits(ds * u * (1.0f + g * os), ds * g);
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / x by the special-function unit (1 ulp; 0 for x = +inf).
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Gradients of silu(g) * u for the gradients d of two such products: with
+// s = sigmoid(g), du = d g s and dg = d u s (1 + g (1 - s)), returned as (dg, du)
+// in bf16 for each.  s = 1 / (1 + 2^(-g log2 e)) is 0 where the power
+// overflows (g below -88).  1 - s is taken as a difference: its error, 2^-24,
+// is relative to the 1 that g (1 - s) is added to.
+__device__ __forceinline__ void swiglu_grad2(uint64_t g, uint64_t u, uint64_t d, uint32_t &z0, uint32_t &z1)
+{
+    const uint64_t one = pair_both(1.0f);
+    const uint64_t x = mul2(g, pair_both(-kLog2e));
+    const uint64_t den = add2(one, pack2(__float_as_uint(ex2(lo_of(x))), __float_as_uint(ex2(hi_of(x)))));
+    const uint64_t s = pack2(__float_as_uint(rcp(lo_of(den))), __float_as_uint(rcp(hi_of(den))));
+    const uint64_t ds = mul2(d, s);
+    const uint64_t dg = mul2(mul2(ds, u), fma2(g, sub2(one, s), one));
+    const uint64_t du = mul2(ds, g);
+    z0 = to_bf16x2_bits(lo_of(dg), lo_of(du));
+    z1 = to_bf16x2_bits(hi_of(dg), hi_of(du));
 }
 
 // Sixteen bf16 of a row of dout as eight words, columns [f0, f0 + 16) of
@@ -518,6 +561,7 @@ __device__ __forceinline__ void epilogue_swiglu_grad(uint32_t tbase, int row0, i
                                                      Release release)
 {
     const int F = N >> 1;
+    const uint64_t xm2 = pair_both(xm);
     const uint16_t *drow = ex.dout + (int64_t)(row0 + lane) * F;
 #pragma unroll 1
     for (int c0 = c_lo; c0 < c_lo + kEpiCols; c0 += 32) {
@@ -532,26 +576,21 @@ __device__ __forceinline__ void epilogue_swiglu_grad(uint32_t tbase, int row0, i
         tmem_ld_wait();
         if (c0 + 32 == c_lo + kEpiCols)
             release();
-        float y[32];
-        outputs32(cur, c0, xm, wsv, bsv, has_bias, y);
+        // the tile's scales are staged with the middle two of four columns
+        // exchanged (stage_column), so that gates and ups pair with their like
 #pragma unroll
-        for (int p = 0; p < 16; ++p) {
-            const float dv = __uint_as_float((p & 1) ? d[p >> 1] & 0xFFFF0000u : d[p >> 1] << 16);
-            packed[p] = swiglu_grad(y[2 * p], y[2 * p + 1], dv);
+        for (int p = 0; p < 8; ++p) {
+            const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(wsv + c0 + 4 * p);
+            ulonglong2 b = make_ulonglong2(0ull, 0ull);
+            if (has_bias)
+                b = *reinterpret_cast<const ulonglong2 *>(bsv + c0 + 4 * p);
+            const uint64_t g = output_pair(cur[4 * p], cur[4 * p + 2], xm2, w.x, b.x, has_bias);
+            const uint64_t u = output_pair(cur[4 * p + 1], cur[4 * p + 3], xm2, w.y, b.y, has_bias);
+            swiglu_grad2(g, u, pack2(d[p] << 16, d[p] & 0xFFFF0000u), packed[2 * p], packed[2 * p + 1]);
         }
         if (col_base + c0 < N)
             store_half_unit(packed, col_base + c0, row0, lane, tmOut, stage_buf, units_issued);
     }
-}
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-// 2^x by the special-function unit (2 ulp; 0 for x = -inf, inf for +inf).
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // A row's sum of exponentials as a pair: the reference (its maximum in the
@@ -580,7 +619,9 @@ __device__ __forceinline__ float2 epilogue_ce_stats(uint32_t tbase, int row, int
     const float kNegInf = __int_as_float(0xFF800000);
     const int64_t t = row_ok ? ex.targets[row] : -1, lo = (int64_t)ex.n0 + col_base + c_lo;
     const int tcol = (t >= lo && t < lo + kEpiCols && t - ex.n0 < N) ? c_lo + (int)(t - lo) : -1;
-    float ref = kNegInf, s0 = 0.0f, s1 = 0.0f, tl = 0.0f;
+    const uint64_t xm2 = pair_both(xm);
+    float ref = kNegInf, tl = 0.0f;
+    uint64_t s = 0ull;
 #pragma unroll 1
     for (int c0 = c_lo; c0 < c_lo + kEpiCols; c0 += 32) {
         uint32_t cur[32];
@@ -589,41 +630,43 @@ __device__ __forceinline__ float2 epilogue_ce_stats(uint32_t tbase, int row, int
         tmem_ld_wait();
         if (c0 + 32 == c_lo + kEpiCols)
             release();
-        float y[32];
-        outputs32(cur, c0, xm, wsv, bsv, has_bias, y);
+        uint64_t y[16];
+        outputs32(cur, c0, xm2, wsv, bsv, has_bias, y);
         if (col_base + c0 + 32 > N) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (col_base + c0 + j >= N)
-                    y[j] = kNegInf;
+            for (int j = 0; j < 16; ++j)
+                y[j] = pack2(col_base + c0 + 2 * j < N ? (uint32_t)y[j] : __float_as_uint(kNegInf),
+                          col_base + c0 + 2 * j + 1 < N ? (uint32_t)(y[j] >> 32) : __float_as_uint(kNegInf));
         }
         if (tcol >= c0 && tcol < c0 + 32) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (tcol == c0 + j)
-                    tl = y[j];
+            for (int j = 0; j < 16; ++j) {
+                if (tcol == c0 + 2 * j)
+                    tl = lo_of(y[j]);
+                if (tcol == c0 + 2 * j + 1)
+                    tl = hi_of(y[j]);
+            }
         }
-        float m0 = y[0], m1 = y[1];
+        float m0 = lo_of(y[0]), m1 = hi_of(y[0]);
 #pragma unroll
-        for (int j = 2; j < 32; j += 2) {
-            m0 = fmaxf(m0, y[j]);
-            m1 = fmaxf(m1, y[j + 1]);
+        for (int j = 1; j < 16; ++j) {
+            m0 = fmaxf(m0, lo_of(y[j]));
+            m1 = fmaxf(m1, hi_of(y[j]));
         }
         const float next = fmaxf(ref, __fmul_rn(fmaxf(m0, m1), kLog2e));
         const float base = next == kNegInf ? 0.0f : next;
-        const float scale = ex2(ref - base);  // 0 at the first chunk
-        s0 *= scale;
-        s1 *= scale;
+        s = mul2(s, pair_both(ex2(ref - base)));  // times 0 at the first chunk
+        const uint64_t l2 = pair_both(kLog2e), nb = pair_both(-base);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-            s0 += ex2(__fmaf_rn(y[j], kLog2e, -base));
-            s1 += ex2(__fmaf_rn(y[j + 1], kLog2e, -base));
+        for (int j = 0; j < 16; ++j) {
+            const uint64_t x = fma2(y[j], l2, nb);
+            s = add2(s, pack2(__float_as_uint(ex2(lo_of(x))), __float_as_uint(ex2(hi_of(x)))));
         }
         ref = next;
     }
     if (tcol >= 0)
         ex.tlogit[row] = tl;
-    return make_float2(ref, s0 + s1);
+    return make_float2(ref, lo_of(s) + hi_of(s));
 }
 
 // Epilogue of kCeGrad: dl[m, n] = e^(y - lse[m]) - [n = target], zero for
@@ -649,6 +692,7 @@ __device__ __forceinline__ void epilogue_ce_grad(uint32_t tbase, int row0, int c
             tcol = (t >= lo && t < lo + BN) ? (int)(t - lo) : -1;
         }
     }
+    const uint64_t xm2 = pair_both(xm), nlse = pair_both(-lse2);
 #pragma unroll 1
     for (int c0 = c_lo; c0 < c_lo + kEpiCols; c0 += 32) {
         uint32_t cur[32], packed[16];
@@ -657,26 +701,28 @@ __device__ __forceinline__ void epilogue_ce_grad(uint32_t tbase, int row0, int c
         tmem_ld_wait();
         if (c0 + 32 == c_lo + kEpiCols)
             release();
-        float y[32];
-        outputs32(cur, c0, xm, wsv, bsv, has_bias, y);
+        uint64_t y[16];
+        outputs32(cur, c0, xm2, wsv, bsv, has_bias, y);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            y[j] = ex2(__fmaf_rn(y[j], kLog2e, -lse2));
+        for (int j = 0; j < 16; ++j) {
+            const uint64_t x = fma2(y[j], pair_both(kLog2e), nlse);
+            y[j] = pack2(__float_as_uint(ex2(lo_of(x))), __float_as_uint(ex2(hi_of(x))));
+        }
         if (tcol >= c0 && tcol < c0 + 32) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (tcol == c0 + j)
-                    y[j] -= 1.0f;
+            for (int j = 0; j < 16; ++j)
+                y[j] = add2(y[j], pack2(tcol == c0 + 2 * j ? __float_as_uint(-1.0f) : 0u,
+                                        tcol == c0 + 2 * j + 1 ? __float_as_uint(-1.0f) : 0u));
         }
         if (col_base + c0 + 32 > N) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (col_base + c0 + j >= N)
-                    y[j] = 0.0f;
+            for (int j = 0; j < 16; ++j)
+                y[j] = pack2(col_base + c0 + 2 * j < N ? (uint32_t)y[j] : 0u,
+                          col_base + c0 + 2 * j + 1 < N ? (uint32_t)(y[j] >> 32) : 0u);
         }
 #pragma unroll
         for (int p = 0; p < 16; ++p)
-            packed[p] = to_bf16x2_bits(y[2 * p], y[2 * p + 1]);
+            packed[p] = to_bf16x2_bits(lo_of(y[p]), hi_of(y[p]));
         if (col_base + c0 < N)
             store_half_unit(packed, col_base + c0, row0, lane, tmOut, stage_buf, units_issued);
     }
@@ -930,9 +976,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             ++local;
             if constexpr (!BF16) {
                 for (int j = et; j < BN; j += 32 * epi_warps(MODE)) {
-                    const int n = tn * BN + j;
-                    sh.wsb[buf][j] = n < N ? ws[n] : 0.0f;
-                    sh.biasb[buf][j] = (bias != nullptr && n < N) ? bias[n] : 0.0f;
+                    const int n = tn * BN + j, at = stage_column<MODE>(j);
+                    sh.wsb[buf][at] = n < N ? ws[n] : 0.0f;
+                    sh.biasb[buf][at] = (bias != nullptr && n < N) ? bias[n] : 0.0f;
                 }
             }
             asm volatile("bar.sync 2, %0;" ::"n"(32 * epi_warps(MODE)) : "memory");
@@ -1191,9 +1237,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             ++local;
             if constexpr (!BF16) {
                 for (int j = et; j < BN; j += 32 * epi_warps(MODE)) {
-                    const int n = tn * BN + j;
-                    sh.wsb[buf][j] = n < N ? ws[n] : 0.0f;
-                    sh.biasb[buf][j] = (bias != nullptr && n < N) ? bias[n] : 0.0f;
+                    const int n = tn * BN + j, at = stage_column<MODE>(j);
+                    sh.wsb[buf][at] = n < N ? ws[n] : 0.0f;
+                    sh.biasb[buf][at] = (bias != nullptr && n < N) ? bias[n] : 0.0f;
                 }
             }
             asm volatile("bar.sync 2, %0;" ::"n"(32 * epi_warps(MODE)) : "memory");

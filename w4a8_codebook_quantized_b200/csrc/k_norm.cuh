@@ -171,13 +171,11 @@ __device__ __forceinline__ void load_gamma_pairs(const void *gamma, int64_t k, u
     load_gamma16<GBF16>(gamma, k, f);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        g[i] = rq::pk(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]));
+        g[i] = pack2(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]));
 }
 
 // Both bf16 values of a word as an fp32 pair.
-__device__ __forceinline__ uint64_t pair_of(uint32_t w) { return rq::pk(w << 16, w & 0xFFFF0000u); }
-
-__device__ __forceinline__ uint64_t pair_both(float v) { return rq::pk(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ uint64_t pair_of(uint32_t w) { return pack2(w << 16, w & 0xFFFF0000u); }
 
 // The maximum over the CTA of a non-negative, NaN-free value.
 template <int THREADS>
@@ -417,7 +415,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_pairs_kernel(const FwdArgs a)
             load_h(p, w0[0], w1[0]);
     }
     const float rs = row_rs<THREADS>(ss, a.inv_k, a.eps, warp_ss);
-    const uint64_t rs2 = rq::pk(__float_as_uint(rs), __float_as_uint(rs));
+    const uint64_t rs2 = pack2(__float_as_uint(rs), __float_as_uint(rs));
 
     uint64_t v[kHeld][16];
     auto rotate = [&](int p, const uint32_t (&u0)[8], const uint32_t (&u1)[8], uint64_t (&vj)[16]) {
@@ -433,11 +431,11 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_pairs_kernel(const FwdArgs a)
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint64_t lo = rq::pk(u0[i] << 16, u1[i] << 16);
-            const uint64_t hi = rq::pk(u0[i] & 0xFFFF0000u, u1[i] & 0xFFFF0000u);
-            vj[2 * i] = rq::mul2(rq::mul2(lo, rs2), rq::pk(__float_as_uint(g0[2 * i]), __float_as_uint(g1[2 * i])));
-            vj[2 * i + 1] = rq::mul2(rq::mul2(hi, rs2),
-                                     rq::pk(__float_as_uint(g0[2 * i + 1]), __float_as_uint(g1[2 * i + 1])));
+            const uint64_t lo = pack2(u0[i] << 16, u1[i] << 16);
+            const uint64_t hi = pack2(u0[i] & 0xFFFF0000u, u1[i] & 0xFFFF0000u);
+            vj[2 * i] = mul2(mul2(lo, rs2), pack2(__float_as_uint(g0[2 * i]), __float_as_uint(g1[2 * i])));
+            vj[2 * i + 1] = mul2(mul2(hi, rs2),
+                                     pack2(__float_as_uint(g0[2 * i + 1]), __float_as_uint(g1[2 * i + 1])));
         }
         rq::rotate_pair_regs(L, tr, hmask, vj);
     };
@@ -570,13 +568,13 @@ __device__ __forceinline__ void rotate_rows16(int L, float *tr, unsigned hmask, 
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             uint32_t a0, a1, a2, a3;
-            rq::unpk(u[2 * q], a0, a1);
-            rq::unpk(u[2 * q + 1], a2, a3);
+            unpack2(u[2 * q], a0, a1);
+            unpack2(u[2 * q + 1], a2, a3);
             float f0 = __uint_as_float(a0), f1 = __uint_as_float(a1), f2 = __uint_as_float(a2),
                   f3 = __uint_as_float(a3);
             rq::h4_quad(f0, f1, f2, f3);
-            u[2 * q] = rq::pk(__float_as_uint(f0), __float_as_uint(f1));
-            u[2 * q + 1] = rq::pk(__float_as_uint(f2), __float_as_uint(f3));
+            u[2 * q] = pack2(__float_as_uint(f0), __float_as_uint(f1));
+            u[2 * q + 1] = pack2(__float_as_uint(f2), __float_as_uint(f3));
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -588,8 +586,8 @@ __device__ __forceinline__ void rotate_rows16(int L, float *tr, unsigned hmask, 
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         uint32_t a0, a1, b0, b1;
-        rq::unpk(v[2 * c], a0, a1);
-        rq::unpk(v[2 * c + 1], b0, b1);
+        unpack2(v[2 * c], a0, a1);
+        unpack2(v[2 * c + 1], b0, b1);
         rowp[c ^ sw] = make_uint4(a0, a1, b0, b1);
     }
     __syncwarp(hmask);
@@ -599,13 +597,13 @@ __device__ __forceinline__ void rotate_rows16(int L, float *tr, unsigned hmask, 
         col[k] = reinterpret_cast<uint32_t *>(tr) + 4 * ((L >> 2) ^ k) + (L & 3);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        v[i] = rq::pk(col[i & 3][32 * i], col[i & 3][32 * i + 16]);
+        v[i] = pack2(col[i & 3][32 * i], col[i & 3][32 * i + 16]);
     digits(v);
     // a lane's column is its own: it goes back to the places it came from
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         uint32_t lo, hi;
-        rq::unpk(v[i], lo, hi);
+        unpack2(v[i], lo, hi);
         col[i & 3][32 * i] = lo;
         col[i & 3][32 * i + 16] = hi;
     }
@@ -613,8 +611,8 @@ __device__ __forceinline__ void rotate_rows16(int L, float *tr, unsigned hmask, 
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const uint4 t = rowp[c ^ sw];
-        v[2 * c] = rq::pk(t.x, t.y);
-        v[2 * c + 1] = rq::pk(t.z, t.w);
+        v[2 * c] = pack2(t.x, t.y);
+        v[2 * c + 1] = pack2(t.z, t.w);
     }
     __syncwarp(hmask);
 }
@@ -648,15 +646,15 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotate_kernel(const uint16_t *
         uint64_t v[16];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[2 * i] = rq::pk(w0[i] << 16, w1[i] << 16);
-            v[2 * i + 1] = rq::pk(w0[i] & 0xFFFF0000u, w1[i] & 0xFFFF0000u);
+            v[2 * i] = pack2(w0[i] << 16, w1[i] << 16);
+            v[2 * i + 1] = pack2(w0[i] & 0xFFFF0000u, w1[i] & 0xFFFF0000u);
         }
         rq::rotate_pair_regs(L, tr, hmask, v);
         // column L out: word (a, L) at chunk (L / 4) ^ ((a / 2) % 4) of row a
 #pragma unroll
         for (int a = 0; a < 16; ++a) {
             uint32_t lo, hi;
-            rq::unpk(rq::mul2(v[a], 0x3D8000003D800000ull), lo, hi);  // times 1/16
+            unpack2(mul2(v[a], 0x3D8000003D800000ull), lo, hi);  // times 1/16
             tw[16 * a + 4 * ((L >> 2) ^ ((a >> 1) & 3)) + (L & 3)] =
                 to_bf16x2_bits(__uint_as_float(lo), __uint_as_float(hi));
         }
@@ -764,14 +762,14 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(const BwdArgs
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             uint32_t lo, hi;
-            rq::unpk(rq::fma2(g[i], rs16, rq::fma2(pair_of(hp[i]), k, pair_of(r[i]))), lo, hi);
+            unpack2(fma2(g[i], rs16, fma2(pair_of(hp[i]), k, pair_of(r[i]))), lo, hi);
             o[i] = to_bf16x2_bits(__uint_as_float(lo), __uint_as_float(hi));
         }
         store16(a.dx + at, a.wide, o);
     };
     auto sum_pair = [](uint64_t v) {
         uint32_t lo, hi;
-        rq::unpk(v, lo, hi);
+        unpack2(v, lo, hi);
         return __uint_as_float(lo) + __uint_as_float(hi);
     };
 
@@ -830,10 +828,10 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(const BwdArgs
                     load_gamma_pairs<GBF16>(a.gamma, 256 * b + 16 * L, gm);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const uint64_t xh = rq::mul2(pair_of(hp[j][i]), rs16);
-                        acc[j][i] = rq::fma2(g[j][i], xh, acc[j][i]);
-                        g[j][i] = rq::mul2(g[j][i], gm[i]);
-                        s = rq::fma2(g[j][i], xh, s);
+                        const uint64_t xh = mul2(pair_of(hp[j][i]), rs16);
+                        acc[j][i] = fma2(g[j][i], xh, acc[j][i]);
+                        g[j][i] = mul2(g[j][i], gm[i]);
+                        s = fma2(g[j][i], xh, s);
                     }
                 }
             }
@@ -875,12 +873,12 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(const BwdArgs
                     uint64_t xh[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        xh[e] = rq::mul2(pair_of(hp[2 * q + e]), rs16);
-                        s = rq::fma2(rq::mul2(g[2 * q + e], gm[2 * q + e]), xh[e], s);
+                        xh[e] = mul2(pair_of(hp[2 * q + e]), rs16);
+                        s = fma2(mul2(g[2 * q + e], gm[2 * q + e]), xh[e], s);
                     }
                     if (prow != nullptr) {
                         const ulonglong2 t = m == blockIdx.x ? make_ulonglong2(0ull, 0ull) : pp[q];
-                        pp[q] = make_ulonglong2(rq::fma2(g[2 * q], xh[0], t.x), rq::fma2(g[2 * q + 1], xh[1], t.y));
+                        pp[q] = make_ulonglong2(fma2(g[2 * q], xh[0], t.x), fma2(g[2 * q + 1], xh[1], t.y));
                     }
                 }
             }
@@ -896,7 +894,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(const BwdArgs
                 load_gamma_pairs<GBF16>(a.gamma, 256 * b + 16 * L, gm);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    g[i] = rq::mul2(g[i], gm[i]);
+                    g[i] = mul2(g[i], gm[i]);
                 finish(at, g, hp, r, rs, c);
             }
         }

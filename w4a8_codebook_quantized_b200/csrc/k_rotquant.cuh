@@ -337,48 +337,6 @@ inline cudaError_t launch_rows_t(const uint16_t *x, int64_t M, int64_t K, int64_
 
 // ================================================================ packed form (batches of many rows)
 
-// ---------------------------------------------------------------- fp32 pairs in 64-bit registers
-
-__device__ __forceinline__ uint64_t pk(uint32_t lo, uint32_t hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-
-__device__ __forceinline__ void unpk(uint64_t v, uint32_t &lo, uint32_t &hi)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-}
-
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
 // One digit of the rotation on a quadruple of pairs (row a of h4 is all ones
 // except -1 at column 3 - a).  2v is exact, so fma(-2, v, S) is S - 2v
 // rounded once.
@@ -418,8 +376,8 @@ __device__ __forceinline__ void rotate_pair_regs(int L, uint64_t *tr, unsigned h
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             uint32_t a0, a1, b0, b1;
-            unpk(v[2 * c], a0, a1);
-            unpk(v[2 * c + 1], b0, b1);
+            unpack2(v[2 * c], a0, a1);
+            unpack2(v[2 * c + 1], b0, b1);
             rowp[c ^ (L & 7)] = make_uint4(a0, a1, b0, b1);
         }
     }
@@ -459,8 +417,8 @@ __device__ __forceinline__ void rotate_pair(const uint16_t *__restrict__ blk0, c
     const uint32_t w1[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        v[2 * i] = pk(w0[i] << 16, w1[i] << 16);                      // element 2i: low bf16
-        v[2 * i + 1] = pk(w0[i] & 0xFFFF0000u, w1[i] & 0xFFFF0000u);  // element 2i+1: high bf16
+        v[2 * i] = pack2(w0[i] << 16, w1[i] << 16);                      // element 2i: low bf16
+        v[2 * i + 1] = pack2(w0[i] & 0xFFFF0000u, w1[i] & 0xFFFF0000u);  // element 2i+1: high bf16
     }
     rotate_pair_regs(L, tr, hmask, v);
 }
@@ -473,7 +431,7 @@ __device__ __forceinline__ float max_abs_pairs(const uint64_t (&v)[16])
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         uint32_t lo, hi;
-        unpk(v[i], lo, hi);
+        unpack2(v[i], lo, hi);
         m[i] = fmaxf(fabsf(__uint_as_float(lo)), fabsf(__uint_as_float(hi)));
     }
 #pragma unroll
@@ -502,10 +460,10 @@ __device__ __forceinline__ void quantise_store_pair(const uint64_t (&v)[16], flo
 {
     constexpr float kThr = 0.499969482421875f;  // 0.5 - 2^-15
     if (!exact_row) {
-        const uint64_t inv2 = pk(__float_as_uint(inv16), __float_as_uint(inv16));
+        const uint64_t inv2 = pack2(__float_as_uint(inv16), __float_as_uint(inv16));
         const uint64_t magic2 = 0x4B4000004B400000ull;  // (1.5 * 2^23, 1.5 * 2^23)
         const uint32_t nthr = __float_as_uint(-(kThr * kThr));
-        const uint64_t nthr2 = pk(nthr, nthr);
+        const uint64_t nthr2 = pack2(nthr, nthr);
         uint32_t all_neg = 0xFFFFFFFFu;  // sign bit stays set while no element is near a tie
 #pragma unroll
         for (int a = 0; a < 16; ++a) {
@@ -513,9 +471,9 @@ __device__ __forceinline__ void quantise_store_pair(const uint64_t (&v)[16], flo
             const uint64_t tm = add2(t, magic2);
             const uint64_t d = sub2(t, sub2(tm, magic2));
             uint32_t e0, e1, b0, b1;
-            unpk(fma2(d, d, nthr2), e0, e1);
+            unpack2(fma2(d, d, nthr2), e0, e1);
             all_neg &= e0 & e1;
-            unpk(tm, b0, b1);
+            unpack2(tm, b0, b1);
             tb[16 * a + L] = (uint8_t)b0;
             tb[256 + 16 * a + L] = (uint8_t)b1;
         }
@@ -524,7 +482,7 @@ __device__ __forceinline__ void quantise_store_pair(const uint64_t (&v)[16], flo
 #pragma unroll
             for (int a = 0; a < 16; ++a) {
                 uint32_t r0, r1;
-                unpk(v[a], r0, r1);
+                unpack2(v[a], r0, r1);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float R = __uint_as_float(h == 0 ? r0 : r1);
@@ -541,7 +499,7 @@ __device__ __forceinline__ void quantise_store_pair(const uint64_t (&v)[16], flo
 #pragma unroll
         for (int a = 0; a < 16; ++a) {
             uint32_t r0, r1;
-            unpk(v[a], r0, r1);
+            unpack2(v[a], r0, r1);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float r = __fmul_rn(__uint_as_float(h == 0 ? r0 : r1), 0.0625f);
