@@ -347,6 +347,64 @@ def test_cross_entropy_row_blocks():
     assert torch.equal(loss[s], loss2) and torch.equal(lse[s], lse2) and torch.equal(dx[s], dx2)
 
 
+def test_cross_entropy_forward_row_blocks():
+    """More rows than one block of the forward holds."""
+    M, V, K = 32768 + 77, 300, 256
+    ly = inputs.layer(V, K, 31)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 32)
+    t = dev(_targets(M, V, 33))
+    w, _ = _layer_dev(ly)
+    loss, lse = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, t)
+    s = slice(32768, M)
+    loss2, lse2 = cr.cr_w4a8_cross_entropy(xq_d[s].clone(), xs_d[s].clone(), *w, t[s].clone())
+    assert torch.equal(loss[s], loss2) and torch.equal(lse[s], lse2)
+    r_loss, r_lse, _ = cross_entropy(ly, xq[:50], xs[:50], host(t[:50]))
+    assert np.allclose(f64(lse[:50]), r_lse, rtol=1e-6) and np.allclose(f64(loss[:50]), r_loss, rtol=1e-5, atol=1e-6)
+
+
+@pytest.mark.parametrize("M", [6, 300])
+def test_work_buffers_aligned_to_16_bytes_only(M):
+    """A work buffer of exactly the stated size at any 16-byte boundary."""
+    N, K = 520, 512
+    ly = inputs.layer(N, K, 41)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 42)
+    t = dev(_targets(M, N, 43))
+    w, _ = _layer_dev(ly)
+    dout = torch.randn(M, N // 2, device="cuda").to(torch.bfloat16)
+    one = torch.ones(M, device="cuda")
+    loss, lse = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, t)
+    dx = cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, t, lse, one)
+    sx, sz = cr.cr_w4a8_swiglu_backward(dout, xq_d, xs_d, *w)
+    for shift in (16, 144):
+        def work(name):
+            need = getattr(cr.lib(), name + "_work_bytes")(M, N, K)
+            g = Guarded((need + shift,), torch.uint8)
+            g.tensor = g.tensor[shift:]
+            g.tensor.fill_(0xFF)
+            return g
+        a, b, c = (work("cr_w4a8_" + n) for n in ("cross_entropy", "cross_entropy_backward", "swiglu_backward"))
+        l2, e2 = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, t, work=a.tensor)
+        d2 = cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, t, lse, one, work=b.tensor)
+        x2, z2 = cr.cr_w4a8_swiglu_backward(dout, xq_d, xs_d, *w, work=c.tensor)
+        torch.cuda.synchronize()
+        assert a.intact() and b.intact() and c.intact()
+        assert torch.equal(l2, loss) and torch.equal(e2, lse) and torch.equal(d2, dx)
+        assert torch.equal(x2, sx) and torch.equal(z2, sz)
+
+
+def test_overlapping_buffers_are_refused():
+    M, N, K = 16, 512, 256
+    ly = inputs.layer(N, K, 44)
+    _, _, xq, xs = _quantised(M, K, 45)
+    w, _ = _layer_dev(ly)
+    big = torch.zeros(2 * M * N, dtype=torch.bfloat16, device="cuda")
+    dz, dout, dx = big[:M * N].view(M, N), big[M * N // 2:M * N].view(M, N // 2), big[:M * K].view(M, K)
+    with pytest.raises(cr.CrError):
+        cr.cr_w4a8_swiglu_backward(dout, xq, xs, *w, dz=dz)
+    with pytest.raises(cr.CrError):
+        cr.cr_w4a8_swiglu_backward(torch.zeros(M, N // 2, dtype=torch.bfloat16, device="cuda"), xq, xs, *w, dz=dz, dx=dx)
+
+
 def test_no_rows():
     ly = inputs.layer(64, 256, 1)
     w, _ = _layer_dev(ly)

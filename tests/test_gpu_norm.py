@@ -240,6 +240,73 @@ def test_norm_on_another_stream_and_in_a_graph():
         assert all(torch.equal(a, b) for a, b in zip(step(), out))
 
 
+def _shifted(t):
+    """The same values 16 bytes past a 512-byte boundary: rows that are not
+    aligned to 32 bytes."""
+    raw = torch.empty(t.numel() * t.element_size() + 16, dtype=torch.uint8, device="cuda")
+    out = raw[16:].view(t.dtype).view(t.shape)
+    out.copy_(t)
+    assert out.data_ptr() % 32 == 16
+    return out
+
+
+@pytest.mark.parametrize("M,K", [(3, 1024), (3, 20480), (40, 768), (40, 36864), (200, 2048)])
+def test_norm_of_rows_aligned_to_16_bytes_only(M, K):
+    dr, h, gamma, rs, dd = _grad_inputs(M, K, 51, torch.float32, True)
+    dr, x, g, rs, r = dr.cuda(), h.cuda(), dev(gamma), dev(rs), dd.cuda()
+    ref = [*cr.cr_rmsnorm_quant_act(x, g, EPS, residual=r), *cr.cr_rmsnorm_backward(dr, x, g, rs, dres=r),
+           cr.cr_rotate(x)]
+    sx, sr, sdr = _shifted(x), _shifted(r), _shifted(dr)
+    got = [*cr.cr_rmsnorm_quant_act(sx, _shifted(g), EPS, residual=sr, h=_shifted(x)),
+           *cr.cr_rmsnorm_backward(sdr, sx, _shifted(g), rs, dres=sr, dx=_shifted(x)),
+           cr.cr_rotate(sx, out=_shifted(x))]
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
+def test_norm_of_more_than_two_to_the_31_elements():
+    """Offsets past 32 bits: the last rows of a batch of 2.4e9 elements equal
+    those computed alone."""
+    M, K = 295_000, 8192
+    x = torch.randn(1000, K, device="cuda").to(torch.bfloat16).repeat(M // 1000, 1)
+    x[-3:] *= 3
+    g = torch.rand(K, device="cuda") + 0.5
+    xq, xs, h, rs = cr.cr_rmsnorm_quant_act(x, g, EPS, residual=x)
+    tail = x[-40:].clone()
+    tq, ts, th, trs = cr.cr_rmsnorm_quant_act(tail, g, EPS, residual=tail)
+    assert torch.equal(xq[-40:], tq) and torch.equal(xs[-40:], ts) and torch.equal(h[-40:], th)
+    assert torch.equal(rs[-40:], trs)
+    del xq, xs
+    dx, dg = cr.cr_rmsnorm_backward(x, h, g, rs, dres=x)
+    assert torch.equal(dx[-40:], cr.cr_rmsnorm_backward(tail, th, g, trs, dres=tail)[0])
+    assert torch.isfinite(dg).all()
+    del dx
+    assert torch.equal(cr.cr_rotate(x, out=h)[-40:], cr.cr_rotate(tail))
+
+
+def test_norm_from_two_threads():
+    import threading
+    M, K = 64, 4096
+    sets = [_grad_inputs(M, K, s, torch.float32, True) for s in (61, 62)]
+    args = [(dr.cuda(), h.cuda(), dev(g), dev(rs)) for dr, h, g, rs, _ in sets]
+    refs = [cr.cr_rmsnorm_backward(*a) for a in args]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(50):
+                dx, dg = cr.cr_rmsnorm_backward(*args[i])
+                s.synchronize()
+                if not (torch.equal(dx, refs[i][0]) and torch.equal(dg, refs[i][1])):
+                    bad.append(i)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert not bad
+
+
 def test_norm_refusals():
     K = 512
     x = torch.zeros(4, K, dtype=torch.bfloat16, device="cuda")

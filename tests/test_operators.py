@@ -122,7 +122,7 @@ def test_swiglu_backward_validation(L):
     need = L.cr_w4a8_swiglu_backward_work_bytes(4, 8, 256)
     assert need >= 3 * 8 * 256 and L.cr_w4a8_swiglu_backward_work_bytes(4, 8, 300) == 0
 
-    def call(ptrs=(A,) * 8, M=4, N=8, K=256, dx=B, dz=C, work=A, wb=need):
+    def call(ptrs=(A,) * 8, M=4, N=8, K=256, dx=B, dz=C, work=A, wb=need):  # dout at A, apart from dx and dz
         return L.cr_w4a8_swiglu_backward(*ptrs, M, N, K, dx, dz, work, wb, None)
 
     assert call(M=-1) == INVALID and call(M=2 ** 31) == UNSUPPORTED and call(N=-8) == INVALID
@@ -134,6 +134,7 @@ def test_swiglu_backward_validation(L):
     assert call(dx=None) == INVALID and call(dz=None) == INVALID and call(work=None) == INVALID
     assert call(dx=MIS) == ALIGNMENT and call(dz=MIS) == ALIGNMENT and call(work=MIS) == ALIGNMENT
     assert call(wb=need - 1) == INVALID
+    assert call(dz=B) == INVALID and call(dz=A) == INVALID and call(dx=A) == INVALID  # overlapping buffers
     assert call(ptrs=(None,) * 8, M=0, dx=None, dz=None, work=None, wb=0) == OK
 
 

@@ -1470,6 +1470,9 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
     st = check_contraction(xq, xs, qdata, srel, codebook, s_channel, bias, M, N, K, CR_OUT_BF16, dz, nullptr);
     if (st != CR_OK)
         return st;
+    if (overlap(dz, 2 * M * N, dout, M * N) || overlap(dz, 2 * M * N, dx, 2 * M * K) ||
+        overlap(dx, 2 * M * K, dout, M * N))
+        return CR_ERR_INVALID_ARG;
     const SwigluWork w(work, M, N, K);
     st = check_work(work, work_bytes, w.bytes);
     if (st != CR_OK)
