@@ -17,6 +17,7 @@ Storage of one layer (ai-toolkit convrot_w4a8_quant.py, module docstring):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional, Tuple
@@ -255,7 +256,6 @@ def _on_stream(fn):
     current stream for the call, so that the outputs and work buffers the call
     allocates belong to the stream that uses them: the caching allocator may
     hand a freed buffer to later work of the stream it was allocated on only."""
-    import functools
     body = _on_device(fn)
 
     @functools.wraps(fn)
@@ -263,13 +263,15 @@ def _on_stream(fn):
         torch = _torch()
         if stream is None:
             # the usual call, all tensors on the current device, without the wrapper's search
-            here = torch.cuda.current_device()
-            for a in args:
-                if a.__class__ is torch.Tensor and a.get_device() != here:
-                    return body(*args, **kwargs)
-            for a in kwargs.values():
-                if a.__class__ is torch.Tensor and a.get_device() != here:
-                    return body(*args, **kwargs)
+            tensor, here = torch.Tensor, -1
+            for a in (*args, *kwargs.values()) if kwargs else args:
+                if isinstance(a, tensor):
+                    dev = a.get_device()  # -1: not on a GPU, for the function to refuse
+                    if dev < 0 or here not in (-1, dev):
+                        return body(*args, **kwargs)
+                    here = dev
+            if here < 0 or here != torch._C._cuda_getDevice():
+                return body(*args, **kwargs)
             return fn(*args, **kwargs)
         dev = _cuda_device_of(args, kwargs)
         if not hasattr(stream, "cuda_stream"):
@@ -282,9 +284,20 @@ def _on_stream(fn):
     return wrapper
 
 
+def _here(t):
+    """The current stream's handle on t's device (the current one, in a call under _on_stream)."""
+    return _torch_module._C._cuda_getCurrentRawStream(t.get_device())
+
+
+@functools.lru_cache(maxsize=1024)
+def _work_bytes(name, *shape):
+    """The size the library states for an entry point's work buffer (a function of the shape alone)."""
+    return getattr(lib(), name + "_work_bytes")(*shape)
+
+
 def _want(t, name, dtype, shape):
     """_need for one dtype and a known shape: the checks alone where they pass."""
-    if not (t.__class__ is _torch().Tensor and t.dtype == dtype and t.shape == shape and t.is_cuda
+    if not (isinstance(t, _torch_module.Tensor) and t.dtype == dtype and t.shape == shape and t.is_cuda
             and t.is_contiguous()):
         _need(t, name, (dtype,), shape=shape)
 
@@ -1017,9 +1030,12 @@ def cr_w4a8_dequant_t_bf16(qdata, srel, codebook, s_channel, wt=None, stream=Non
 # ---------------------------------------------------------------- between the layers
 
 def _gamma(gamma, K):
-    torch = _torch()
+    torch = _torch_module
+    if isinstance(gamma, torch.Tensor) and gamma.dtype == torch.float32:
+        _want(gamma, "gamma", torch.float32, (K,))
+        return CR_OUT_F32
     _need(gamma, "gamma", (torch.bfloat16, torch.float32), shape=(K,))
-    return CR_OUT_BF16 if gamma.dtype == torch.bfloat16 else CR_OUT_F32
+    return CR_OUT_BF16
 
 
 @_on_stream
@@ -1039,11 +1055,12 @@ def cr_rmsnorm_quant_act(x, gamma, eps: float = 1e-6, residual=None, mp: Optiona
         _want(residual, "residual", torch.bfloat16, (M, K))
         if h is None:
             h = torch.empty_like(x)
-        _want(h, "h", torch.bfloat16, (M, K))
+        else:
+            _want(h, "h", torch.bfloat16, (M, K))
     elif h is not None and h is not x:
         raise ValueError("h is an output of the residual's addition: without a residual it is x")
     if xq is None:
-        xq = torch.empty(MP, K, dtype=torch.int8, device=x.device)
+        xq = torch.empty((MP, K), dtype=torch.int8, device=x.device)
     else:
         _want(xq, "xq", torch.int8, (MP, K))
     if xs is None:
@@ -1054,9 +1071,9 @@ def cr_rmsnorm_quant_act(x, gamma, eps: float = 1e-6, residual=None, mp: Optiona
         rs = torch.empty(M, dtype=torch.float32, device=x.device)
     else:
         _want(rs, "rs", torch.float32, (M,))
-    _check(lib().cr_rmsnorm_quant_act(_ptr(x), _ptr(residual), _ptr(gamma), code, float(eps), M, K, MP, int(act_qmax),
-                                      _ptr(h) if residual is not None else None, _ptr(xq), _ptr(xs), _ptr(rs),
-                                      _stream(None)), "cr_rmsnorm_quant_act")
+    r, hp = (None, None) if residual is None else (residual.data_ptr(), h.data_ptr())
+    _check(lib().cr_rmsnorm_quant_act(x.data_ptr(), r, gamma.data_ptr(), code, float(eps), M, K, MP, int(act_qmax), hp,
+                                      xq.data_ptr(), xs.data_ptr(), rs.data_ptr(), _here(x)), "cr_rmsnorm_quant_act")
     return xq, xs, (x if residual is None else h), rs
 
 
@@ -1077,7 +1094,7 @@ def cr_rmsnorm_backward(dr, h, gamma, rs, dres=None, dx=None, dgamma=None, work=
     if dres is not None:
         _want(dres, "dres", torch.bfloat16, (M, K))
     if dx is None:
-        dx = torch.empty(M, K, dtype=torch.bfloat16, device=dr.device)
+        dx = torch.empty_like(dr)
     else:
         _want(dx, "dx", torch.bfloat16, (M, K))
     if with_dgamma:
@@ -1085,14 +1102,14 @@ def cr_rmsnorm_backward(dr, h, gamma, rs, dres=None, dx=None, dgamma=None, work=
             dgamma = torch.empty(K, dtype=torch.float32, device=dr.device)
         else:
             _want(dgamma, "dgamma", torch.float32, (K,))
-        work = _work_buffer(work, lib().cr_rmsnorm_backward_work_bytes(M, K), dr.device)
+        work = _work_buffer(work, _work_bytes("cr_rmsnorm_backward", M, K), dr.device)
     elif dgamma is not None:
         raise ValueError("dgamma given with with_dgamma=False")
     else:
         work = None
-    _check(lib().cr_rmsnorm_backward(_ptr(dr), _ptr(h), _ptr(gamma), code, _ptr(rs), _ptr(dres), M, K, _ptr(dx),
-                                     _ptr(dgamma), _ptr(work), 0 if work is None else work.numel(), _stream(None)),
-           "cr_rmsnorm_backward")
+    _check(lib().cr_rmsnorm_backward(dr.data_ptr(), h.data_ptr(), gamma.data_ptr(), code, rs.data_ptr(), _ptr(dres), M, K,
+                                     dx.data_ptr(), _ptr(dgamma), _ptr(work), 0 if work is None else work.numel(),
+                                     _here(dr)), "cr_rmsnorm_backward")
     return dx, dgamma
 
 
@@ -1118,7 +1135,8 @@ def cr_rotate(x, out=None):
         out = torch.empty_like(x)
     else:
         _want(out, "out", torch.bfloat16, x.shape)
-    _check(lib().cr_rotate(_ptr(x), x.shape[0], x.shape[1], _ptr(out), _stream(None)), "cr_rotate")
+    M, K = x.shape
+    _check(lib().cr_rotate(x.data_ptr(), M, K, out.data_ptr(), _here(x)), "cr_rotate")
     return out
 
 
@@ -1154,7 +1172,7 @@ def cr_w4a8_swiglu_backward(dout, xq, xs, qdata, srel, codebook, s_channel, bias
         dz = torch.empty(M, N, dtype=torch.bfloat16, device=dout.device)
     else:
         _want(dz, "dz", torch.bfloat16, (M, N))
-    work = _work_buffer(work, lib().cr_w4a8_swiglu_backward_work_bytes(M, N, K), dout.device)
+    work = _work_buffer(work, _work_bytes("cr_w4a8_swiglu_backward", M, N, K), dout.device)
     _check(lib().cr_w4a8_swiglu_backward(_ptr(dout), _ptr(xq), _ptr(xs), _ptr(qdata), _ptr(srel), _ptr(codebook),
                                          _ptr(s_channel), _ptr(bias), M, N, K, _ptr(dx), _ptr(dz), _ptr(work),
                                          work.numel(), _stream(None)), "cr_w4a8_swiglu_backward")
@@ -1181,7 +1199,7 @@ def cr_w4a8_cross_entropy(xq, xs, qdata, srel, codebook, s_channel, targets, bia
         lse = torch.empty(M, dtype=torch.float32, device=xq.device)
     else:
         _want(lse, "lse", torch.float32, (M,))
-    work = _work_buffer(work, lib().cr_w4a8_cross_entropy_work_bytes(M, V, K), xq.device)
+    work = _work_buffer(work, _work_bytes("cr_w4a8_cross_entropy", M, V, K), xq.device)
     _check(lib().cr_w4a8_cross_entropy(_ptr(xq), _ptr(xs), _ptr(qdata), _ptr(srel), _ptr(codebook), _ptr(s_channel),
                                        _ptr(bias), _ptr(targets), int(ignore_index), M, V, K, _ptr(loss), _ptr(lse),
                                        _ptr(work), work.numel(), _stream(None)), "cr_w4a8_cross_entropy")
@@ -1206,7 +1224,7 @@ def cr_w4a8_cross_entropy_backward(xq, xs, qdata, srel, codebook, s_channel, tar
         dx = torch.empty(M, K, dtype=torch.bfloat16, device=xq.device)
     else:
         _want(dx, "dx", torch.bfloat16, (M, K))
-    work = _work_buffer(work, lib().cr_w4a8_cross_entropy_backward_work_bytes(M, V, K), xq.device)
+    work = _work_buffer(work, _work_bytes("cr_w4a8_cross_entropy_backward", M, V, K), xq.device)
     _check(lib().cr_w4a8_cross_entropy_backward(_ptr(xq), _ptr(xs), _ptr(qdata), _ptr(srel), _ptr(codebook),
                                                 _ptr(s_channel), _ptr(bias), _ptr(targets), int(ignore_index),
                                                 _ptr(lse), _ptr(dloss), M, V, K, _ptr(dx), _ptr(work), work.numel(),
