@@ -39,6 +39,7 @@ struct DeviceState {
     // flags so that concurrent first calls do not race on the flag itself)
     std::atomic<bool> gemm_attr_set[cr::gm::kModes] = {};  // by gm::Mode
     std::atomic<bool> gemm_pair_attr_set[cr::gm::kModes] = {};
+    std::atomic<bool> gemm_narrow_attr_set[cr::gm::kModes] = {};
     std::atomic<bool> gemv_attr_set{false};
     std::atomic<bool> gemv_split_attr_set{false};
     std::atomic<bool> gemv32_attr_set{false};
@@ -466,6 +467,7 @@ struct GemmEpilogue {
     void *out = nullptr;
     int32_t *acc_out = nullptr;
     bool pair = false;                  // B as [K, N]: one tile per SM pair (the plan's choice)
+    bool narrow = false;                // epilogues with exponentials: 128 x 128 tiles (narrow_tiles)
     const CUtensorMap *copies = nullptr;  // and where split tiles go
     int64_t b_rows = 0;  // rows that a B given as [K, N] has, where K counts padding of A past them (0: K)
     cr::gm::EpiArgs ex;
@@ -491,23 +493,26 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
         return true;
     };
     const int64_t pair_tiles = ((M + 255) / 256) * ((N + gm::BN - 1) / gm::BN);
-    const bool use_pair = gm::b_is_kn(MODE) ? e.pair : pair_tiles >= d.num_sms / 2;
+    const bool use_pair = gm::b_is_kn(MODE)             ? e.pair
+                          : gm::has_exponentials(MODE) && e.narrow ? false
+                                                        : pair_tiles >= d.num_sms / 2;
+    const int64_t tn = gm::has_exponentials(MODE) && e.narrow ? 128 : gm::BN;
     CUtensorMap ta, tb;
     if (!map(&ta, A, M, (uint32_t)gm::BM) ||
         !(gm::b_is_kn(MODE) ? make_tmap_bf16(&tb, B, (uint64_t)N, (uint64_t)(e.b_rows ? e.b_rows : K), 64u, 64u)
-                            : map(&tb, B, N, use_pair ? 128u : (uint32_t)gm::BN)))
+                            : map(&tb, B, N, use_pair ? 128u : (uint32_t)tn)))
         return CR_ERR_CUDA;
     const CUtensorMap &tm_out = to ? *to : ta;  // placeholders where nothing leaves through them
     const CUtensorMap &tm_copy = e.copies ? *e.copies : ta;
     if (use_pair) {
-        if (!opt_in(d.gemm_pair_attr_set[MODE], (const void *)gm::gemm_pair_kernel<MODE>, gm::pair::kSmemBytes))
+        if (!opt_in(d.gemm_pair_attr_set[MODE], (const void *)gm::gemm_pair_kernel<MODE>, gm::pair::smem_bytes<MODE>()))
             return CR_ERR_CUDA;
         const int64_t units = gm::b_is_kn(MODE) ? e.ex.slots : pair_tiles;
         const int64_t pairs = units < d.num_sms / 2 ? units : d.num_sms / 2;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(2 * pairs));
         cfg.blockDim = dim3(gm::threads(MODE));
-        cfg.dynamicSmemBytes = gm::pair::kSmemBytes;
+        cfg.dynamicSmemBytes = gm::pair::smem_bytes<MODE>();
         cfg.stream = stream;
         cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -521,22 +526,46 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
         return launched(cudaLaunchKernelEx(&cfg, gm::gemm_pair_kernel<MODE>, ta, tb, tm_out, tm_copy, e.xs, e.ws, e.bias, (int)M,
                                            (int)N, (int)K, e.out_f32, e.swiglu, e.tma_out, e.out, e.acc_out, e.ex));
     }
-    if (!opt_in(d.gemm_attr_set[MODE], (const void *)gm::gemm_kernel<MODE>, gm::kSmemBytes))
-        return CR_ERR_CUDA;
-    const int64_t tiles = gm::b_is_kn(MODE) ? e.ex.slots : ((M + gm::BM - 1) / gm::BM) * ((N + gm::BN - 1) / gm::BN);
-    const int grid = (int)(tiles < d.num_sms ? tiles : d.num_sms);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(gm::threads(MODE));
-    cfg.dynamicSmemBytes = gm::kSmemBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = gm::dependent(MODE) ? 1 : 0;
-    return launched(cudaLaunchKernelEx(&cfg, gm::gemm_kernel<MODE>, ta, tb, tm_out, tm_copy, e.xs, e.ws, e.bias, (int)M, (int)N,
-                                       (int)K, e.out_f32, e.swiglu, e.tma_out, e.out, e.acc_out, e.ex));
+    auto launch_single = [&](auto kern, std::atomic<bool> &flag, size_t smem) {
+        if (!opt_in(flag, (const void *)kern, smem))
+            return CR_ERR_CUDA;
+        const int64_t tiles = gm::b_is_kn(MODE) ? e.ex.slots : ((M + gm::BM - 1) / gm::BM) * ((N + tn - 1) / tn);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(tiles < d.num_sms ? tiles : d.num_sms));
+        cfg.blockDim = dim3(gm::threads(MODE));
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = gm::dependent(MODE) ? 1 : 0;
+        return launched(cudaLaunchKernelEx(&cfg, kern, ta, tb, tm_out, tm_copy, e.xs, e.ws, e.bias, (int)M, (int)N,
+                                           (int)K, e.out_f32, e.swiglu, e.tma_out, e.out, e.acc_out, e.ex));
+    };
+    if constexpr (gm::has_exponentials(MODE)) {
+        if (e.narrow)
+            return launch_single(gm::gemm_kernel<MODE, 128>, d.gemm_narrow_attr_set[MODE], gm::smem_bytes<MODE, 128>());
+    }
+    return launch_single(gm::gemm_kernel<MODE>, d.gemm_attr_set[MODE], gm::smem_bytes<MODE, gm::BN>());
+}
+
+// Whether an int8 contraction whose epilogue has exponentials runs on 128 x
+// 128 tiles: by the rounds of tiles an SM goes through, counting 1 for its 128
+// x 256 (one SM's half of a pair's tile too) and for a 128 x 128 tile what was
+// measured, 0.57 at K = 1024 and 0.78 at K = 4096 (its operand bytes per
+// product are a third more, and short reductions are mostly set-up and
+// epilogue).  Wide against narrow: gated 333 x 2824 x 1280 32.2 -> 29.8 us,
+// cross entropy 500 x 10007 x 1024 20.2 -> 18.5 us, its gradient 42.4 -> 39.8;
+// not for 1000 x 6000 x 4096 (36.1 -> 40.1) or gated 1000 x 4096 x 2048
+// (44.2 -> 45.8).
+bool narrow_tiles(int64_t M, int64_t N, int64_t K)
+{
+    const int64_t pairs = (M + 255) / 256 * ((N + 255) / 256), m = (M + 127) / 128;
+    const int64_t wide = pairs >= 74 ? (pairs + 73) / 74 : (m * ((N + 255) / 256) + 147) / 148;
+    const int64_t narrow = (m * ((N + 127) / 128) + 147) / 148;
+    const double c = K < 4096 ? 0.5 + 0.07 * (double)K / 1024.0 : 0.78;
+    return c * (double)narrow < (double)wide;
 }
 
 // The tensor map of a row-major output [M, cols] leaving in boxes of 32 rows x
@@ -1354,6 +1383,7 @@ int64_t ce_piece(int64_t V, int64_t per_entry)
 
 struct CeFwdWork {
     int64_t rows, piece, slices;
+    bool narrow = false;  // of every launch, so that the slices have one width
     int8_t *w8 = nullptr;
     float *y = nullptr;
     float2 *part;
@@ -1368,7 +1398,8 @@ struct CeFwdWork {
             slices = (V + cr::ce::kSlice - 1) / cr::ce::kSlice;
             y = static_cast<float *>(p.take(4 * M * V));
         } else {
-            slices = (V + cr::gm::BN - 1) / cr::gm::BN;
+            narrow = narrow_tiles(rows, piece < V ? piece : V, K);
+            slices = (V + (narrow ? 127 : 255)) / (narrow ? 128 : 256);
             w8 = static_cast<int8_t *>(p.take((piece < V ? piece : V) * K));
         }
         part = static_cast<float2 *>(p.take(8 * slices * rows));
@@ -1494,6 +1525,7 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
     e.ws = s_channel;
     e.bias = bias;
     e.ex.dout = dout;
+    e.narrow = narrow_tiles(M, N, K);
     st = launch_gemm<gm::kSwigluGrad>(*d, xq, w.w8, &tz, M, N, K, e, stream);
     if (st != CR_OK)
         return st;
@@ -1556,6 +1588,7 @@ cr_status cr_w4a8_cross_entropy(const int8_t *xq, const float *xs, const uint8_t
             e.ex.n0 = (int)n0;
             e.ex.part = w.part;
             e.ex.slices = (int)w.slices;
+            e.narrow = w.narrow;
             e.ex.tlogit = w.tlogit;
             st = launch_gemm<gm::kCeStats>(*d, xq + m0 * K, w.w8, nullptr, rows, n, K, e, stream);
             if (st != CR_OK)
@@ -1638,6 +1671,7 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
             e.bias = bias ? bias + n0 : nullptr;
             e.ex = ex;
             e.ex.n0 = (int)n0;
+            e.narrow = narrow_tiles(rows, n, K);
             st = launch_gemm<gm::kCeGrad>(*d, bxq, w.w8, &tl, rows, n, K, e, stream);
             if (st != CR_OK)
                 return st;

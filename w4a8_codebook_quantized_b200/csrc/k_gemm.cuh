@@ -59,10 +59,13 @@ constexpr bool row_factor(int mode) { return mode == kBf16Rows || mode == kBf16R
 // it waits for the predecessor before it reads or writes anything.
 constexpr bool dependent(int mode) { return mode != kI8 && mode != kBf16; }
 
-// The epilogues that evaluate exponentials per output take eight warps (each
-// 32 rows x 128 columns of a tile) where the others take four (32 x 256): with
-// four, the epilogue of an int8 tile outlasted the tile's own MMAs.
-constexpr int epi_warps(int mode) { return mode == kSwigluGrad || mode == kCeStats || mode == kCeGrad ? 8 : 4; }
+// Eight warps for the epilogues that evaluate exponentials per output (each 32
+// rows x half a tile's columns) and those of split contractions, where the
+// layer's own takes four (32 rows x all columns): with four, the epilogue of an
+// int8 tile outlasted the tile's own MMAs, and a split tile's took as long as
+// its range of the reduction.
+constexpr bool has_exponentials(int mode) { return mode == kSwigluGrad || mode == kCeStats || mode == kCeGrad; }
+constexpr int epi_warps(int mode) { return mode == kI8 || mode == kBf16 ? 4 : 8; }
 constexpr int threads(int mode) { return 64 + 32 * epi_warps(mode); }
 
 // Where a tile's column j has its scale and bias in shared memory: for the
@@ -131,9 +134,10 @@ __host__ __device__ __forceinline__ int tile_number(int tm, int tn, int tiles_m,
 struct Tiling {
     int tiles_m, tiles_n, kblocks, full, splits, units;
 
-    __host__ __device__ Tiling(int M, int N, int kb, int bm, int slots, int max_splits, int split_tail)
+    __host__ __device__ Tiling(int M, int N, int kb, int bm, int slots, int max_splits, int split_tail,
+                               int cols = kSlotCols)
     {
-        tiles_n = (N + kSlotCols - 1) / kSlotCols;
+        tiles_n = (N + cols - 1) / cols;
         kblocks = kb;
         tiles_m = (M + bm - 1) / bm;
         const int tiles = tiles_m * tiles_n;
@@ -166,21 +170,27 @@ struct Tiling {
 };
 
 constexpr int BM = 128, BN = 256, BK = 128;  // BK in int8 elements = bytes
-constexpr int kStages = 4;
 constexpr int kABytes = BM * BK;              // 16 KB
-constexpr int kBBytes = BN * BK;              // 32 KB
-constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kKnBytes = 64 * 128;            // 8 KB: 64 terms x 64 columns of a B given as [K, N]
-constexpr int kTmemCols = 2 * BN;             // two accumulators
-constexpr uint32_t kIdesc = idesc_i8(BM, BN);
+constexpr int kEpiBytes = 32 * 128;           // one epilogue store unit: 32 rows x 128 bytes
 
-constexpr int kEpiBytes = 32 * 128;  // one epilogue store unit: 32 rows x 128 bytes
+// Staging of the epilogue: a 4 KB unit per warp, half of one where the warps
+// of the epilogues with exponentials store 64 bytes a row.
+constexpr int epi_units(int mode) { return has_exponentials(mode) ? epi_warps(mode) / 2 : epi_warps(mode); }
+// Per-tile channel scales: none in the modes that have no use for them.
+constexpr int scale_cols(int mode, int tn) { return b_is_kn(mode) ? 4 : tn; }
 
+// One CTA's shared memory for 128 x TN tiles (TN 256, or 128 for problems of
+// few tiles): a ring of 4 or 6 stages, 192 KB.
+template <int MODE, int TN>
 struct __align__(1024) Smem {
-    uint8_t stage[kStages][kStageBytes];  // A at +0, B at +kABytes; every buffer 1024-aligned
-    uint8_t epi[4][kEpiBytes];            // per epilogue warp, one 128B-swizzled staging unit
-    float wsb[2][BN];                     // per-tile channel scales (double-buffered by tile parity)
-    float biasb[2][BN];                   // per-tile bias
+    static constexpr int kStages = TN == 256 ? 4 : 6;
+    static constexpr int kStageBytes = kABytes + TN * BK;
+    static constexpr int kTmemCols = 2 * TN;  // two accumulators
+    uint8_t stage[kStages][kStageBytes];           // A at +0, B at +kABytes; every buffer 1024-aligned
+    uint8_t epi[epi_units(MODE)][kEpiBytes];       // swizzled staging units
+    float wsb[2][scale_cols(MODE, TN)];            // per-tile channel scales (double-buffered by tile parity)
+    float biasb[2][scale_cols(MODE, TN)];          // per-tile bias
     uint64_t full[kStages];
     uint64_t empty[kStages];
     uint64_t tmem_full[2];
@@ -189,7 +199,14 @@ struct __align__(1024) Smem {
     int abort;
 };
 
-constexpr size_t kSmemBytes = sizeof(Smem) + 1024;  // + slack to align the base
+constexpr size_t kMaxSmem = 227 * 1024;  // per CTA
+
+template <int MODE, int TN>
+constexpr size_t smem_bytes()
+{
+    static_assert(sizeof(Smem<MODE, TN>) + 1024 <= kMaxSmem, "shared memory of one CTA");
+    return sizeof(Smem<MODE, TN>) + 1024;  // + slack to align the base
+}
 
 static_assert(BN == kSlotCols, "tile width of Tiling");
 
@@ -261,7 +278,7 @@ __device__ __forceinline__ void store_half_unit(const uint32_t (&p)[16], int uco
 // RAW: the accumulator holds fp32 values that are the outputs themselves
 // (bf16 GEMM; ROWS: times xm); no channel scales, bias or SwiGLU.  ADD: the fp32 outputs are added to
 // what is there, by the bulk stores' own reduction (tma_out only).
-template <bool RAW, bool ROWS, bool ADD, class Release>
+template <bool RAW, bool ROWS, bool ADD, int COLS, class Release>
 __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_base, int lane, float xm, bool row_ok,
                                               const float *wsv, const float *bsv, bool has_bias, int M, int N,
                                               int out_f32, int swiglu, int tma_out, const CUtensorMap *tmOut,
@@ -328,14 +345,14 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_
         // stays in registers)
         auto units = [&](auto uo_c) {
             constexpr int uo = decltype(uo_c)::value;
-            for (int un = 0; un < BN / (2 * uo); ++un) {
+            for (int un = 0; un < COLS / (2 * uo); ++un) {
 #pragma unroll
                 for (int k = 0; k < uo / 16; ++k) {
                     const int c0 = 2 * uo * un + 32 * k;
                     __syncwarp();
                     tmem_ld_32cols(tbase + (uint32_t)c0, cur);
                     tmem_ld_wait();
-                    if (c0 + 32 == BN)
+                    if (c0 + 32 == COLS)
                         release();
                     float y[16];
                     pairs16(c0, y);
@@ -357,12 +374,12 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_
         } else if (tma_out) {
             units(std::integral_constant<int, 64>{});
         } else {
-            for (int ch = 0; ch < BN / 32; ++ch) {
+            for (int ch = 0; ch < COLS / 32; ++ch) {
                 const int c0 = 32 * ch;
                 __syncwarp();
                 tmem_ld_32cols(tbase + (uint32_t)c0, cur);
                 tmem_ld_wait();
-                if (ch + 1 == BN / 32)
+                if (ch + 1 == COLS / 32)
                     release();
                 float y[16];
                 pairs16(c0, y);
@@ -388,12 +405,12 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_
     tmem_ld_wait();
     if (tma_out && !out_f32) {
         // units of 64 columns: two 32-column chunks each
-        for (int u = 0; u < BN / 64; ++u) {
+        for (int u = 0; u < COLS / 64; ++u) {
             __syncwarp();
             tmem_ld_32cols(tbase + (uint32_t)(64 * u + 32), nxt);
             convert32(cur, 64 * u, packed);
             tmem_ld_wait();
-            if (u + 1 < BN / 64) {
+            if (u + 1 < COLS / 64) {
                 __syncwarp();
                 tmem_ld_32cols(tbase + (uint32_t)(64 * u + 64), cur);
             } else {
@@ -401,13 +418,13 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_
             }
             convert32(nxt, 64 * u + 32, packed + 16);
             store_unit(packed, col_base + 64 * u);
-            if (u + 1 < BN / 64)
+            if (u + 1 < COLS / 64)
                 tmem_ld_wait();
         }
     } else if (tma_out) {
         // units of 32 fp32 columns
-        for (int u = 0; u < BN / 32; ++u) {
-            if (u + 1 < BN / 32) {
+        for (int u = 0; u < COLS / 32; ++u) {
+            if (u + 1 < COLS / 32) {
                 __syncwarp();
                 tmem_ld_32cols(tbase + (uint32_t)(32 * u + 32), nxt);
             } else {
@@ -415,7 +432,7 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_
             }
             convert32(cur, 32 * u, packed);
             store_unit(packed, col_base + 32 * u);
-            if (u + 1 < BN / 32) {
+            if (u + 1 < COLS / 32) {
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
@@ -423,8 +440,8 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_
             }
         }
     } else {
-        for (int ch = 0; ch < BN / 32; ++ch) {
-            if (ch + 1 < BN / 32) {
+        for (int ch = 0; ch < COLS / 32; ++ch) {
+            if (ch + 1 < COLS / 32) {
                 __syncwarp();
                 tmem_ld_32cols(tbase + (uint32_t)(32 * (ch + 1)), nxt);
             } else {
@@ -449,7 +466,7 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_
                         acc_out[base + j] = (int32_t)cur[j];
                 }
             }
-            if (ch + 1 < BN / 32) {
+            if (ch + 1 < COLS / 32) {
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
@@ -544,16 +561,15 @@ __device__ __forceinline__ void load_dout16(const uint16_t *drow, int f0, int F,
     }
 }
 
-// The epilogues below take one warp's 32 rows and columns [c_lo, c_lo + 128)
-// of a tile, 32 columns at a time.
-constexpr int kEpiCols = 128;
+// The epilogues below take one warp's 32 rows and columns [c_lo, c_lo + COLS)
+// of a tile (half of its columns), 32 at a time.
 
 // Epilogue of kSwigluGrad: accumulator columns 2f and 2f + 1 are gate and up
 // of output column f; their gradients leave as the same two columns of dz
 // [M, N] bf16.  Each row's 16 values of dout for the next 32 columns are loaded
 // while the current ones are used (`dn`: those of the first, loaded by the
 // caller before it waits for the accumulator).
-template <class Release>
+template <int COLS, class Release>
 __device__ __forceinline__ void epilogue_swiglu_grad(uint32_t tbase, int row0, int col_base, int c_lo, int lane,
                                                      float xm, bool row_ok, const float *wsv, const float *bsv,
                                                      bool has_bias, int N, const EpiArgs &ex, const CUtensorMap *tmOut,
@@ -564,17 +580,17 @@ __device__ __forceinline__ void epilogue_swiglu_grad(uint32_t tbase, int row0, i
     const uint64_t xm2 = pair_both(xm);
     const uint16_t *drow = ex.dout + (int64_t)(row0 + lane) * F;
 #pragma unroll 1
-    for (int c0 = c_lo; c0 < c_lo + kEpiCols; c0 += 32) {
+    for (int c0 = c_lo; c0 < c_lo + COLS; c0 += 32) {
         uint32_t cur[32], d[8], packed[16];
         __syncwarp();
         tmem_ld_32cols(tbase + (uint32_t)c0, cur);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             d[i] = dn[i];
-        if (c0 + 32 < c_lo + kEpiCols)
+        if (c0 + 32 < c_lo + COLS)
             load_dout16(drow, (col_base + c0 + 32) >> 1, F, row_ok, dn);
         tmem_ld_wait();
-        if (c0 + 32 == c_lo + kEpiCols)
+        if (c0 + 32 == c_lo + COLS)
             release();
         // the tile's scales are staged with the middle two of four columns
         // exchanged (stage_column), so that gates and ups pair with their like
@@ -611,24 +627,24 @@ __device__ __forceinline__ void join(float2 &a, const float2 b)
 // reference's rounding.  Columns past N are left out; -inf outputs (a bias
 // that masks a vocabulary entry) contribute 0, also where there is nothing
 // else.  The target's output goes to tlogit.
-template <class Release>
+template <int COLS, class Release>
 __device__ __forceinline__ float2 epilogue_ce_stats(uint32_t tbase, int row, int col_base, int c_lo, float xm,
                                                     bool row_ok, const float *wsv, const float *bsv, bool has_bias,
                                                     int N, const EpiArgs &ex, Release release)
 {
     const float kNegInf = __int_as_float(0xFF800000);
     const int64_t t = row_ok ? ex.targets[row] : -1, lo = (int64_t)ex.n0 + col_base + c_lo;
-    const int tcol = (t >= lo && t < lo + kEpiCols && t - ex.n0 < N) ? c_lo + (int)(t - lo) : -1;
+    const int tcol = (t >= lo && t < lo + COLS && t - ex.n0 < N) ? c_lo + (int)(t - lo) : -1;
     const uint64_t xm2 = pair_both(xm);
     float ref = kNegInf, tl = 0.0f;
     uint64_t s = 0ull;
 #pragma unroll 1
-    for (int c0 = c_lo; c0 < c_lo + kEpiCols; c0 += 32) {
+    for (int c0 = c_lo; c0 < c_lo + COLS; c0 += 32) {
         uint32_t cur[32];
         __syncwarp();
         tmem_ld_32cols(tbase + (uint32_t)c0, cur);
         tmem_ld_wait();
-        if (c0 + 32 == c_lo + kEpiCols)
+        if (c0 + 32 == c_lo + COLS)
             release();
         uint64_t y[16];
         outputs32(cur, c0, xm2, wsv, bsv, has_bias, y);
@@ -675,7 +691,7 @@ __device__ __forceinline__ float2 epilogue_ce_stats(uint32_t tbase, int row, int
 // contraction: dl at the target is then -1 rounded by at most the target's
 // probability, where -dloss itself would carry bf16's relative rounding, the
 // same one in every row of a mean (0.4 percent of dx at worst).
-template <class Release>
+template <int COLS, class Release>
 __device__ __forceinline__ void epilogue_ce_grad(uint32_t tbase, int row0, int col_base, int c_lo, int lane, float xm,
                                                  bool row_ok, const float *wsv, const float *bsv, bool has_bias,
                                                  int N, const EpiArgs &ex, const CUtensorMap *tmOut,
@@ -689,17 +705,17 @@ __device__ __forceinline__ void epilogue_ce_grad(uint32_t tbase, int row0, int c
         if (t != ex.ignore) {
             lse2 = __fmul_rn(ex.lse[row], kLog2e);
             const int64_t lo = (int64_t)ex.n0 + col_base;
-            tcol = (t >= lo && t < lo + BN) ? (int)(t - lo) : -1;
+            tcol = (t >= lo && t < lo + 2 * COLS) ? (int)(t - lo) : -1;
         }
     }
     const uint64_t xm2 = pair_both(xm), nlse = pair_both(-lse2);
 #pragma unroll 1
-    for (int c0 = c_lo; c0 < c_lo + kEpiCols; c0 += 32) {
+    for (int c0 = c_lo; c0 < c_lo + COLS; c0 += 32) {
         uint32_t cur[32], packed[16];
         __syncwarp();
         tmem_ld_32cols(tbase + (uint32_t)c0, cur);
         tmem_ld_wait();
-        if (c0 + 32 == c_lo + kEpiCols)
+        if (c0 + 32 == c_lo + COLS)
             release();
         uint64_t y[16];
         outputs32(cur, c0, xm2, wsv, bsv, has_bias, y);
@@ -733,7 +749,7 @@ __device__ __forceinline__ void epilogue_ce_grad(uint32_t tbase, int row0, int c
 // and out_col are where the tile's outputs go (bf16 modes: a split tile's copy
 // has its own place and type).  wait() waits for the accumulator and is called
 // after whatever can be loaded before it; it returns false after an abort.
-template <int MODE, class Sh, class Wait, class Release>
+template <int MODE, int TN, class Sh, class Wait, class Release>
 __device__ __forceinline__ void epilogue_any(Sh &sh, int ew, int buf, uint32_t tbase, int row0, int out_row0,
                                              int tile_n, int out_col, int lane, const float *xs, bool has_bias, int M, int N,
                                              int out_f32, int swiglu, int tma_out, const CUtensorMap *tmOut,
@@ -743,15 +759,17 @@ __device__ __forceinline__ void epilogue_any(Sh &sh, int ew, int buf, uint32_t t
     const int row = row0 + lane;
     const bool row_ok = row < M;
     const float *wsv = sh.wsb[buf], *bsv = sh.biasb[buf];
-    if constexpr (epi_warps(MODE) == 4) {
+    constexpr int COLS = TN * 4 / epi_warps(MODE);  // the warp's columns of the tile
+    const int c_lo = (ew >> 2) * COLS;
+    if constexpr (!has_exponentials(MODE)) {
         if (!wait())
             return;
         const float xm = !row_ok ? 0.0f : row_factor(MODE) ? ex.row_scale(row) : is_bf16(MODE) ? 0.0f : xs[row];
-        epilogue_tile<is_bf16(MODE), row_factor(MODE), MODE == kBf16RowsAdd>(
-            tbase, out_row0, out_col, lane, xm, row_ok, wsv, bsv, has_bias, M, N, out_f32, swiglu, tma_out, tmOut,
-            sh.epi[ew], units_issued, out, acc_out, ws, bias, release);
+        epilogue_tile<is_bf16(MODE), row_factor(MODE), MODE == kBf16RowsAdd, COLS>(
+            tbase + (uint32_t)c_lo, out_row0, out_col + c_lo, lane, xm, row_ok, wsv + c_lo, bsv + c_lo, has_bias, M, N,
+            out_f32, swiglu, tma_out, tmOut, sh.epi[ew], units_issued, out, acc_out, ws, bias, release);
     } else {
-        const int c_lo = (ew >> 2) * kEpiCols, col_base = tile_n * BN;
+        const int col_base = tile_n * TN;
         uint8_t *stage_buf = &sh.epi[0][0] + ew * (kEpiBytes / 2);
         const float xm = row_ok ? xs[row] : 0.0f;
         if constexpr (MODE == kSwigluGrad) {
@@ -759,12 +777,12 @@ __device__ __forceinline__ void epilogue_any(Sh &sh, int ew, int buf, uint32_t t
             load_dout16(ex.dout + (int64_t)row * (N >> 1), (col_base + c_lo) >> 1, N >> 1, row_ok, dn);
             if (!wait())
                 return;
-            epilogue_swiglu_grad(tbase, row0, col_base, c_lo, lane, xm, row_ok, wsv, bsv, has_bias, N, ex, tmOut,
+            epilogue_swiglu_grad<COLS>(tbase, row0, col_base, c_lo, lane, xm, row_ok, wsv, bsv, has_bias, N, ex, tmOut,
                                  stage_buf, units_issued, dn, release);
         } else if constexpr (MODE == kCeGrad) {
             if (!wait())
                 return;
-            epilogue_ce_grad(tbase, row0, col_base, c_lo, lane, xm, row_ok, wsv, bsv, has_bias, N, ex, tmOut,
+            epilogue_ce_grad<COLS>(tbase, row0, col_base, c_lo, lane, xm, row_ok, wsv, bsv, has_bias, N, ex, tmOut,
                              stage_buf, units_issued, release);
         } else {
             // the two warps of a row join their halves: the upper one's pairs
@@ -773,14 +791,14 @@ __device__ __forceinline__ void epilogue_any(Sh &sh, int ew, int buf, uint32_t t
             const bool ok = wait();
             float2 a = make_float2(0.0f, 0.0f);
             if (ok)
-                a = epilogue_ce_stats(tbase, row, col_base, c_lo, xm, row_ok, wsv, bsv, has_bias, N, ex, release);
+                a = epilogue_ce_stats<COLS>(tbase, row, col_base, c_lo, xm, row_ok, wsv, bsv, has_bias, N, ex, release);
             float2 *half = reinterpret_cast<float2 *>(&sh.epi[0][0]) + 32 * (ew & 3);
             if (ew >= 4)
                 half[lane] = a;
             asm volatile("bar.sync 3, 256;" ::: "memory");
             if (ok && ew < 4 && row_ok) {
                 join(a, half[lane]);
-                ex.part[(int64_t)row * ex.slices + ex.n0 / BN + tile_n] = a;
+                ex.part[(int64_t)row * ex.slices + ex.n0 / TN + tile_n] = a;
             }
         }
     }
@@ -789,7 +807,7 @@ __device__ __forceinline__ void epilogue_any(Sh &sh, int ew, int buf, uint32_t t
 // BF16 modes: A and B are bf16 (K counted in bf16 elements, 64 per 128-byte
 // stage row), tcgen05.mma kind::f16 into fp32, and the epilogue writes the
 // accumulators as they are (xs, ws, bias, swiglu and acc_out unused).
-template <int MODE>
+template <int MODE, int TN = BN>
 __global__ void __launch_bounds__(threads(MODE), 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmCopy,
@@ -799,7 +817,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
 {
     constexpr bool BF16 = is_bf16(MODE);
     extern __shared__ uint8_t smem_raw[];
-    Smem &sh = smem_aligned_1024<Smem>(smem_raw);
+    using Sh = Smem<MODE, TN>;
+    constexpr int kStages = Sh::kStages;
+    Sh &sh = smem_aligned_1024<Sh>(smem_raw);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int BKE = BF16 ? BK / 2 : BK;  // K elements per stage
@@ -818,7 +838,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 1) {
-        tmem_alloc(&sh.tmem_base, kTmemCols);
+        tmem_alloc(&sh.tmem_base, Sh::kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -835,7 +855,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             M = min(M, __ldcg(ex.count));
     }
     const Tiling tiling(M, N, kblocks, BM, b_is_kn(MODE) ? ex.slots : 1, b_is_kn(MODE) ? ex.max_splits : 1,
-                        b_is_kn(MODE) ? ex.split_tail : 0);
+                        b_is_kn(MODE) ? ex.split_tail : 0, TN);
     const int num_tiles = tiling.units;
     auto coords = [&](int unit, int &tm, int &tn, int &k0, int &k1, int &copy) {
         if constexpr (b_is_kn(MODE)) {
@@ -872,15 +892,15 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&sh.full[stage], kStageBytes);
+                    mbar_arrive_expect_tx(&sh.full[stage], Sh::kStageBytes);
                     tma_load_2d(sh.stage[stage], &tmA, kb * BKE, tm * BM, &sh.full[stage]);
                     if constexpr (b_is_kn(MODE)) {
 #pragma unroll
-                        for (int i = 0; i < BN / 64; ++i)  // boxes of 64 columns x 64 terms
-                            tma_load_2d(sh.stage[stage] + kABytes + i * kKnBytes, &tmB, tn * BN + 64 * i, kb * BKE,
+                        for (int i = 0; i < TN / 64; ++i)  // boxes of 64 columns x 64 terms
+                            tma_load_2d(sh.stage[stage] + kABytes + i * kKnBytes, &tmB, tn * TN + 64 * i, kb * BKE,
                                         &sh.full[stage]);
                     } else {
-                        tma_load_2d(sh.stage[stage] + kABytes, &tmB, kb * BKE, tn * BN, &sh.full[stage]);
+                        tma_load_2d(sh.stage[stage] + kABytes, &tmB, kb * BKE, tn * TN, &sh.full[stage]);
                     }
                     ++issued;
                     if (++stage == kStages) {
@@ -921,22 +941,22 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(buf * BN);
+                const uint32_t d = tmem + (uint32_t)(buf * TN);
                 for (int kb = k0; kb < k1; ++kb) {
                     if (!mbar_wait_bounded(&sh.full[stage], phase, abort)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = (uint32_t)stage * (kStageBytes >> 4);
+                    const uint32_t st = (uint32_t)stage * (Sh::kStageBytes >> 4);
 #pragma unroll
                     for (int kk = 0; kk < BK / 32; ++kk) {
                         const uint64_t ad = sw128_desc(a_lo + st + 2u * kk);
                         const uint64_t bd = sw128_desc(b_lo + st + kBStep * kk);
                         if constexpr (BF16)
-                            mma_bf16(d, ad, bd, idesc_bf16(BM, BN, b_is_kn(MODE)), kk == 0 ? kb != k0 : 1u);
+                            mma_bf16(d, ad, bd, idesc_bf16(BM, TN, b_is_kn(MODE)), kk == 0 ? kb != k0 : 1u);
                         else
-                            mma_i8(d, ad, bd, kIdesc, kk == 0 ? kb != k0 : 1u);
+                            mma_i8(d, ad, bd, idesc_i8(BM, TN), kk == 0 ? kb != k0 : 1u);
                     }
                     tc_commit(&sh.empty[stage]);
                     if (++stage == kStages) {
@@ -975,8 +995,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             const uint32_t use = (uint32_t)(local >> 1) & 1u;
             ++local;
             if constexpr (!BF16) {
-                for (int j = et; j < BN; j += 32 * epi_warps(MODE)) {
-                    const int n = tn * BN + j, at = stage_column<MODE>(j);
+                for (int j = et; j < TN; j += 32 * epi_warps(MODE)) {
+                    const int n = tn * TN + j, at = stage_column<MODE>(j);
                     sh.wsb[buf][at] = n < N ? ws[n] : 0.0f;
                     sh.biasb[buf][at] = (bias != nullptr && n < N) ? bias[n] : 0.0f;
                 }
@@ -987,11 +1007,11 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                 tc_fence_after();
                 return ok;
             };
-            const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * BN);
+            const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * TN);
             const int row0 = tm * BM + 32 * q;
             const bool whole = copy < 0;  // a whole tile: its outputs have their own place
-            epilogue_any<MODE>(sh, warp - 2, buf, tbase, row0, whole ? row0 : copy * BM + 32 * q, tn,
-                               whole ? tn * BN : 0, lane, xs, bias != nullptr, M, N, whole ? out_f32 : 1, swiglu,
+            epilogue_any<MODE, TN>(sh, warp - 2, buf, tbase, row0, whole ? row0 : copy * BM + 32 * q, tn,
+                               whole ? tn * TN : 0, lane, xs, bias != nullptr, M, N, whole ? out_f32 : 1, swiglu,
                                tma_out, whole ? &tmOut : &tmCopy, units_issued, out, acc_out, ws, bias, ex, wait, [&]() {
                               tc_fence_before();
                               __syncwarp();
@@ -1008,7 +1028,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, Sh::kTmemCols);
     }
 }
 
@@ -1030,11 +1050,12 @@ constexpr int kHalfBytes = 128 * BK;           // 16 KB: one CTA's half of A or 
 constexpr int kStageBytes = 2 * kHalfBytes;    // A half at +0, B half at +16 KB
 constexpr uint32_t kIdesc = idesc_i8(256, BN);
 
+template <int MODE>
 struct __align__(1024) Smem {
     uint8_t stage[kStages][kStageBytes];
-    uint8_t epi[4][kEpiBytes];
-    float wsb[2][BN];
-    float biasb[2][BN];
+    uint8_t epi[epi_units(MODE)][kEpiBytes];
+    float wsb[2][scale_cols(MODE, BN)];
+    float biasb[2][scale_cols(MODE, BN)];
     uint64_t full[kStages];       // leader: both CTAs' bytes of a stage
     uint64_t empty[kStages];      // each CTA: its stage may be refilled
     uint64_t tmem_full[2];        // each CTA: its accumulator rows are complete
@@ -1042,7 +1063,13 @@ struct __align__(1024) Smem {
     uint32_t tmem_base;
     int abort;
 };
-constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+constexpr int kTmemCols = 2 * BN;  // two accumulators
+template <int MODE>
+constexpr size_t smem_bytes()
+{
+    static_assert(sizeof(Smem<MODE>) + 1024 <= kMaxSmem, "shared memory of one CTA");
+    return sizeof(Smem<MODE>) + 1024;
+}
 }  // namespace pair
 
 // BF16 as for gemm_kernel.
@@ -1056,7 +1083,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
 {
     constexpr bool BF16 = is_bf16(MODE);
     extern __shared__ uint8_t smem_raw[];
-    pair::Smem &sh = smem_aligned_1024<pair::Smem>(smem_raw);
+    pair::Smem<MODE> &sh = smem_aligned_1024<pair::Smem<MODE>>(smem_raw);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -1078,7 +1105,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 1) {
-        tmem_alloc_pair(&sh.tmem_base, kTmemCols);
+        tmem_alloc_pair(&sh.tmem_base, pair::kTmemCols);
         tmem_relinquish_pair();
     }
     tc_fence_before();
@@ -1252,7 +1279,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * BN);
             const uint32_t release_addr = mapa_shared(smem_u32(&sh.tmem_empty[buf]), 0);
             const bool whole = copy < 0;  // a whole tile: its outputs have their own place
-            epilogue_any<MODE>(sh, warp - 2, buf, tbase, row0, whole ? row0 : copy * 256 + (int)rank * 128 + 32 * q, tn,
+            epilogue_any<MODE, BN>(sh, warp - 2, buf, tbase, row0, whole ? row0 : copy * 256 + (int)rank * 128 + 32 * q, tn,
                                whole ? tn * BN : 0, lane, xs, bias != nullptr, M, N, whole ? out_f32 : 1, swiglu,
                                tma_out, whole ? &tmOut : &tmCopy, units_issued, out, acc_out, ws, bias, ex, wait, [&]() {
                               tc_fence_before();
@@ -1271,7 +1298,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     cluster_sync();  // no CTA leaves while its partner may still signal it
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, kTmemCols);
+        tmem_dealloc_pair(tmem, pair::kTmemCols);
     }
 }
 
