@@ -1385,9 +1385,9 @@ struct CeFwdWork {
     int64_t rows, piece, slices;
     bool narrow = false;  // of every launch, so that the slices have one width
     int8_t *w8 = nullptr;
-    float *y = nullptr;
-    float2 *part;
-    float *tlogit;
+    float *y = nullptr;  // a decode batch's outputs
+    float2 *part = nullptr;
+    float *tlogit = nullptr;
     int64_t bytes;
     CeFwdWork(void *work, int64_t M, int64_t V, int64_t K)
     {
@@ -1395,15 +1395,15 @@ struct CeFwdWork {
         rows = M < kFwdRows ? M : kFwdRows;
         piece = ce_piece(V, K);
         if (M <= CR_GEMV_MAX_M) {
-            slices = (V + cr::ce::kSlice - 1) / cr::ce::kSlice;
+            slices = 0;
             y = static_cast<float *>(p.take(4 * M * V));
         } else {
             narrow = narrow_tiles(rows, piece < V ? piece : V, K);
             slices = (V + (narrow ? 127 : 255)) / (narrow ? 128 : 256);
             w8 = static_cast<int8_t *>(p.take((piece < V ? piece : V) * K));
+            part = static_cast<float2 *>(p.take(8 * slices * rows));
+            tlogit = static_cast<float *>(p.take(4 * rows));
         }
-        part = static_cast<float2 *>(p.take(8 * slices * rows));
-        tlogit = static_cast<float *>(p.take(4 * rows));
         bytes = p.used;
     }
 };
@@ -1565,9 +1565,7 @@ cr_status cr_w4a8_cross_entropy(const int8_t *xq, const float *xs, const uint8_t
         st = run_gemv(d->num_sms, d->gemv_attr_set, xq, xs, qdata, srel, codebook, s_channel, bias, M, V, K,
                       CR_OUT_F32, w.y, nullptr, stream, /*pdl=*/true, 0, &d->gemv32_attr_set);
         if (st == CR_OK)
-            st = launched(ce::launch_stats(w.y, M, V, targets, w.part, w.tlogit, stream));
-        if (st == CR_OK)
-            st = launched(ce::launch_loss(w.part, w.slices, M, targets, ignore_index, V, w.tlogit, loss, lse, stream));
+            st = launched(ce::launch_row_loss(w.y, M, V, targets, ignore_index, loss, lse, stream));
         return st;
     }
     for (int64_t m0 = 0; m0 < M; m0 += w.rows) {

@@ -15,56 +15,89 @@ namespace cr {
 namespace ce {
 
 constexpr int kThreads = 256;
-constexpr int kSlice = 2048;  // columns per CTA of stats_kernel
 
 using gm::join;
 
-// Statistics of stored fp32 outputs y [M, V] (a decode batch, whose outputs
-// the GEMV wrote), kSlice columns per CTA: grid (slices, M).
-__global__ void __launch_bounds__(kThreads) stats_kernel(const float *__restrict__ y, int64_t V,
-                                                         const int64_t *__restrict__ targets,
-                                                         float2 *__restrict__ part, float *__restrict__ tlogit)
+// lse and loss from a row's joined statistics and its target's output (the
+// latter not used for an ignored or invalid target).  In fp64: a few operations
+// per row, and the loss is often a small difference of larger numbers.
+__device__ __forceinline__ void finish_row(const float2 a, float tlogit, int64_t t, int64_t ignore, int64_t V,
+                                           float *loss, float *lse)
 {
+    // the references are in units of the fp32 constant that made them
+    const double l = (double)a.x / (double)gm::kLog2e + log((double)a.y);
+    *lse = (float)l;
+    float out = 0.0f;
+    if (t != ignore)
+        out = (t >= 0 && t < V) ? (float)(l - (double)tlogit) : __int_as_float(0x7FC00000);
+    *loss = out;
+}
+
+// The whole loss of stored fp32 outputs y [M, V] (a decode batch, whose outputs
+// the GEMV wrote): a cluster of eight CTAs per row, an eighth of the row each;
+// the first one joins the eight from the others' shared memory, in order.
+constexpr int kRowCtas = 8;
+
+__global__ void __cluster_dims__(kRowCtas, 1, 1) __launch_bounds__(kThreads)
+    row_loss_kernel(const float *__restrict__ y, int64_t V, const int64_t *__restrict__ targets, int64_t ignore,
+                    float *__restrict__ loss, float *__restrict__ lse)
+{
+    const float kNegInf = __int_as_float(0xFF800000);
+    constexpr int kPer = 8;  // columns per thread and step
+    __shared__ float2 warp_stat[kThreads / 32];
+    __shared__ __align__(8) float2 stat;      // the CTA's statistics
+    __shared__ __align__(8) float2 target;    // .x: the target's output, in the CTA that has it
     asm volatile("griddepcontrol.launch_dependents;" :::);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const float kNegInf = __int_as_float(0xFF800000);
-    __shared__ float2 sh[kThreads / 32];
-    const int64_t m = blockIdx.y, n0 = (int64_t)blockIdx.x * kSlice;
+    const int64_t m = blockIdx.y, t = targets[m];
+    const int rank = (int)cluster_ctarank();
+    const int64_t slice = (V + kRowCtas - 1) / kRowCtas, n0 = rank * slice, n1 = n0 + slice < V ? n0 + slice : V;
     const float *row = y + m * V;
-    const int64_t t = targets[m];
-    float v[kSlice / kThreads];
-    float mx = kNegInf;
+    float2 a = make_float2(kNegInf, 0.0f);
+    for (int64_t n = n0 + threadIdx.x; n < n1; n += kPer * kThreads) {
+        float v[kPer], mx = kNegInf;
 #pragma unroll
-    for (int i = 0; i < kSlice / kThreads; ++i) {
-        const int64_t n = n0 + i * kThreads + threadIdx.x;
-        v[i] = n < V ? row[n] : kNegInf;
-        if (n == t && n < V)
-            tlogit[m] = v[i];
-        mx = fmaxf(mx, v[i]);
+        for (int i = 0; i < kPer; ++i) {
+            const int64_t c = n + i * kThreads;
+            v[i] = c < n1 ? row[c] : kNegInf;
+            if (c == t && c < n1)
+                target.x = v[i];
+            mx = fmaxf(mx, v[i]);
+        }
+        float2 b = make_float2(__fmul_rn(mx, gm::kLog2e), 0.0f);
+        const float base = b.x == kNegInf ? 0.0f : b.x;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            b.y += gm::ex2(__fmaf_rn(v[i], gm::kLog2e, -base));
+        join(a, b);
     }
-    float2 a = make_float2(__fmul_rn(mx, gm::kLog2e), 0.0f);
-    const float base = a.x == kNegInf ? 0.0f : a.x;
-#pragma unroll
-    for (int i = 0; i < kSlice / kThreads; ++i)
-        a.y += gm::ex2(__fmaf_rn(v[i], gm::kLog2e, -base));
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1)
         join(a, make_float2(__shfl_xor_sync(0xFFFFFFFFu, a.x, o), __shfl_xor_sync(0xFFFFFFFFu, a.y, o)));
     if ((threadIdx.x & 31) == 0)
-        sh[threadIdx.x >> 5] = a;
+        warp_stat[threadIdx.x >> 5] = a;
     __syncthreads();
     if (threadIdx.x == 0) {
 #pragma unroll
         for (int w = 1; w < kThreads / 32; ++w)
-            join(a, sh[w]);
-        part[m * gridDim.x + blockIdx.x] = a;
+            join(a, warp_stat[w]);
+        stat = a;
     }
+    cluster_sync();
+    if (rank == 0 && threadIdx.x == 0) {
+#pragma unroll
+        for (int r = 1; r < kRowCtas; ++r)
+            join(a, ld_cluster_f2(mapa_shared(smem_u32(&stat), (uint32_t)r)));
+        float tl = 0.0f;
+        if (t >= 0 && t < V)
+            tl = ld_cluster_f2(mapa_shared(smem_u32(&target), (uint32_t)(t / slice))).x;
+        finish_row(a, tl, t, ignore, V, loss + m, lse + m);
+    }
+    cluster_sync();  // nobody leaves while its shared memory may be read
 }
 
-// lse and loss from the statistics, a warp per row: the lanes take every 32nd
-// slice each and are joined in a fixed order.  The last steps are in fp64: a
-// few operations per row, and the loss is often a small difference of larger
-// numbers.
+// lse and loss from the statistics of a row's slices, a warp per row: the lanes
+// take every 32nd slice each and are joined in a fixed order.
 __global__ void __launch_bounds__(kThreads) loss_kernel(const float2 *__restrict__ part, int64_t slices, int64_t M,
                                                         const int64_t *__restrict__ targets, int64_t ignore, int64_t V,
                                                         const float *__restrict__ tlogit, float *__restrict__ loss,
@@ -83,16 +116,8 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const float2 *__restrict
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1)
         join(a, make_float2(__shfl_xor_sync(0xFFFFFFFFu, a.x, o), __shfl_xor_sync(0xFFFFFFFFu, a.y, o)));
-    if (lane == 0) {
-        // the references are in units of the fp32 constant that made them
-        const double l = (double)a.x / (double)gm::kLog2e + log((double)a.y);
-        lse[m] = (float)l;
-        const int64_t t = targets[m];
-        float out = 0.0f;
-        if (t != ignore)
-            out = (t >= 0 && t < V) ? (float)(l - (double)tlogit[m]) : __int_as_float(0x7FC00000);
-        loss[m] = out;
-    }
+    if (lane == 0)
+        finish_row(a, tlogit[m], targets[m], ignore, V, loss + m, lse + m);
 }
 
 // The rows that take part in the loss, gathered: every row's index, quantised
@@ -223,11 +248,11 @@ __global__ void __launch_bounds__(kThreads) split_sum_kernel(const SumArgs a)
     }
 }
 
-inline cudaError_t launch_stats(const float *y, int64_t M, int64_t V, const int64_t *targets, float2 *part,
-                                float *tlogit, cudaStream_t stream)
+inline cudaError_t launch_row_loss(const float *y, int64_t M, int64_t V, const int64_t *targets, int64_t ignore,
+                                   float *loss, float *lse, cudaStream_t stream)
 {
-    return launch_dependent(stats_kernel, dim3((unsigned)((V + kSlice - 1) / kSlice), (unsigned)M), kThreads, 0,
-                            stream, y, V, targets, part, tlogit);
+    return launch_dependent(row_loss_kernel, dim3(kRowCtas, (unsigned)M), kThreads, 0, stream, y, V, targets, ignore,
+                            loss, lse);
 }
 
 inline cudaError_t launch_loss(const float2 *part, int64_t slices, int64_t M, const int64_t *targets, int64_t ignore,
