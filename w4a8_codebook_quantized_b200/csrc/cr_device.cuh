@@ -316,6 +316,18 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     }
 }
 
+// True in one lane of the (converged) warp, the same one at every call.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
+}
+
 // The same bounded wait, taken by a whole warp: every lane polls, and the
 // outcome is the same in all lanes (warp-collective instructions follow it).
 __device__ __forceinline__ bool mbar_wait_bounded_warp(uint64_t *bar, uint32_t parity, volatile int *abort,

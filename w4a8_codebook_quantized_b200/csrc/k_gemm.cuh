@@ -919,7 +919,10 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        // The whole warp walks the loop, so that the descriptors stay in uniform
+        // registers, where the MMA instruction takes them from; one lane issues.
+        {
+            const bool issuer = elect_one();
             int stage = 0;
             uint32_t phase = 0;
             int local = 0;
@@ -936,35 +939,37 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                     continue;
                 const int buf = local & 1;
                 const uint32_t use = (uint32_t)(local >> 1) & 1u;
-                if (!mbar_wait_bounded(&sh.tmem_empty[buf], use ^ 1u, abort)) {
+                if (!mbar_wait_bounded_warp(&sh.tmem_empty[buf], use ^ 1u, abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * TN);
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!mbar_wait_bounded(&sh.full[stage], phase, abort)) {
+                    if (!mbar_wait_bounded_warp(&sh.full[stage], phase, abort)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t st = (uint32_t)stage * (Sh::kStageBytes >> 4);
+                    if (issuer) {
 #pragma unroll
-                    for (int kk = 0; kk < BK / 32; ++kk) {
-                        const uint64_t ad = sw128_desc(a_lo + st + 2u * kk);
-                        const uint64_t bd = sw128_desc(b_lo + st + kBStep * kk);
-                        if constexpr (BF16)
-                            mma_bf16(d, ad, bd, idesc_bf16(BM, TN, b_is_kn(MODE)), kk == 0 ? kb != k0 : 1u);
-                        else
-                            mma_i8(d, ad, bd, idesc_i8(BM, TN), kk == 0 ? kb != k0 : 1u);
+                        for (int kk = 0; kk < BK / 32; ++kk) {
+                            const uint64_t ad = sw128_desc(a_lo + st + 2u * kk);
+                            const uint64_t bd = sw128_desc(b_lo + st + kBStep * kk);
+                            if constexpr (BF16)
+                                mma_bf16(d, ad, bd, idesc_bf16(BM, TN, b_is_kn(MODE)), kk == 0 ? kb != k0 : 1u);
+                            else
+                                mma_i8(d, ad, bd, idesc_i8(BM, TN), kk == 0 ? kb != k0 : 1u);
+                        }
+                        tc_commit(&sh.empty[stage]);
                     }
-                    tc_commit(&sh.empty[stage]);
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                if (ok)
+                if (ok && issuer)
                     tc_commit(&sh.tmem_full[buf]);
                 ++local;
             }
@@ -1199,7 +1204,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader only)
-        if (leader && lane == 0) {
+        if (leader) {  // the whole warp, as in gemm_kernel
+            const bool issuer = elect_one();
             int stage = 0;
             uint32_t phase = 0;
             int local = 0;
@@ -1216,35 +1222,37 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                     continue;
                 const int buf = local & 1;
                 const uint32_t use = (uint32_t)(local >> 1) & 1u;
-                if (!mbar_wait_bounded(&sh.tmem_empty[buf], use ^ 1u, abort)) {
+                if (!mbar_wait_bounded_warp(&sh.tmem_empty[buf], use ^ 1u, abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * BN);
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!mbar_wait_bounded(&sh.full[stage], phase, abort)) {
+                    if (!mbar_wait_bounded_warp(&sh.full[stage], phase, abort)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t st = (uint32_t)stage * (pair::kStageBytes >> 4);
+                    if (issuer) {
 #pragma unroll
-                    for (int kk = 0; kk < BK / 32; ++kk) {
-                        const uint64_t ad = sw128_desc(a_lo + st + 2u * kk);
-                        const uint64_t bd = sw128_desc(b_lo + st + kBStep * kk);
-                        if constexpr (BF16)
-                            mma_bf16_pair(d, ad, bd, idesc_bf16(256, BN, b_is_kn(MODE)), kk == 0 ? kb != k0 : 1u);
-                        else
-                            mma_i8_pair(d, ad, bd, pair::kIdesc, kk == 0 ? kb != k0 : 1u);
+                        for (int kk = 0; kk < BK / 32; ++kk) {
+                            const uint64_t ad = sw128_desc(a_lo + st + 2u * kk);
+                            const uint64_t bd = sw128_desc(b_lo + st + kBStep * kk);
+                            if constexpr (BF16)
+                                mma_bf16_pair(d, ad, bd, idesc_bf16(256, BN, b_is_kn(MODE)), kk == 0 ? kb != k0 : 1u);
+                            else
+                                mma_i8_pair(d, ad, bd, pair::kIdesc, kk == 0 ? kb != k0 : 1u);
+                        }
+                        tc_commit_both(smem_u32(&sh.empty[0]) + 8u * (uint32_t)stage);
                     }
-                    tc_commit_both(smem_u32(&sh.empty[0]) + 8u * (uint32_t)stage);
                     if (++stage == pair::kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                if (ok)
+                if (ok && issuer)
                     tc_commit_both(smem_u32(&sh.tmem_full[buf]));
                 ++local;
             }
