@@ -902,24 +902,27 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(const BwdArgs
 }
 
 // dgamma[k] = sum over p of part[p, k], in a fixed order: a CTA takes 32
-// columns, its eight warps every eighth partial row each, then one warp adds
-// the eight.
-__global__ void __launch_bounds__(256) dgamma_kernel(const float *__restrict__ part, int P, int64_t K,
-                                                     float *__restrict__ dgamma)
+// columns, its 32 warps every 32nd partial row each, then one warp adds the 32
+// (with eight warps the chain of loads took 9 us of the 8192 x 4096 gradient,
+// cold).
+constexpr int kSumWarps = 32;
+
+__global__ void __launch_bounds__(32 * kSumWarps) dgamma_kernel(const float *__restrict__ part, int P, int64_t K,
+                                                                float *__restrict__ dgamma)
 {
-    __shared__ float sh[8][32];
+    __shared__ float sh[kSumWarps][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t k = 32 * (int64_t)blockIdx.x + lane;  // K is a multiple of 256
     float s = 0.0f;
 #pragma unroll 8
-    for (int p = w; p < P; p += 8)
+    for (int p = w; p < P; p += kSumWarps)
         s += part[(int64_t)p * K + k];
     sh[w][lane] = s;
     __syncthreads();
     if (w == 0) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i)
+        for (int i = 1; i < kSumWarps; ++i)
             s += sh[i][lane];
         dgamma[k] = s;
     }
@@ -952,7 +955,7 @@ inline cudaError_t launch_bwd_t(const BwdArgs &a, float *dgamma, cudaStream_t st
         e = launch_dependent(rmsnorm_backward_kernel<1, true, 512, GBF16>, dim3((unsigned)(P)), 512, 0, stream, a);
     if (e != cudaSuccess || dgamma == nullptr)
         return e;
-    return launch_dependent(dgamma_kernel, dim3((unsigned)(a.K / 32)), 256, 0, stream, (const float *)a.part, (int)P, a.K, dgamma);
+    return launch_dependent(dgamma_kernel, dim3((unsigned)(a.K / 32)), 32 * kSumWarps, 0, stream, (const float *)a.part, (int)P, a.K, dgamma);
 }
 
 inline cudaError_t launch_bwd(BwdArgs a, bool gamma_bf16, float *dgamma, cudaStream_t stream)
