@@ -33,7 +33,11 @@
  *   returns CR_ERR_CUDA and launches nothing.  The *_ws variants
  *   (cr_w4a8_gemm_ws, cr_w4a8_linear_ws, cr_w4a8_ste_backward_ws) take the
  *   transient from the caller instead and allocate nothing; every other entry
- *   point allocates no device memory.
+ *   point allocates no device memory.  (20), (22) and (23) take their scratch as
+ *   one `work` buffer whose size is a function of the shape that the library
+ *   states (cr_*_work_bytes, host only; 0 for shapes the call refuses or that
+ *   are empty); its contents on return mean nothing, and calls whose kernels
+ *   overlap need one each.
  * - cr_w4a8_linear (and _swiglu, _ws, _grouped, cr_w4a8_plan_forward) with
  *   M > 8 run the weight decode on a side stream of the library (one
  *   non-blocking stream and two events per device, created on first use and
@@ -55,13 +59,14 @@
  * - Calls that read a buffer another call on another stream is writing race,
  *   as with any CUDA kernel.
  * - Overlapped launches.  cr_rotate_quant_act, cr_w4a8_gemv, cr_w4a8_linear
- *   (decode path) and cr_w4a8_linear_decode_noalloc launch their kernels as
+ *   (decode path), cr_w4a8_linear_decode_noalloc and (19) to (23) launch their
+ *   kernels as
  *   programmatic dependents of the previous kernel on the stream, and those
  *   kernels allow the next kernel to launch early.  Stream order still holds
  *   for every activation, scale and output buffer: each kernel waits for its
  *   predecessor to complete before it reads a result of it or writes a
- *   buffer that the predecessor may read.  The decode GEMV alone starts
- *   reading the layer (qdata, srel, codebook) before that wait, so the layer
+ *   buffer that the predecessor may read.  The decode GEMV (that of (23) with
+ *   M <= 8 too) alone starts reading the layer (qdata, srel, codebook) before that wait, so the layer
  *   must not be written by a kernel that itself allows early launch of its
  *   dependents (griddepcontrol.launch_dependents / PDL) and immediately
  *   precedes the GEMV on the stream; a kernel that does not, and every copy
@@ -626,9 +631,11 @@ cr_status cr_rotate(const uint16_t *x, int64_t M, int64_t K, uint16_t *out, cr_s
  * dout [M, N / 2] bf16; xq [>= M, K] int8 and xs [>= M] fp32: the quantised
  * activations of the forward; the interleaved layer as in (9).  dx [M, K] bf16,
  * dz [M, N] bf16, written.  N must be a multiple of 8 (CR_ERR_UNSUPPORTED
- * otherwise); N == 0 writes dx = 0.  work: at least
- * cr_w4a8_swiglu_backward_work_bytes(M, N, K) bytes (the decoded weight, 3 N K),
- * 16-byte aligned; CR_ERR_INVALID_ARG when smaller.  Nothing is allocated.
+ * otherwise); N == 0 writes dx = 0.  dout, dx and dz must not overlap
+ * (CR_ERR_INVALID_ARG).  work: at least
+ * cr_w4a8_swiglu_backward_work_bytes(M, N, K) bytes (the decoded weight, 3 N K,
+ * and up to 20 MB for a split reduction), 16-byte aligned; CR_ERR_INVALID_ARG
+ * when smaller.  Nothing is allocated.
  */
 int64_t cr_w4a8_swiglu_backward_work_bytes(int64_t M, int64_t N, int64_t K);
 cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const float *xs, const uint8_t *qdata,
@@ -653,8 +660,10 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
  * loss [M], lse [M] fp32, written.  work: at least
  * cr_w4a8_cross_entropy_work_bytes(M, V, K) bytes, 16-byte aligned
  * (CR_ERR_INVALID_ARG when smaller): a decoded piece of the weight (64 MB or
- * 256 K bytes, whichever is more) and 8 bytes per row and 256 outputs.  Nothing
- * is allocated.
+ * 256 K bytes, whichever is more) and 8 bytes per row (of at most 32768 at a
+ * time) and 256 outputs, 128 for short problems; for M <= 8 the M V fp32
+ * outputs themselves.  Nothing is allocated.  Results are the same from run to
+ * run; between batch sizes the sums' order, and so the last bits, may differ.
  *
  * (23b) Its gradient with respect to the layer's rotated input:
  *   dl[m, n] = bf16( e^(y[m, n] - lse[m]) - [n == targets[m]] )
@@ -662,8 +671,10 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
  *              0 in ignored rows, NaN in rows with an invalid target
  * lse from (23) on the same arguments; dloss [M] fp32, the gradient of loss
  * (1 / count for the mean over count rows).  dx [M, K] bf16, written: (20) or
- * (21) take it back.  work: at least
- * cr_w4a8_cross_entropy_backward_work_bytes(M, V, K) bytes.
+ * (21) take it back.  Ignored rows cost little: in larger problems the others
+ * are gathered first.  work: at least
+ * cr_w4a8_cross_entropy_backward_work_bytes(M, V, K) bytes (some 0.5 GB at most
+ * for K = 4096).
  */
 int64_t cr_w4a8_cross_entropy_work_bytes(int64_t M, int64_t V, int64_t K);
 cr_status cr_w4a8_cross_entropy(const int8_t *xq, const float *xs, const uint8_t *qdata, const uint8_t *srel,

@@ -21,6 +21,9 @@
 //
 // All three are bound by HBM: the forward's floor is 2 bytes in per element
 // (4 with a residual) and 1 (3) out, the backward's 6 (8), the rotation's 4.
+// Measured on B200 (copy bandwidth 6.5 TB/s), inputs larger than L2: forward
+// 16384 x 8192 with a residual 167 us (5.6 TB/s), backward 8192 x 4096 with dres
+// and dgamma 51 us (5.2 TB/s), rotation 4096 x 12288 37.5 us (5.4 TB/s).
 #pragma once
 
 #include <climits>
