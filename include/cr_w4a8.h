@@ -569,7 +569,8 @@ cr_status cr_gemm_s8(const int8_t *xq, const float *xs, const int8_t *w8, const 
  * x, residual [M, K] bf16 bits; residual may be NULL.  gamma [K] bf16 or fp32
  * per gamma_dtype.  h [M, K] bf16 is written when a residual is given (and
  * required then); it may be x or residual itself, but not overlap them
- * otherwise; without a residual it is not written and may be NULL.
+ * otherwise; without a residual it is not written and may be NULL.  xq must
+ * not overlap x, residual or h (CR_ERR_INVALID_ARG, as for h).
  * xq [MP, K] int8, xs [MP] fp32, written.  rs [M] fp32 or NULL: what (20) needs.
  * eps in [1e-30, 1e30] (CR_ERR_INVALID_ARG otherwise); v must meet the bound
  * on activations.  MP, act_qmax as in (1).
@@ -657,7 +658,7 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
  * otherwise), any V.  M <= 8 takes the decode GEMV.
  *
  * xq [>= M, K] int8, xs [>= M] fp32, the layer as in (3); targets [M] int64.
- * loss [M], lse [M] fp32, written.  work: at least
+ * loss [M], lse [M] fp32, written (apart: CR_ERR_INVALID_ARG otherwise).  work: at least
  * cr_w4a8_cross_entropy_work_bytes(M, V, K) bytes, 16-byte aligned
  * (CR_ERR_INVALID_ARG when smaller): a decoded piece of the weight (64 MB or
  * 256 K bytes, whichever is more) and 8 bytes per row (of at most 32768 at a
@@ -670,8 +671,8 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
  *   dx[m, k] = bf16( dloss[m] * sum_n dl[m, n] * w[n, k] )   (w as in (13); the sum in fp32);
  *              0 in ignored rows, NaN in rows with an invalid target
  * lse from (23) on the same arguments; dloss [M] fp32, the gradient of loss
- * (1 / count for the mean over count rows).  dx [M, K] bf16, written: (20) or
- * (21) take it back.  Ignored rows cost little: in larger problems the others
+ * (1 / count for the mean over count rows).  dx [M, K] bf16, written, apart from
+ * xq (CR_ERR_INVALID_ARG otherwise): (20) or (21) take it back.  Ignored rows cost little: in larger problems the others
  * are gathered first.  work: at least
  * cr_w4a8_cross_entropy_backward_work_bytes(M, V, K) bytes (some 0.5 GB at most
  * for K = 4096).

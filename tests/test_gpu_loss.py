@@ -547,6 +547,46 @@ def test_training_step_on_a_stream_and_in_a_graph():
         assert all(torch.equal(eager[k], out[k]) for k in out)
 
 
+def test_decode_batch_loss_in_a_graph_and_on_a_stream():
+    """The loss and its gradient of a decode batch (the GEMV path), on another
+    stream whose inputs are dropped at once, and captured and replayed."""
+    M, V, K = 5, 3000, 512
+    ly = inputs.layer(V, K, 51)
+    w, _ = _layer_dev(ly)
+    sets = [_quantised(M, K, s)[2:] for s in (52, 53, 54)]
+    t = dev(_targets(M, V, 55))
+    one = torch.ones(M, device="cuda")
+
+    def both(xq, xs, **kw):
+        loss, lse = cr.cr_w4a8_cross_entropy(xq, xs, *w, t, **kw)
+        return loss, lse, cr.cr_w4a8_cross_entropy_backward(xq, xs, *w, t, lse, one, **kw)
+
+    refs = [both(*s) for s in sets]
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    for s, ref in zip(sets, refs):
+        got = both(s[0].clone(), s[1].clone(), stream=_after(stream))
+        junk = [torch.full_like(s[0], 99) for _ in range(4)]
+        stream.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, got)) and len(junk) == 4
+    xq, xs = sets[0][0].clone(), sets[0][1].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both(xq, xs)
+    for s, ref in zip(sets[::-1], refs[::-1]):
+        xq.copy_(s[0])
+        xs.copy_(s[1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, out))
+
+
+def _after(stream):
+    """`stream`, ordered behind the current one."""
+    stream.wait_stream(torch.cuda.current_stream())
+    return stream
+
+
 def test_two_streams_at_once():
     """Two steps whose kernels overlap share no workspace."""
     blks = [_Block(64, 512, 512, 900, seed=s) for s in (4, 5)]

@@ -37,6 +37,8 @@ def test_norm_quant_validation(L):
     assert call(res=C) == INVALID                       # a residual needs h
     assert call(res=C, h=A + 512) == INVALID            # h overlaps x without being x
     assert call(res=C, h=C + 512) == INVALID
+    assert call(xq=A + 1024) == INVALID                 # xq overlaps x
+    assert call(res=C, h=0x9000000, xq=C) == INVALID and call(res=C, h=B, xq=B) == INVALID
     for name in ("x", "gamma", "xq", "xs", "rs"):
         assert call(**{name: MIS}) == ALIGNMENT
     assert call(res=MIS, h=B) == ALIGNMENT and call(res=C, h=MIS) == ALIGNMENT
@@ -144,7 +146,7 @@ def test_cross_entropy_validation(L, backward):
     need = getattr(L, name + "_work_bytes")(16, 8, 256)
     assert need > 0 and getattr(L, name + "_work_bytes")(16, 0, 256) == 0
 
-    def call(ptrs=(A,) * 8, M=16, V=8, K=256, two=(B, C), dx=A, work=A, wb=need):
+    def call(ptrs=(A,) * 8, M=16, V=8, K=256, two=(B, C), dx=0x9000000, work=A, wb=need):
         f = getattr(L, name)
         if backward:
             return f(*ptrs, -100, *two, M, V, K, dx, work, wb, None)
@@ -162,6 +164,9 @@ def test_cross_entropy_validation(L, backward):
         assert call(two=two) == ALIGNMENT
     if backward:
         assert call(dx=None) == INVALID and call(dx=MIS) == ALIGNMENT
+        assert call(dx=A) == INVALID        # over xq
+    else:
+        assert call(two=(B, B)) == INVALID  # loss and lse in one place
     assert call(work=None) == INVALID and call(work=MIS) == ALIGNMENT and call(wb=need - 1) == INVALID
     assert call(ptrs=(None,) * 8, M=0, two=(None, None), dx=None, work=None, wb=0) == OK
 

@@ -278,6 +278,11 @@ def _on_stream(fn):
             stream = torch.cuda.ExternalStream(int(stream), device=dev)
         elif dev is not None and stream.device != dev:
             raise ValueError(f"stream of {stream.device}, the tensors are on {dev}")
+        if not torch.cuda.is_current_stream_capturing():
+            # the inputs are read by that stream: the allocator keeps their memory until it is done
+            for a in (*args, *kwargs.values()):
+                if isinstance(a, torch.Tensor) and a.is_cuda:
+                    a.record_stream(stream)
         with torch.cuda.stream(stream):
             return body(*args, **kwargs)
 

@@ -1175,7 +1175,10 @@ cr_status cr_rmsnorm_quant_act(const uint16_t *x, const uint16_t *residual, cons
     if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(h) || !aligned16(xq) ||
         !aligned16(xs) || !aligned16(rs))
         return CR_ERR_ALIGNMENT;
-    if (residual && (overlap_other(h, 2 * M * K, x, 2 * M * K) || overlap_other(h, 2 * M * K, residual, 2 * M * K)))
+    if (residual && (overlap_other(h, 2 * M * K, x, 2 * M * K) || overlap_other(h, 2 * M * K, residual, 2 * M * K) ||
+                     overlap(xq, MP * K, residual, 2 * M * K) || overlap(xq, MP * K, h, 2 * M * K)))
+        return CR_ERR_INVALID_ARG;
+    if (overlap(xq, MP * K, x, 2 * M * K))
         return CR_ERR_INVALID_ARG;
     DeviceState *d = nullptr;
     const cr_status ds = current_device(&d);
@@ -1552,6 +1555,8 @@ cr_status cr_w4a8_cross_entropy(const int8_t *xq, const float *xs, const uint8_t
     cr_status st = check_ce(xq, xs, qdata, srel, codebook, s_channel, bias, targets, M, V, K, loss, lse, lse);
     if (st != CR_OK || M == 0)
         return st;
+    if (overlap(loss, 4 * M, lse, 4 * M))
+        return CR_ERR_INVALID_ARG;
     const CeFwdWork w(work, M, V, K);
     st = check_work(work, work_bytes, w.bytes);
     if (st != CR_OK)
@@ -1615,6 +1620,8 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
     cr_status st = check_ce(xq, xs, qdata, srel, codebook, s_channel, bias, targets, M, V, K, dx, lse, dloss);
     if (st != CR_OK || M == 0)
         return st;
+    if (overlap(dx, 2 * M * K, xq, M * K))
+        return CR_ERR_INVALID_ARG;
     const CeBwdWork w(work, M, V, K);
     st = check_work(work, work_bytes, w.bytes);
     if (st != CR_OK)
