@@ -47,7 +47,7 @@ def test_norm_quant_validation(L):
 
 def test_norm_backward_validation(L):
     need = L.cr_rmsnorm_backward_work_bytes(4, 256)
-    assert need == 4 * 256 * 4
+    assert need == 256 * 4 and L.cr_rmsnorm_backward_work_bytes(4, 1280) == 4 * 1280 * 4
     assert L.cr_rmsnorm_backward_work_bytes(0, 256) == 0 and L.cr_rmsnorm_backward_work_bytes(4, 300) == 0
 
     def call(dr=A, h=B, gamma=A, gdt=0, rs=A, dres=None, M=4, K=256, dx=C, dg=A, work=A, wb=need):

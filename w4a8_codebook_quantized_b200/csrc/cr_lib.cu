@@ -1203,7 +1203,7 @@ int64_t cr_rmsnorm_backward_work_bytes(int64_t M, int64_t K)
 {
     if (M <= 0 || check_k(K) != CR_OK)
         return 0;
-    return cr::nm::backward_ctas(M, K) * K * 4;
+    return cr::nm::backward_groups(M, K) * K * 4;
 }
 
 cr_status cr_rmsnorm_backward(const uint16_t *dr, const uint16_t *h, const void *gamma, cr_out_dtype gamma_dtype,

@@ -83,6 +83,7 @@ __global__ void __cluster_dims__(kRowCtas, 1, 1) __launch_bounds__(kThreads)
             join(a, warp_stat[w]);
         stat = a;
     }
+    __syncwarp();
     cluster_sync();
     if (rank == 0 && threadIdx.x == 0) {
 #pragma unroll
@@ -93,6 +94,7 @@ __global__ void __cluster_dims__(kRowCtas, 1, 1) __launch_bounds__(kThreads)
             tl = ld_cluster_f2(mapa_shared(smem_u32(&target), (uint32_t)(t / slice))).x;
         finish_row(a, tl, t, ignore, V, loss + m, lse + m);
     }
+    __syncwarp();
     cluster_sync();  // nobody leaves while its shared memory may be read
 }
 

@@ -494,6 +494,87 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_pairs_kernel(const FwdArgs a)
     }
 }
 
+// ---------------------------------------------------------------- forward, many short rows
+//
+// K <= 1024: G half-warps per row (1 for K <= 512, 2 above), a pair of blocks
+// each, eight half-warps a CTA.  A row is one warp's or half a warp's, so its
+// two reductions are shuffles and no CTA-wide barrier is left; with a CTA per
+// row, three quarters of its threads had no block at K = 256 (393216 rows: 765
+// us instead of 196).
+template <int G, bool GBF16>
+__global__ void __launch_bounds__(128) rmsnorm_small_kernel(const FwdArgs a, int64_t MP)
+{
+    __shared__ __align__(16) uint64_t tr_all[8][256];
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, hw = tid >> 4, L = tid & 15;
+    const unsigned hmask = 0xFFFFu << (16 * (hw & 1)), rmask = G == 1 ? hmask : 0xFFFFFFFFu;
+    const int64_t m = (8 / G) * (int64_t)blockIdx.x + hw / G;
+    const int p = hw % G;  // the half-warp's pair of blocks
+    const int NB = (int)(a.K / 256);
+    if (m >= MP)
+        return;
+    if (m >= a.M) {  // padding row of the decode GEMV's operand
+        for (int64_t c = 16 * p + L; c < a.K / 16; c += 16 * G)
+            reinterpret_cast<uint4 *>(a.xq + m * a.K)[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (p == 0 && L == 0)
+            a.xs[m] = 1.0f;
+        return;
+    }
+    const bool one = 2 * p < NB, two = 2 * p + 1 < NB;
+    const int64_t at = m * a.K + 512 * p + 16 * L;
+    uint64_t *tr = tr_all[hw];
+    uint8_t *tb = reinterpret_cast<uint8_t *>(tr) + 64 * (hw & 1);
+    uint32_t w0[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u}, w1[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    double ss = 0.0;
+    auto load_h = [&](int64_t k, uint32_t (&w)[8]) {
+        load16(a.x + k, a.wide, w);
+        if (a.res != nullptr) {
+            uint32_t r[8];
+            load16(a.res + k, a.wide, r);
+            add16(w, r);
+            store16(a.h + k, a.wide, w);
+        }
+        ss += squares16(w);
+    };
+    if (one)
+        load_h(at, w0);
+    if (two)
+        load_h(at + 256, w1);
+#pragma unroll
+    for (int o = 8 * G; o >= 1; o >>= 1)
+        ss += __shfl_xor_sync(rmask, ss, o);
+    const float rs = (float)rsqrt(fma(ss, a.inv_k, a.eps));
+    const uint64_t rs2 = pair_both(rs);
+    float g0[16], g1[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        g0[i] = g1[i] = 0.0f;
+    if (one)
+        load_gamma16<GBF16>(a.gamma, 512 * p + 16 * L, g0);
+    if (two)
+        load_gamma16<GBF16>(a.gamma, 512 * p + 256 + 16 * L, g1);
+    uint64_t v[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[2 * i] = mul2(mul2(pack2(w0[i] << 16, w1[i] << 16), rs2),
+                        pack2(__float_as_uint(g0[2 * i]), __float_as_uint(g1[2 * i])));
+        v[2 * i + 1] = mul2(mul2(pack2(w0[i] & 0xFFFF0000u, w1[i] & 0xFFFF0000u), rs2),
+                            pack2(__float_as_uint(g0[2 * i + 1]), __float_as_uint(g1[2 * i + 1])));
+    }
+    rq::rotate_pair_regs(L, tr, hmask, v);
+    const uint32_t bits = __reduce_max_sync(rmask, __float_as_uint(rq::max_abs_pairs(v)));
+    const RowScale s(__uint_as_float(bits), a.qmax);
+    if (one)
+        rq::quantise_store_pair(v, s.scale, s.inv16, a.qmax, s.exact_row, L, tb, hmask, a.xq + m * a.K + 512 * p,
+                                two ? a.xq + m * a.K + 512 * p + 256 : nullptr);
+    if (p == 0 && L == 0) {
+        a.xs[m] = s.scale;
+        if (a.rs != nullptr)
+            a.rs[m] = rs;
+    }
+}
+
 template <bool GBF16, int THREADS>
 inline cudaError_t launch_fwd_rows(const FwdArgs &a, int64_t MP, cudaStream_t stream)
 {
@@ -505,7 +586,7 @@ inline cudaError_t launch_fwd_rows(const FwdArgs &a, int64_t MP, cudaStream_t st
     return launch_dependent(kern, dim3((unsigned)(MP)), THREADS, 0, stream, a);
 }
 
-// Opt the 384- and 512-thread CTAs of the packed form into their transpose
+// Opt the 384- to 1024-thread CTAs of the packed form into their transpose
 // buffers (above 48 KB).  Once per device, before the first launch.
 inline cudaError_t set_attributes()
 {
@@ -514,6 +595,8 @@ inline cudaError_t set_attributes()
         int bytes;
     };
     const Need need[] = {
+        {rmsnorm_pairs_kernel<1, false, 1024, true>, rq::smem_bytes<1024>()},
+        {rmsnorm_pairs_kernel<1, false, 1024, false>, rq::smem_bytes<1024>()},
         {rmsnorm_pairs_kernel<1, false, 512, true>, rq::smem_bytes<512>()},
         {rmsnorm_pairs_kernel<1, false, 512, false>, rq::smem_bytes<512>()},
         {rmsnorm_pairs_kernel<1, true, 512, true>, rq::smem_bytes<512>()},
@@ -534,6 +617,10 @@ inline cudaError_t launch_fwd_t(const FwdArgs &a, int64_t MP, cudaStream_t strea
 {
     if (MP <= rq::kShortRows)
         return a.K >= 8192 ? launch_fwd_rows<GBF16, 512>(a, MP, stream) : launch_fwd_rows<GBF16, 256>(a, MP, stream);
+    if (a.K <= 512)
+        return launch_dependent(rmsnorm_small_kernel<1, GBF16>, dim3((unsigned)((MP + 7) / 8)), 128, 0, stream, a, MP);
+    if (a.K <= 1024)
+        return launch_dependent(rmsnorm_small_kernel<2, GBF16>, dim3((unsigned)((MP + 3) / 4)), 128, 0, stream, a, MP);
     const int64_t pairs = (a.K / 256 + 1) / 2;
     if (pairs <= 4)
         return launch_dependent(rmsnorm_pairs_kernel<1, false, 64, GBF16>, dim3((unsigned)(MP)), 64, rq::smem_bytes<64>(), stream, a);
@@ -545,12 +632,16 @@ inline cudaError_t launch_fwd_t(const FwdArgs &a, int64_t MP, cudaStream_t strea
         return launch_dependent(rmsnorm_pairs_kernel<1, false, 384, GBF16>, dim3((unsigned)(MP)), 384, rq::smem_bytes<384>(), stream, a);
     if (pairs <= 32)
         return launch_dependent(rmsnorm_pairs_kernel<1, false, 512, GBF16>, dim3((unsigned)(MP)), 512, rq::smem_bytes<512>(), stream, a);
+    if (pairs <= 64)
+        return launch_dependent(rmsnorm_pairs_kernel<1, false, 1024, GBF16>, dim3((unsigned)(MP)), 1024,
+                                rq::smem_bytes<1024>(), stream, a);
     return launch_dependent(rmsnorm_pairs_kernel<1, true, 512, GBF16>, dim3((unsigned)(MP)), 512, rq::smem_bytes<512>(), stream, a);
 }
 
 // Short batches take the scalar form, 512 threads for K >= 8192 and 256 below;
-// longer ones the packed form with one half-warp per block pair where that fits
-// in 512 threads (K <= 16384), and the re-reading form beyond.
+// longer ones the packed form: several rows a CTA up to K = 1024, then one
+// half-warp per block pair while that fits a CTA (K <= 32768), and the
+// re-reading form beyond.
 inline cudaError_t launch_fwd(FwdArgs a, int64_t MP, bool gamma_bf16, cudaStream_t stream)
 {
     a.inv_k = 1.0 / (double)a.K;
@@ -691,11 +782,9 @@ inline cudaError_t launch_rotate(const uint16_t *x, int64_t M, int64_t K, uint16
 // ---------------------------------------------------------------- backward
 //
 // A persistent grid over rows, so that a CTA adds up its share of dgamma in
-// registers (one value per element of its blocks) and writes it once, as row
-// `blockIdx.x` of the partials [P, K]; a second kernel adds the partials in a
-// fixed order, so dgamma is the same from run to run.  kWide (rows longer than
-// the registers hold): dv is computed twice per row, and the CTA's partial row
-// is added to in memory by the thread that owns the element.
+// registers (one value per element of its blocks) and writes it once, as a row
+// of the partials [P, K]; a second kernel adds the partials in a fixed order, so
+// dgamma is the same from run to run.
 struct BwdArgs {
     const uint16_t *dr, *h;
     const void *gamma;
@@ -703,7 +792,7 @@ struct BwdArgs {
     const uint16_t *dres;
     int64_t M, K;
     uint16_t *dx;
-    float *part;  // [gridDim.x, K], or null: no dgamma
+    float *part;  // [P, K], or null: no dgamma
     bool wide;    // dr, h, dres and dx on 32-byte boundaries
 };
 
@@ -725,7 +814,194 @@ __device__ __forceinline__ float block_sum(float s, float (*warp_sum)[THREADS / 
     return t;
 }
 
-template <int J, bool kWide, int THREADS, bool GBF16>
+// What the backward kernels share: one block's arithmetic in packed pairs of
+// neighbouring elements.  V = 16 dv comes out of the rotation; the 1/16 (exact)
+// sits in rs16 = rs / 16: with
+//   g' = V * gamma,  xh' = h * rs16:  V * xh' = dv * xh,  g' * xh' = g * xh,
+//   dx = g' * rs16 + (h * (-rs * rs * c) + dres).
+struct BwdBlock {
+    uint32_t d[8], h[8], r[8];  // dr, h and dres of the block's sixteen elements
+
+    __device__ __forceinline__ void load(const BwdArgs &a, int64_t at)
+    {
+        load16(a.dr + at, a.wide, d);
+        load16(a.h + at, a.wide, h);
+        if (a.dres != nullptr) {
+            load16(a.dres + at, a.wide, r);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                r[i] = 0u;
+        }
+    }
+    // g' of the block; adds dv * xh to acc and g * xh to s
+    template <bool GBF16>
+    __device__ __forceinline__ void first(const BwdArgs &a, int64_t k, int L, float *tr, unsigned hmask, uint64_t rs16,
+                                          uint64_t (&g)[8], uint64_t (&acc)[8], uint64_t &s) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            g[i] = pair_of(d[i]);
+        rotate_rows16(L, tr, hmask, g);
+        uint64_t gm[8];
+        load_gamma_pairs<GBF16>(a.gamma, k, gm);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t xh = mul2(pair_of(h[i]), rs16);
+            acc[i] = fma2(g[i], xh, acc[i]);
+            g[i] = mul2(g[i], gm[i]);
+            s = fma2(g[i], xh, s);
+        }
+    }
+    __device__ __forceinline__ void finish(const BwdArgs &a, int64_t at, const uint64_t (&g)[8], float rs, float c) const
+    {
+        const uint64_t rs16 = pair_both(rs * 0.0625f), k = pair_both(-(rs * rs) * c);
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t lo, hi;
+            unpack2(fma2(g[i], rs16, fma2(pair_of(h[i]), k, pair_of(r[i]))), lo, hi);
+            o[i] = to_bf16x2_bits(__uint_as_float(lo), __uint_as_float(hi));
+        }
+        store16(a.dx + at, a.wide, o);
+    }
+};
+
+__device__ __forceinline__ float sum_pair(uint64_t v)
+{
+    uint32_t lo, hi;
+    unpack2(v, lo, hi);
+    return __uint_as_float(lo) + __uint_as_float(hi);
+}
+
+__device__ __forceinline__ void store_partial(float *p, const uint64_t (&acc)[8])
+{
+    ulonglong2 *pp = reinterpret_cast<ulonglong2 *>(p);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        pp[q] = make_ulonglong2(acc[2 * q], acc[2 * q + 1]);
+}
+
+// K <= 512: a row is half a warp's (K = 256) or a warp's, 8 / G rows at once in
+// a CTA of eight half-warps, the row's sum a few shuffles; a CTA adds up its
+// row groups' shares of dgamma in shared memory at the end.
+template <int G, bool GBF16>
+__global__ void __launch_bounds__(128) rmsnorm_backward_small_kernel(const BwdArgs a)
+{
+    __shared__ __align__(16) float tr_all[8][16 * 16 + 16];
+    __shared__ float share[8][256];
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int hw = threadIdx.x >> 4, L = threadIdx.x & 15, b = hw % G;
+    const unsigned hmask = 0xFFFFu << (16 * (hw & 1)), rmask = G == 1 ? hmask : 0xFFFFFFFFu;
+    const float inv_k = 1.0f / (float)a.K;
+    const int64_t k = 256 * b + 16 * L, step = (8 / G) * (int64_t)gridDim.x;
+    uint64_t acc[8] = {0ull, 0ull, 0ull, 0ull, 0ull, 0ull, 0ull, 0ull};
+    int64_t m = (8 / G) * (int64_t)blockIdx.x + hw / G;
+    BwdBlock next;
+    float nrs = 0.0f;
+    if (m < a.M) {
+        next.load(a, m * a.K + k);
+        nrs = a.rs[m];
+    }
+    for (; m < a.M; m += step) {
+        const BwdBlock cur = next;
+        const float rs = nrs;
+        if (m + step < a.M) {
+            next.load(a, (m + step) * a.K + k);
+            nrs = a.rs[m + step];
+        }
+        uint64_t g[8], s2 = 0ull;
+        cur.first<GBF16>(a, k, L, tr_all[hw], hmask, pair_both(rs * 0.0625f), g, acc, s2);
+        float s = sum_pair(s2);
+#pragma unroll
+        for (int o = 8 * G; o >= 1; o >>= 1)
+            s += __shfl_xor_sync(rmask, s, o);
+        cur.finish(a, m * a.K + k, g, rs, s * inv_k);
+    }
+    if (a.part == nullptr)
+        return;
+    store_partial(&share[hw][16 * L], acc);
+    __syncthreads();
+    for (int c = threadIdx.x; c < 256 * G; c += 128) {
+        float t = share[c >> 8][c & 255];
+#pragma unroll
+        for (int i = 1; i < 8 / G; ++i)
+            t += share[G * i + (c >> 8)][c & 255];
+        a.part[(int64_t)blockIdx.x * a.K + c] = t;
+    }
+}
+
+// 16384 < K <= 32768: a cluster of five to eight CTAs per row, each with a share
+// of its blocks (at most one per half-warp) and of dgamma's partial row; the
+// row's sum goes round by shared memory, one cluster barrier a row (the slots
+// alternate).  A CTA per row would have to rotate every block twice (16640
+// columns, 6049 rows: 463 us against 297).  For 8192 < K <= 16384 two blocks a
+// half-warp, some of them spilled, are still faster (8448: 258 us against 330).
+template <bool GBF16>
+__global__ void __launch_bounds__(256) rmsnorm_backward_cluster_kernel(const BwdArgs a, int ctas)
+{
+    constexpr int THREADS = 256;
+    constexpr int kHalfWarps = THREADS / 16;
+    __shared__ __align__(16) float tr_all[kHalfWarps][16 * 16 + 16];
+    __shared__ float warp_sum[2][THREADS / 32];
+    __shared__ __align__(8) float2 slot_sum[2];  // .x: this CTA's share of the row's sum
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int hw = threadIdx.x >> 4, L = threadIdx.x & 15;
+    const unsigned hmask = 0xFFFFu << (16 * (hw & 1));
+    const int rank = (int)cluster_ctarank(), NB = (int)(a.K / 256), per = (NB + ctas - 1) / ctas;
+    const int b = rank * per + hw;
+    const bool mine = hw < per && b < NB;
+    const int64_t k = 256 * (int64_t)b + 16 * L, row0 = blockIdx.x / ctas, step = gridDim.x / ctas;
+    const float inv_k = 1.0f / (float)a.K;
+    uint64_t acc[8] = {0ull, 0ull, 0ull, 0ull, 0ull, 0ull, 0ull, 0ull};
+    BwdBlock next;
+    float nrs = 0.0f;
+    auto fetch = [&](int64_t m) {
+        if (m < a.M) {
+            nrs = a.rs[m];
+            if (mine)
+                next.load(a, m * a.K + k);
+        }
+    };
+    fetch(row0);
+    int slot = 0;
+    for (int64_t m = row0; m < a.M; m += step, slot ^= 1) {
+        const BwdBlock cur = next;
+        const float rs = nrs;
+        fetch(m + step);
+        uint64_t g[8], s2 = 0ull;
+        if (mine)
+            cur.first<GBF16>(a, k, L, tr_all[hw], hmask, pair_both(rs * 0.0625f), g, acc, s2);
+        const float own = block_sum<THREADS>(sum_pair(s2), warp_sum, slot);
+        if (threadIdx.x == 0)
+            slot_sum[slot].x = own;
+        __syncwarp();
+        cluster_sync();
+        // lane r of every warp fetches CTA r's share (one remote load in flight a
+        // warp, not one after another), added by a butterfly
+        const int lane = threadIdx.x & 31;
+        float sum = 0.0f;
+        if (lane < ctas)
+            sum = ld_cluster_f2(mapa_shared(smem_u32(&slot_sum[slot]), (uint32_t)lane)).x;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (mine)
+            cur.finish(a, m * a.K + k, g, rs, sum * inv_k);
+    }
+    if (a.part != nullptr && mine)
+        store_partial(a.part + row0 * a.K + k, acc);
+    __syncwarp();
+    cluster_sync();  // nobody leaves while its shared memory may be read
+}
+
+// One CTA per row at a time, J blocks per half-warp (512 < K <= 16384); with one
+// block the next row's values are loaded while the current row is worked on.
+// (Written out, not with BwdBlock: the compiler kept the struct form's registers
+// in another order, and 8192 x 4096 took 57 us instead of 51.)
+template <int J, int THREADS, bool GBF16>
 __global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(const BwdArgs a)
 {
     constexpr int kHalfWarps = THREADS / 16;
@@ -740,18 +1016,13 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(const BwdArgs
     const float inv_k = 1.0f / (float)a.K;
     float *tr = tr_all[hw];
     float *prow = a.part != nullptr ? a.part + (int64_t)blockIdx.x * a.K : nullptr;
-    constexpr int kHeld = kWide ? 1 : J;
-    uint64_t acc[kHeld][8];
+    uint64_t acc[J][8];
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j)
+    for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             acc[j][i] = 0ull;
 
-    // Packed pairs of neighbouring elements throughout.  V = 16 dv comes out of
-    // the rotation; the 1/16 (exact) sits in rs16 = rs / 16: with
-    //   g' = V * gamma,  xh' = h * rs16:  V * xh' = dv * xh,  g' * xh' = g * xh,
-    //   dx = g' * rs16 + (h * (-rs * rs * c) + dres).
     auto rotated = [&](const uint32_t (&w)[8], uint64_t (&v)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -770,136 +1041,136 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(const BwdArgs
         }
         store16(a.dx + at, a.wide, o);
     };
-    auto sum_pair = [](uint64_t v) {
-        uint32_t lo, hi;
-        unpack2(v, lo, hi);
-        return __uint_as_float(lo) + __uint_as_float(hi);
-    };
-
     int slot = 0;
-    if constexpr (!kWide) {
-        // the next row's values are loaded while the current row is worked on
-        uint32_t nd[J][8], nh[J][8], nr[J][8];
-        float nrs = 0.0f;
-        auto fetch = [&](int64_t m) {
-            if (m >= a.M)
-                return;
-            nrs = a.rs[m];
+    // the next row's values are loaded while the current row is worked on
+    uint32_t nd[J][8], nh[J][8], nr[J][8];
+    float nrs = 0.0f;
+    auto fetch = [&](int64_t m) {
+        if (m >= a.M)
+            return;
+        nrs = a.rs[m];
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int b = hw + kHalfWarps * j;
-                if (b < NB) {
-                    const int64_t at = m * a.K + 256 * b + 16 * L;
-                    load16(a.dr + at, a.wide, nd[j]);
-                    load16(a.h + at, a.wide, nh[j]);
-                    if (a.dres != nullptr) {
-                        load16(a.dres + at, a.wide, nr[j]);
-                    } else {
+        for (int j = 0; j < J; ++j) {
+            const int b = hw + kHalfWarps * j;
+            if (b < NB) {
+                const int64_t at = m * a.K + 256 * b + 16 * L;
+                load16(a.dr + at, a.wide, nd[j]);
+                load16(a.h + at, a.wide, nh[j]);
+                if (a.dres != nullptr) {
+                    load16(a.dres + at, a.wide, nr[j]);
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            nr[j][i] = 0u;
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        nr[j][i] = 0u;
                 }
             }
-        };
-        constexpr bool kAhead = J == 1;  // two blocks a half-warp leave no registers for it
-        if (kAhead)
-            fetch(blockIdx.x);
-        for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, slot ^= 1) {
-            if (!kAhead)
-                fetch(m);
-            const float rs = nrs;
-            const uint64_t rs16 = pair_both(rs * 0.0625f);
-            uint64_t s = 0ull, g[J][8];
-            uint32_t hp[J][8], r[J][8], d[J][8];
+        }
+    };
+    constexpr bool kAhead = J == 1;  // two blocks a half-warp leave no registers for it
+    if (kAhead)
+        fetch(blockIdx.x);
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, slot ^= 1) {
+        if (!kAhead)
+            fetch(m);
+        const float rs = nrs;
+        const uint64_t rs16 = pair_both(rs * 0.0625f);
+        uint64_t s = 0ull, g[J][8];
+        uint32_t hp[J][8], r[J][8], d[J][8];
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                d[j][i] = nd[j][i];
+                hp[j][i] = nh[j][i];
+                r[j][i] = nr[j][i];
+            }
+        if (kAhead)
+            fetch(m + gridDim.x);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int b = hw + kHalfWarps * j;
+            if (b < NB) {
+                rotated(d[j], g[j]);
+                uint64_t gm[8];
+                load_gamma_pairs<GBF16>(a.gamma, 256 * b + 16 * L, gm);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    d[j][i] = nd[j][i];
-                    hp[j][i] = nh[j][i];
-                    r[j][i] = nr[j][i];
-                }
-            if (kAhead)
-                fetch(m + gridDim.x);
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int b = hw + kHalfWarps * j;
-                if (b < NB) {
-                    rotated(d[j], g[j]);
-                    uint64_t gm[8];
-                    load_gamma_pairs<GBF16>(a.gamma, 256 * b + 16 * L, gm);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint64_t xh = mul2(pair_of(hp[j][i]), rs16);
-                        acc[j][i] = fma2(g[j][i], xh, acc[j][i]);
-                        g[j][i] = mul2(g[j][i], gm[i]);
-                        s = fma2(g[j][i], xh, s);
-                    }
-                }
-            }
-            const float c = block_sum<THREADS>(sum_pair(s), warp_sum, slot) * inv_k;
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int b = hw + kHalfWarps * j;
-                if (b < NB)
-                    finish(m * a.K + 256 * b + 16 * L, g[j], hp[j], r[j], rs, c);
-            }
-        }
-        if (prow != nullptr) {
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int b = hw + kHalfWarps * j;
-                if (b < NB) {
-                    ulonglong2 *pp = reinterpret_cast<ulonglong2 *>(prow + 256 * b + 16 * L);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        pp[q] = make_ulonglong2(acc[j][2 * q], acc[j][2 * q + 1]);
+                    const uint64_t xh = mul2(pair_of(hp[j][i]), rs16);
+                    acc[j][i] = fma2(g[j][i], xh, acc[j][i]);
+                    g[j][i] = mul2(g[j][i], gm[i]);
+                    s = fma2(g[j][i], xh, s);
                 }
             }
         }
-    } else {
-        for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, slot ^= 1) {
-            const float rs = a.rs[m];
-            const uint64_t rs16 = pair_both(rs * 0.0625f);
-            uint64_t s = 0ull, g[8], gm[8];
-            uint32_t hp[8], d[8];
-            for (int b = hw; b < NB; b += kHalfWarps) {
-                const int64_t at = m * a.K + 256 * b + 16 * L;
-                load16(a.dr + at, a.wide, d);
-                load16(a.h + at, a.wide, hp);
-                rotated(d, g);
-                load_gamma_pairs<GBF16>(a.gamma, 256 * b + 16 * L, gm);
+        const float c = block_sum<THREADS>(sum_pair(s), warp_sum, slot) * inv_k;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int b = hw + kHalfWarps * j;
+            if (b < NB)
+                finish(m * a.K + 256 * b + 16 * L, g[j], hp[j], r[j], rs, c);
+        }
+    }
+    if (prow != nullptr) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int b = hw + kHalfWarps * j;
+            if (b < NB) {
                 ulonglong2 *pp = reinterpret_cast<ulonglong2 *>(prow + 256 * b + 16 * L);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint64_t xh[2];
+                for (int q = 0; q < 4; ++q)
+                    pp[q] = make_ulonglong2(acc[j][2 * q], acc[j][2 * q + 1]);
+            }
+        }
+    }
+}
+
+// Rows longer than a cluster holds (K > 32768): every block is read and rotated
+// twice, and the CTA's partial row of dgamma is added to in memory by the
+// thread that owns the element (65536 columns, 1536 rows: 365 us; a cluster of
+// CTAs of 512 threads took 529).
+template <bool GBF16>
+__global__ void __launch_bounds__(512) rmsnorm_backward_wide_kernel(const BwdArgs a)
+{
+    constexpr int kHalfWarps = 32;
+    __shared__ __align__(16) float tr_all[kHalfWarps][16 * 16 + 16];
+    __shared__ float warp_sum[2][16];
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int hw = threadIdx.x >> 4, L = threadIdx.x & 15;
+    const unsigned hmask = 0xFFFFu << (16 * (hw & 1));
+    const int NB = (int)(a.K / 256);
+    const float inv_k = 1.0f / (float)a.K;
+    int slot = 0;
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, slot ^= 1) {
+        const float rs = a.rs[m];
+        const uint64_t rs16 = pair_both(rs * 0.0625f);
+        uint64_t g[8], s2 = 0ull;
+        BwdBlock blk;
+        for (int b = hw; b < NB; b += kHalfWarps) {
+            const int64_t k = 256 * (int64_t)b + 16 * L;
+            float *pp = a.part != nullptr ? a.part + (int64_t)blockIdx.x * a.K + k : nullptr;
+            uint64_t acc[8] = {0ull, 0ull, 0ull, 0ull, 0ull, 0ull, 0ull, 0ull};
+            if (pp != nullptr && m != blockIdx.x) {
+                const ulonglong2 *p2 = reinterpret_cast<const ulonglong2 *>(pp);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        xh[e] = mul2(pair_of(hp[2 * q + e]), rs16);
-                        s = fma2(mul2(g[2 * q + e], gm[2 * q + e]), xh[e], s);
-                    }
-                    if (prow != nullptr) {
-                        const ulonglong2 t = m == blockIdx.x ? make_ulonglong2(0ull, 0ull) : pp[q];
-                        pp[q] = make_ulonglong2(fma2(g[2 * q], xh[0], t.x), fma2(g[2 * q + 1], xh[1], t.y));
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    const ulonglong2 t = p2[q];
+                    acc[2 * q] = t.x;
+                    acc[2 * q + 1] = t.y;
                 }
             }
-            const float c = block_sum<THREADS>(sum_pair(s), warp_sum, slot) * inv_k;
-            for (int b = hw; b < NB; b += kHalfWarps) {
-                const int64_t at = m * a.K + 256 * b + 16 * L;
-                uint32_t r[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-                load16(a.dr + at, a.wide, d);
-                load16(a.h + at, a.wide, hp);
-                if (a.dres != nullptr)
-                    load16(a.dres + at, a.wide, r);
-                rotated(d, g);
-                load_gamma_pairs<GBF16>(a.gamma, 256 * b + 16 * L, gm);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    g[i] = mul2(g[i], gm[i]);
-                finish(at, g, hp, r, rs, c);
-            }
+            blk.load(a, m * a.K + k);
+            blk.first<GBF16>(a, k, L, tr_all[hw], hmask, rs16, g, acc, s2);
+            if (pp != nullptr)
+                store_partial(pp, acc);
+        }
+        const float c = block_sum<512>(sum_pair(s2), warp_sum, slot) * inv_k;
+        for (int b = hw; b < NB; b += kHalfWarps) {
+            const int64_t k = 256 * (int64_t)b + 16 * L;
+            uint64_t acc[8] = {0ull, 0ull, 0ull, 0ull, 0ull, 0ull, 0ull, 0ull};
+            blk.load(a, m * a.K + k);
+            blk.first<GBF16>(a, k, L, tr_all[hw], hmask, rs16, g, acc, s2);
+            blk.finish(a, m * a.K + k, g, rs, c);
         }
     }
 }
@@ -931,34 +1202,78 @@ __global__ void __launch_bounds__(32 * kSumWarps) dgamma_kernel(const float *__r
     }
 }
 
-// CTAs of the backward's grid, and with it the partial rows of dgamma: a
-// function of the shape alone, so that the caller's workspace has a fixed size.
-inline int64_t backward_ctas(int64_t M, int64_t K)
+// CTAs of a row's cluster for 16384 < K <= 32768: 4096 columns (256 threads, two
+// CTAs an SM) each.
+inline int cluster_ctas(int64_t K) { return (int)((K + 4095) / 4096); }
+
+// Row groups of the backward's grid (CTAs, or clusters), and with it the
+// partial rows of dgamma: a function of the shape alone, so that the caller's
+// workspace has a fixed size.  A cluster's CTAs share a GPC; eight GPCs of at
+// least 16 SMs are counted on, so that every cluster is resident from the start
+// (with two more than fit, 16384 took twice the time).
+inline int64_t backward_groups(int64_t M, int64_t K)
 {
-    const int64_t most = K <= 1024 ? 148 * 8 : K <= 2048 ? 148 * 4 : K <= 4096 ? 148 * 2 : 148;
-    return M < most ? M : most;
+    const int64_t most = K <= 512     ? 148 * 4
+                         : K <= 1024  ? 148 * 8
+                         : K <= 2048  ? 148 * 4
+                         : K <= 4096  ? 148 * 2
+                         : K > 16384 && K <= 32768 ? 32 / cluster_ctas(K) * 8
+                                                   : 148;
+    const int64_t rows = K == 256 ? 8 : K == 512 ? 4 : 1;  // a group's rows at once
+    const int64_t need = (M + rows - 1) / rows;
+    return need < most ? need : most;
+}
+
+// A launch in clusters, as a programmatic dependent.
+template <class... Args>
+inline cudaError_t launch_clusters(void (*kern)(Args...), int64_t clusters, int ctas, int threads, cudaStream_t stream,
+                                   Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * ctas));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <bool GBF16>
 inline cudaError_t launch_bwd_t(const BwdArgs &a, float *dgamma, cudaStream_t stream)
 {
-    const int64_t P = backward_ctas(a.M, a.K);
+    const int64_t P = backward_groups(a.M, a.K);
+    const dim3 grid((unsigned)P);
     cudaError_t e;
-    if (a.K <= 1024)
-        e = launch_dependent(rmsnorm_backward_kernel<1, false, 64, GBF16>, dim3((unsigned)(P)), 64, 0, stream, a);
+    if (a.K == 256)
+        e = launch_dependent(rmsnorm_backward_small_kernel<1, GBF16>, grid, 128, 0, stream, a);
+    else if (a.K == 512)
+        e = launch_dependent(rmsnorm_backward_small_kernel<2, GBF16>, grid, 128, 0, stream, a);
+    else if (a.K <= 1024)
+        e = launch_dependent(rmsnorm_backward_kernel<1, 64, GBF16>, grid, 64, 0, stream, a);
     else if (a.K <= 2048)
-        e = launch_dependent(rmsnorm_backward_kernel<1, false, 128, GBF16>, dim3((unsigned)(P)), 128, 0, stream, a);
+        e = launch_dependent(rmsnorm_backward_kernel<1, 128, GBF16>, grid, 128, 0, stream, a);
     else if (a.K <= 4096)
-        e = launch_dependent(rmsnorm_backward_kernel<1, false, 256, GBF16>, dim3((unsigned)(P)), 256, 0, stream, a);
+        e = launch_dependent(rmsnorm_backward_kernel<1, 256, GBF16>, grid, 256, 0, stream, a);
     else if (a.K <= 8192)
-        e = launch_dependent(rmsnorm_backward_kernel<1, false, 512, GBF16>, dim3((unsigned)(P)), 512, 0, stream, a);
+        e = launch_dependent(rmsnorm_backward_kernel<1, 512, GBF16>, grid, 512, 0, stream, a);
     else if (a.K <= 16384)
-        e = launch_dependent(rmsnorm_backward_kernel<2, false, 512, GBF16>, dim3((unsigned)(P)), 512, 0, stream, a);
+        e = launch_dependent(rmsnorm_backward_kernel<2, 512, GBF16>, grid, 512, 0, stream, a);
+    else if (a.K <= 32768)
+        e = launch_clusters(rmsnorm_backward_cluster_kernel<GBF16>, P, cluster_ctas(a.K), 256, stream, a,
+                            cluster_ctas(a.K));
     else
-        e = launch_dependent(rmsnorm_backward_kernel<1, true, 512, GBF16>, dim3((unsigned)(P)), 512, 0, stream, a);
+        e = launch_dependent(rmsnorm_backward_wide_kernel<GBF16>, grid, 512, 0, stream, a);
     if (e != cudaSuccess || dgamma == nullptr)
         return e;
-    return launch_dependent(dgamma_kernel, dim3((unsigned)(a.K / 32)), 32 * kSumWarps, 0, stream, (const float *)a.part, (int)P, a.K, dgamma);
+    return launch_dependent(dgamma_kernel, dim3((unsigned)(a.K / 32)), 32 * kSumWarps, 0, stream, (const float *)a.part,
+                            (int)P, a.K, dgamma);
 }
 
 inline cudaError_t launch_bwd(BwdArgs a, bool gamma_bf16, float *dgamma, cudaStream_t stream)
