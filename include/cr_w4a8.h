@@ -569,8 +569,9 @@ cr_status cr_gemm_s8(const int8_t *xq, const float *xs, const int8_t *w8, const 
  * x, residual [M, K] bf16 bits; residual may be NULL.  gamma [K] bf16 or fp32
  * per gamma_dtype.  h [M, K] bf16 is written when a residual is given (and
  * required then); it may be x or residual itself, but not overlap them
- * otherwise; without a residual it is not written and may be NULL.  xq must
- * not overlap x, residual or h (CR_ERR_INVALID_ARG, as for h).
+ * otherwise; without a residual it is not written and may be NULL.  Here and in
+ * (20) to (23) no other written buffer (work is one) may overlap another one of
+ * the call's buffers (CR_ERR_INVALID_ARG, as for h).
  * xq [MP, K] int8, xs [MP] fp32, written.  rs [M] fp32 or NULL: what (20) needs.
  * eps in [1e-30, 1e30] (CR_ERR_INVALID_ARG otherwise); v must meet the bound
  * on activations.  MP, act_qmax as in (1).
@@ -592,8 +593,8 @@ cr_status cr_rmsnorm_quant_act(const uint16_t *x, const uint16_t *residual, cons
  *
  * h [M, K] bf16 and rs [M] fp32 from (19) (h = x without a residual); gamma as
  * there.  dres [M, K] bf16 or NULL: the gradient that reaches h by the residual
- * path, added in.  dx may be dr or dres itself, but not overlap them otherwise,
- * nor h.  dgamma [K] fp32, or NULL when it is not wanted; when given, work
+ * path, added in.  dx may be dr or dres itself, but not overlap them otherwise.
+ * dgamma [K] fp32, or NULL when it is not wanted; when given, work
  * holds cr_rmsnorm_backward_work_bytes(M, K) bytes (16-byte aligned;
  * CR_ERR_INVALID_ARG when smaller), else it is not used.  dgamma is the same
  * from run to run (no atomics).  M == 0 writes dgamma = 0.
@@ -632,8 +633,7 @@ cr_status cr_rotate(const uint16_t *x, int64_t M, int64_t K, uint16_t *out, cr_s
  * dout [M, N / 2] bf16; xq [>= M, K] int8 and xs [>= M] fp32: the quantised
  * activations of the forward; the interleaved layer as in (9).  dx [M, K] bf16,
  * dz [M, N] bf16, written.  N must be a multiple of 8 (CR_ERR_UNSUPPORTED
- * otherwise); N == 0 writes dx = 0.  dout, dx and dz must not overlap
- * (CR_ERR_INVALID_ARG).  work: at least
+ * otherwise); N == 0 writes dx = 0.  work: at least
  * cr_w4a8_swiglu_backward_work_bytes(M, N, K) bytes (the decoded weight, 3 N K,
  * and up to 20 MB for a split reduction), 16-byte aligned; CR_ERR_INVALID_ARG
  * when smaller.  Nothing is allocated.
@@ -658,7 +658,7 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
  * otherwise), any V.  M <= 8 takes the decode GEMV.
  *
  * xq [>= M, K] int8, xs [>= M] fp32, the layer as in (3); targets [M] int64.
- * loss [M], lse [M] fp32, written (apart: CR_ERR_INVALID_ARG otherwise).  work: at least
+ * loss [M], lse [M] fp32, written.  work: at least
  * cr_w4a8_cross_entropy_work_bytes(M, V, K) bytes, 16-byte aligned
  * (CR_ERR_INVALID_ARG when smaller): a decoded piece of the weight (64 MB or
  * 256 K bytes, whichever is more) and 8 bytes per row (of at most 32768 at a
@@ -671,8 +671,7 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
  *   dx[m, k] = bf16( dloss[m] * sum_n dl[m, n] * w[n, k] )   (w as in (13); the sum in fp32);
  *              0 in ignored rows, NaN in rows with an invalid target
  * lse from (23) on the same arguments; dloss [M] fp32, the gradient of loss
- * (1 / count for the mean over count rows).  dx [M, K] bf16, written, apart from
- * xq (CR_ERR_INVALID_ARG otherwise): (20) or (21) take it back.  Ignored rows cost little: in larger problems the others
+ * (1 / count for the mean over count rows).  dx [M, K] bf16, written: (20) or (21) take it back.  Ignored rows cost little: in larger problems the others
  * are gathered first.  work: at least
  * cr_w4a8_cross_entropy_backward_work_bytes(M, V, K) bytes (some 0.5 GB at most
  * for K = 4096).

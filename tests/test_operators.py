@@ -5,6 +5,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 import oracle
 import w4a8_codebook_quantized_b200 as cr
@@ -15,6 +16,7 @@ from operator_refs import hadamard, norm_backward, norm_quant, rotate32, rotate6
 A, B, C = 0x10000, 0x4000000, 0x8000000  # aligned stand-in addresses far apart; never dereferenced
 MIS = 0x10008
 OK, INVALID, UNSUPPORTED, ALIGNMENT = (cr.CR_OK, cr.CR_ERR_INVALID_ARG, cr.CR_ERR_UNSUPPORTED, cr.CR_ERR_ALIGNMENT)
+NO_DEVICE = cr.CR_ERR_NO_DEVICE
 
 
 @pytest.fixture(scope="module")
@@ -179,3 +181,56 @@ def test_work_sizes_are_bounded(L):
     assert b(1 << 20, 262144, 4096) == b(8192, 262144, 4096)
     assert f(2048, 262144, 4096) <= (64 << 20) + (2048 * 1024 * 8) + (1 << 20)
     assert f(1 << 20, 131072, 4096) == f(32768, 131072, 4096)
+
+
+def test_written_buffers_overlap_nothing(L):
+    """Any written buffer over another of the call's buffers is refused.  The
+    addresses below (16 MB apart) belong to nothing, so this runs only where a
+    call that is not refused ends at the missing device."""
+    if torch.cuda.is_available():
+        pytest.skip("the good calls would run")
+    at = [0x10000000 + (i << 24) for i in range(16)]
+
+    def pairs(call, written, read):
+        for w in written:
+            for o in [o for o in written if o != w] + read:
+                assert call({w: o}) == INVALID, (w, o)
+        assert call({}) == NO_DEVICE
+
+    def norm(same):
+        a = lambda i: at[same.get(i, i)]
+        return L.cr_rmsnorm_quant_act(a(0), a(1), a(2), 1, 1e-6, 4, 256, 4, 127, a(3), a(4), a(5), a(6), None)
+
+    pairs(norm, [4, 5, 6], [0, 1, 2, 3])
+    assert norm({3: 2}) == INVALID
+
+    def norm_backward(same):
+        a = lambda i: at[same.get(i, i)]
+        return L.cr_rmsnorm_backward(a(0), a(1), a(2), 0, a(3), a(4), 4, 256, a(5), a(6), a(7), 4 * 4 * 256, None)
+
+    pairs(norm_backward, [6, 7], [0, 1, 2, 3, 4, 5])
+    for o in (1, 2, 3, 6, 7):
+        assert norm_backward({5: o}) == INVALID
+    assert norm_backward({5: 0}) == NO_DEVICE and norm_backward({5: 4}) == NO_DEVICE  # in place
+
+    def swiglu(same):
+        a = lambda i: at[same.get(i, i)]
+        need = L.cr_w4a8_swiglu_backward_work_bytes(4, 8, 256)
+        return L.cr_w4a8_swiglu_backward(*(a(i) for i in range(8)), 4, 8, 256, a(8), a(9), a(10), need, None)
+
+    pairs(swiglu, [8, 9, 10], list(range(8)))
+
+    def ce(same):
+        a = lambda i: at[same.get(i, i)]
+        need = L.cr_w4a8_cross_entropy_work_bytes(16, 8, 256)
+        return L.cr_w4a8_cross_entropy(*(a(i) for i in range(8)), -100, 16, 8, 256, a(8), a(9), a(10), need, None)
+
+    pairs(ce, [8, 9, 10], list(range(8)))
+
+    def ce_backward(same):
+        a = lambda i: at[same.get(i, i)]
+        need = L.cr_w4a8_cross_entropy_backward_work_bytes(16, 8, 256)
+        return L.cr_w4a8_cross_entropy_backward(*(a(i) for i in range(8)), -100, a(8), a(9), 16, 8, 256, a(10), a(11),
+                                                need, None)
+
+    pairs(ce_backward, [10, 11], list(range(10)))

@@ -12,6 +12,7 @@
 #include <functional>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 #include <mutex>
 
@@ -1152,6 +1153,26 @@ bool overlap_other(const void *a, int64_t na, const void *b, int64_t nb)
     return a != b && overlap(a, na, b, nb);
 }
 
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+
+// Whether a buffer that a call writes shares a byte with another one that it
+// writes, or with one that it reads.
+bool collide(std::initializer_list<Span> written, std::initializer_list<Span> read)
+{
+    for (const Span *w = written.begin(); w != written.end(); ++w) {
+        for (const Span *o = w + 1; o != written.end(); ++o)
+            if (overlap(w->p, w->bytes, o->p, o->bytes))
+                return true;
+        for (const Span &r : read)
+            if (overlap(w->p, w->bytes, r.p, r.bytes))
+                return true;
+    }
+    return false;
+}
+
 bool bad_out_dtype(cr_out_dtype t) { return t != CR_OUT_BF16 && t != CR_OUT_F32; }
 }  // namespace
 
@@ -1175,10 +1196,11 @@ cr_status cr_rmsnorm_quant_act(const uint16_t *x, const uint16_t *residual, cons
     if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(h) || !aligned16(xq) ||
         !aligned16(xs) || !aligned16(rs))
         return CR_ERR_ALIGNMENT;
-    if (residual && (overlap_other(h, 2 * M * K, x, 2 * M * K) || overlap_other(h, 2 * M * K, residual, 2 * M * K) ||
-                     overlap(xq, MP * K, residual, 2 * M * K) || overlap(xq, MP * K, h, 2 * M * K)))
-        return CR_ERR_INVALID_ARG;
-    if (overlap(xq, MP * K, x, 2 * M * K))
+    const int64_t io = 2 * M * K, gb = K * (gamma_dtype == CR_OUT_F32 ? 4 : 2);
+    const uint16_t *ho = residual ? h : nullptr;  // written with a residual only
+    if (overlap_other(ho, io, x, io) || overlap_other(ho, io, residual, io) ||
+        collide({{xq, MP * K}, {xs, 4 * MP}, {rs, 4 * M}, {ho, io}}, {{gamma, gb}}) ||
+        collide({{xq, MP * K}, {xs, 4 * MP}, {rs, 4 * M}}, {{x, io}, {residual, io}}))
         return CR_ERR_INVALID_ARG;
     DeviceState *d = nullptr;
     const cr_status ds = current_device(&d);
@@ -1222,10 +1244,13 @@ cr_status cr_rmsnorm_backward(const uint16_t *dr, const uint16_t *h, const void 
     if (!aligned16(dr) || !aligned16(h) || !aligned16(gamma) || !aligned16(rs) || !aligned16(dres) ||
         !aligned16(dx) || !aligned16(dgamma) || !aligned16(work))
         return CR_ERR_ALIGNMENT;
-    if (M > 0 && dgamma && (!work || work_bytes < cr_rmsnorm_backward_work_bytes(M, K)))
+    const int64_t wb = dgamma ? cr_rmsnorm_backward_work_bytes(M, K) : 0;
+    if (M > 0 && dgamma && (!work || work_bytes < wb))
         return CR_ERR_INVALID_ARG;
-    if (overlap(dx, 2 * M * K, h, 2 * M * K) || overlap_other(dx, 2 * M * K, dr, 2 * M * K) ||
-        overlap_other(dx, 2 * M * K, dres, 2 * M * K))
+    const int64_t io = 2 * M * K, gb = K * (gamma_dtype == CR_OUT_F32 ? 4 : 2);
+    if (overlap_other(dx, io, dr, io) || overlap_other(dx, io, dres, io) ||
+        collide({{dx, io}, {dgamma, 4 * K}, {work, wb}}, {{h, io}, {gamma, gb}, {rs, 4 * M}}) ||
+        collide({{dgamma, 4 * K}, {work, wb}}, {{dr, io}, {dres, io}}))
         return CR_ERR_INVALID_ARG;
     if (M == 0 && !dgamma)
         return CR_OK;
@@ -1505,13 +1530,14 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
     st = check_contraction(xq, xs, qdata, srel, codebook, s_channel, bias, M, N, K, CR_OUT_BF16, dz, nullptr);
     if (st != CR_OK)
         return st;
-    if (overlap(dz, 2 * M * N, dout, M * N) || overlap(dz, 2 * M * N, dx, 2 * M * K) ||
-        overlap(dx, 2 * M * K, dout, M * N))
-        return CR_ERR_INVALID_ARG;
     const SwigluWork w(work, M, N, K);
     st = check_work(work, work_bytes, w.bytes);
     if (st != CR_OK)
         return st;
+    if (collide({{dx, 2 * M * K}, {dz, 2 * M * N}, {work, w.bytes}},
+                {{dout, M * N}, {xq, M * K}, {xs, 4 * M}, {qdata, N * K / 2}, {srel, N * K / 16}, {codebook, 64},
+                 {s_channel, 4 * N}, {bias, 4 * N}}))
+        return CR_ERR_INVALID_ARG;
     DeviceState *d = nullptr;
     st = current_device(&d);
     if (st != CR_OK)
@@ -1555,12 +1581,14 @@ cr_status cr_w4a8_cross_entropy(const int8_t *xq, const float *xs, const uint8_t
     cr_status st = check_ce(xq, xs, qdata, srel, codebook, s_channel, bias, targets, M, V, K, loss, lse, lse);
     if (st != CR_OK || M == 0)
         return st;
-    if (overlap(loss, 4 * M, lse, 4 * M))
-        return CR_ERR_INVALID_ARG;
     const CeFwdWork w(work, M, V, K);
     st = check_work(work, work_bytes, w.bytes);
     if (st != CR_OK)
         return st;
+    if (collide({{loss, 4 * M}, {lse, 4 * M}, {work, w.bytes}},
+                {{xq, M * K}, {xs, 4 * M}, {qdata, V * K / 2}, {srel, V * K / 16}, {codebook, 64},
+                 {s_channel, 4 * V}, {bias, 4 * V}, {targets, 8 * M}}))
+        return CR_ERR_INVALID_ARG;
     DeviceState *d = nullptr;
     st = current_device(&d);
     if (st != CR_OK)
@@ -1620,12 +1648,14 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
     cr_status st = check_ce(xq, xs, qdata, srel, codebook, s_channel, bias, targets, M, V, K, dx, lse, dloss);
     if (st != CR_OK || M == 0)
         return st;
-    if (overlap(dx, 2 * M * K, xq, M * K))
-        return CR_ERR_INVALID_ARG;
     const CeBwdWork w(work, M, V, K);
     st = check_work(work, work_bytes, w.bytes);
     if (st != CR_OK)
         return st;
+    if (collide({{dx, 2 * M * K}, {work, w.bytes}},
+                {{xq, M * K}, {xs, 4 * M}, {qdata, V * K / 2}, {srel, V * K / 16}, {codebook, 64},
+                 {s_channel, 4 * V}, {bias, 4 * V}, {targets, 8 * M}, {lse, 4 * M}, {dloss, 4 * M}}))
+        return CR_ERR_INVALID_ARG;
     DeviceState *d = nullptr;
     st = current_device(&d);
     if (st != CR_OK)
