@@ -59,7 +59,9 @@ def _check_forward(xb, rb, gamma, gdt, MP, eps=EPS, qmax=127, alias=None):
                                     (2, 16384, 2), (2, 20480, 2), (1, 65536, 1), (33, 768, 33), (100, 256, 100),
                                     (40, 1280, 40), (17, 4096, 40), (24, 12288, 24), (17, 16384, 17), (20, 24576, 20),
                                     (17, 40960, 17), (300, 4096, 300), (17, 131072, 17), (17, 256, 27), (45, 512, 45),
-                                    (19, 1024, 30), (21, 768, 21), (18, 32768, 18)])
+                                    (19, 1024, 30), (21, 768, 21), (18, 32768, 18), (27, 1280, 34), (19, 1536, 19),
+                                    (40, 2560, 40), (20, 3328, 20), (30, 5120, 31), (20, 6912, 20), (18, 10240, 18),
+                                    (18, 13824, 18)])
 @pytest.mark.parametrize("gdt", [torch.bfloat16, torch.float32])
 def test_norm_quant_shapes(M, K, MP, gdt):
     """Every CTA size and holding depth of both forms, with a residual for
@@ -146,7 +148,8 @@ def _grad_inputs(M, K, seed, gdt, dres):
 @pytest.mark.parametrize("M,K", [(1, 256), (2, 512), (37, 1024), (100, 1280), (64, 2048), (450, 4096), (9, 4352),
                                  (200, 8192), (160, 12288), (5, 16384), (150, 16640), (3, 131072), (1500, 256),
                                  (1, 512), (9000, 256), (3001, 512), (77, 768), (400, 8448), (90, 32768), (60, 33024),
-                                 (170, 49152), (40, 65536), (200, 66048)])
+                                 (170, 49152), (40, 65536), (200, 66048), (1600, 1536), (450, 2560), (450, 2816),
+                                 (310, 5120), (150, 9728), (170, 10240)])
 @pytest.mark.parametrize("gdt,dres", [(torch.bfloat16, True), (torch.float32, False)])
 def test_norm_backward(M, K, gdt, dres):
     dr, h, gamma, rs, dd = _grad_inputs(M, K, 21, gdt, dres)

@@ -1065,7 +1065,7 @@ def cr_rmsnorm_quant_act(x, gamma, eps: float = 1e-6, residual=None, mp: Optiona
     elif h is not None and h is not x:
         raise ValueError("h is an output of the residual's addition: without a residual it is x")
     if xq is None:
-        xq = torch.empty((MP, K), dtype=torch.int8, device=x.device)
+        xq = torch.empty(MP, K, dtype=torch.int8, device=x.device)
     else:
         _want(xq, "xq", torch.int8, (MP, K))
     if xs is None:

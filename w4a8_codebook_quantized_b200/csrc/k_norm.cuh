@@ -350,8 +350,10 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_rows_kernel(const FwdArgs a)
 // arithmetic (each half rounded as the scalar instruction rounds it), as
 // rotquant_pairs_kernel: at these sizes the scalar form is bound by the
 // instructions it issues.
+// (Three CTAs of 384 threads an SM take 56 registers, two fewer than it has by
+// itself.)
 template <int J, bool kRecompute, int THREADS, bool GBF16>
-__global__ void __launch_bounds__(THREADS) rmsnorm_pairs_kernel(const FwdArgs a)
+__global__ void __launch_bounds__(THREADS, THREADS == 384 ? 3 : 0) rmsnorm_pairs_kernel(const FwdArgs a)
 {
     constexpr int kHalfWarps = THREADS / 16;
     extern __shared__ __align__(16) uint64_t nm_smem[];
@@ -496,20 +498,28 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_pairs_kernel(const FwdArgs a)
 
 // ---------------------------------------------------------------- forward, many short rows
 //
-// K <= 1024: G half-warps per row (1 for K <= 512, 2 above), a pair of blocks
-// each, eight half-warps a CTA.  A row is one warp's or half a warp's, so its
-// two reductions are shuffles and no CTA-wide barrier is left; with a CTA per
-// row, three quarters of its threads had no block at K = 256 (393216 rows: 765
-// us instead of 196).
+// K <= 1536: G half-warps per row (1 for K <= 512, 2 for K <= 1024, 3 above), a
+// pair of blocks each, eight half-warps a CTA (six for G = 3).  With G <= 2 a
+// row is one warp's or half a warp's, so its two reductions are shuffles and no
+// CTA-wide barrier is left.  With a CTA per row three quarters of its threads
+// had no block at K = 256 (393216 rows: 765 us instead of 184), and one in four
+// at K = 1536 (65536 rows: 146 us instead of 138).  Eight CTAs an SM asked for
+// (64 registers) take G = 1 from 196 to 184 us; G = 2 has 64 by itself and was
+// 2 % slower when asked.
+constexpr int small_half_warps(int G) { return G == 3 ? 6 : 8; }
+
 template <int G, bool GBF16>
-__global__ void __launch_bounds__(128) rmsnorm_small_kernel(const FwdArgs a, int64_t MP)
+__global__ void __launch_bounds__(16 * small_half_warps(G), G == 1 ? 8 : 0) rmsnorm_small_kernel(const FwdArgs a, int64_t MP)
 {
-    __shared__ __align__(16) uint64_t tr_all[8][256];
+    constexpr int kHalfWarps = small_half_warps(G);
+    __shared__ __align__(16) uint64_t tr_all[kHalfWarps][256];
+    __shared__ double hw_ss[kHalfWarps];  // G = 3: a row's shares
+    __shared__ float hw_max[kHalfWarps];
     asm volatile("griddepcontrol.launch_dependents;" :::);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, hw = tid >> 4, L = tid & 15;
-    const unsigned hmask = 0xFFFFu << (16 * (hw & 1)), rmask = G == 1 ? hmask : 0xFFFFFFFFu;
-    const int64_t m = (8 / G) * (int64_t)blockIdx.x + hw / G;
+    const unsigned hmask = 0xFFFFu << (16 * (hw & 1)), rmask = G == 2 ? 0xFFFFFFFFu : hmask;
+    const int64_t m = (kHalfWarps / G) * (int64_t)blockIdx.x + hw / G;
     const int p = hw % G;  // the half-warp's pair of blocks
     const int NB = (int)(a.K / 256);
     if (m >= MP)
@@ -542,8 +552,14 @@ __global__ void __launch_bounds__(128) rmsnorm_small_kernel(const FwdArgs a, int
     if (two)
         load_h(at + 256, w1);
 #pragma unroll
-    for (int o = 8 * G; o >= 1; o >>= 1)
+    for (int o = G == 2 ? 16 : 8; o >= 1; o >>= 1)
         ss += __shfl_xor_sync(rmask, ss, o);
+    if constexpr (G == 3) {  // (rows without work have left; the barriers wait for the others only)
+        if (L == 0)
+            hw_ss[hw] = ss;
+        __syncthreads();
+        ss = (hw_ss[hw - p] + hw_ss[hw - p + 1]) + hw_ss[hw - p + 2];
+    }
     const float rs = (float)rsqrt(fma(ss, a.inv_k, a.eps));
     const uint64_t rs2 = pair_both(rs);
     float g0[16], g1[16];
@@ -563,8 +579,14 @@ __global__ void __launch_bounds__(128) rmsnorm_small_kernel(const FwdArgs a, int
                             pack2(__float_as_uint(g0[2 * i + 1]), __float_as_uint(g1[2 * i + 1])));
     }
     rq::rotate_pair_regs(L, tr, hmask, v);
-    const uint32_t bits = __reduce_max_sync(rmask, __float_as_uint(rq::max_abs_pairs(v)));
-    const RowScale s(__uint_as_float(bits), a.qmax);
+    float rmax = __uint_as_float(__reduce_max_sync(rmask, __float_as_uint(rq::max_abs_pairs(v))));
+    if constexpr (G == 3) {
+        if (L == 0)
+            hw_max[hw] = rmax;
+        __syncthreads();
+        rmax = fmaxf(fmaxf(hw_max[hw - p], hw_max[hw - p + 1]), hw_max[hw - p + 2]);
+    }
+    const RowScale s(rmax, a.qmax);
     if (one)
         rq::quantise_store_pair(v, s.scale, s.inv16, a.qmax, s.exact_row, L, tb, hmask, a.xq + m * a.K + 512 * p,
                                 two ? a.xq + m * a.K + 512 * p + 256 : nullptr);
@@ -599,6 +621,8 @@ inline cudaError_t set_attributes()
         {rmsnorm_pairs_kernel<1, false, 1024, false>, rq::smem_bytes<1024>()},
         {rmsnorm_pairs_kernel<1, false, 512, true>, rq::smem_bytes<512>()},
         {rmsnorm_pairs_kernel<1, false, 512, false>, rq::smem_bytes<512>()},
+        {rmsnorm_pairs_kernel<1, false, 448, true>, rq::smem_bytes<448>()},
+        {rmsnorm_pairs_kernel<1, false, 448, false>, rq::smem_bytes<448>()},
         {rmsnorm_pairs_kernel<1, true, 512, true>, rq::smem_bytes<512>()},
         {rmsnorm_pairs_kernel<1, true, 512, false>, rq::smem_bytes<512>()},
         {rmsnorm_pairs_kernel<1, false, 384, true>, rq::smem_bytes<384>()},
@@ -617,31 +641,56 @@ inline cudaError_t launch_fwd_t(const FwdArgs &a, int64_t MP, cudaStream_t strea
 {
     if (MP <= rq::kShortRows)
         return a.K >= 8192 ? launch_fwd_rows<GBF16, 512>(a, MP, stream) : launch_fwd_rows<GBF16, 256>(a, MP, stream);
-    if (a.K <= 512)
-        return launch_dependent(rmsnorm_small_kernel<1, GBF16>, dim3((unsigned)((MP + 7) / 8)), 128, 0, stream, a, MP);
-    if (a.K <= 1024)
-        return launch_dependent(rmsnorm_small_kernel<2, GBF16>, dim3((unsigned)((MP + 3) / 4)), 128, 0, stream, a, MP);
+    auto several = [&](auto half_warps) {
+        constexpr int G = decltype(half_warps)::value, rows = small_half_warps(G) / G;
+        return launch_dependent(rmsnorm_small_kernel<G, GBF16>, dim3((unsigned)((MP + rows - 1) / rows)),
+                                16 * small_half_warps(G), 0, stream, a, MP);
+    };
+    auto in_one = [&](auto threads) {  // a half-warp per pair of blocks
+        constexpr int T = decltype(threads)::value;
+        return launch_dependent(rmsnorm_pairs_kernel<1, false, T, GBF16>, dim3((unsigned)MP), T, rq::smem_bytes<T>(),
+                                stream, a);
+    };
     const int64_t pairs = (a.K / 256 + 1) / 2;
+    if (pairs == 1)
+        return several(std::integral_constant<int, 1>{});
+    if (pairs == 2)
+        return several(std::integral_constant<int, 2>{});
+    if (pairs == 3)
+        return several(std::integral_constant<int, 3>{});
     if (pairs <= 4)
-        return launch_dependent(rmsnorm_pairs_kernel<1, false, 64, GBF16>, dim3((unsigned)(MP)), 64, rq::smem_bytes<64>(), stream, a);
+        return in_one(std::integral_constant<int, 64>{});
+    if (pairs <= 6)
+        return in_one(std::integral_constant<int, 96>{});
     if (pairs <= 8)
-        return launch_dependent(rmsnorm_pairs_kernel<1, false, 128, GBF16>, dim3((unsigned)(MP)), 128, rq::smem_bytes<128>(), stream, a);
+        return in_one(std::integral_constant<int, 128>{});
+    if (pairs <= 10)
+        return in_one(std::integral_constant<int, 160>{});
+    if (pairs <= 12)
+        return in_one(std::integral_constant<int, 192>{});
+    if (pairs <= 14)
+        return in_one(std::integral_constant<int, 224>{});
     if (pairs <= 16)
-        return launch_dependent(rmsnorm_pairs_kernel<1, false, 256, GBF16>, dim3((unsigned)(MP)), 256, rq::smem_bytes<256>(), stream, a);
+        return in_one(std::integral_constant<int, 256>{});
+    if (pairs <= 20)
+        return in_one(std::integral_constant<int, 320>{});
     if (pairs <= 24)
-        return launch_dependent(rmsnorm_pairs_kernel<1, false, 384, GBF16>, dim3((unsigned)(MP)), 384, rq::smem_bytes<384>(), stream, a);
+        return in_one(std::integral_constant<int, 384>{});
+    if (pairs <= 28)
+        return in_one(std::integral_constant<int, 448>{});
     if (pairs <= 32)
-        return launch_dependent(rmsnorm_pairs_kernel<1, false, 512, GBF16>, dim3((unsigned)(MP)), 512, rq::smem_bytes<512>(), stream, a);
+        return in_one(std::integral_constant<int, 512>{});
     if (pairs <= 64)
-        return launch_dependent(rmsnorm_pairs_kernel<1, false, 1024, GBF16>, dim3((unsigned)(MP)), 1024,
-                                rq::smem_bytes<1024>(), stream, a);
+        return in_one(std::integral_constant<int, 1024>{});
     return launch_dependent(rmsnorm_pairs_kernel<1, true, 512, GBF16>, dim3((unsigned)(MP)), 512, rq::smem_bytes<512>(), stream, a);
 }
 
 // Short batches take the scalar form, 512 threads for K >= 8192 and 256 below;
-// longer ones the packed form: several rows a CTA up to K = 1024, then one
+// longer ones the packed form: several rows a CTA up to K = 1536, then one
 // half-warp per block pair while that fits a CTA (K <= 32768), and the
-// re-reading form beyond.
+// re-reading form beyond.  At 64 registers an SM holds 1024 threads, so a CTA
+// has as few as the row's pairs take (19660 x 5120: 148 us with 256 threads,
+// 122 with 160; 9144 x 11008: 164 us with two CTAs of 384, 139 with three).
 inline cudaError_t launch_fwd(FwdArgs a, int64_t MP, bool gamma_bf16, cudaStream_t stream)
 {
     a.inv_k = 1.0 / (double)a.K;
@@ -936,8 +985,8 @@ __global__ void __launch_bounds__(128) rmsnorm_backward_small_kernel(const BwdAr
 // of its blocks (at most one per half-warp) and of dgamma's partial row; the
 // row's sum goes round by shared memory, one cluster barrier a row (the slots
 // alternate).  A CTA per row would have to rotate every block twice (16640
-// columns, 6049 rows: 463 us against 297).  For 8192 < K <= 16384 two blocks a
-// half-warp, some of them spilled, are still faster (8448: 258 us against 330).
+// columns, 6049 rows: 463 us against 297).  For 10240 < K <= 16384 two blocks a
+// half-warp, some of them spilled, are still faster (12288: 207 us against 258).
 template <bool GBF16>
 __global__ void __launch_bounds__(256) rmsnorm_backward_cluster_kernel(const BwdArgs a, int ctas)
 {
@@ -999,10 +1048,14 @@ __global__ void __launch_bounds__(256) rmsnorm_backward_cluster_kernel(const Bwd
 
 // One CTA per row at a time, J blocks per half-warp (512 < K <= 16384); with one
 // block the next row's values are loaded while the current row is worked on.
+// J = 1 up to 10240 columns, with as few warps as the row takes (39321 x 2560:
+// 170 us with 256 threads, 140 with 160; 9728 columns: 238 us with two blocks a
+// half-warp, 182 with one in 640 threads); one block in 704 threads, which leave
+// 80 registers, was slower than two (11008: 232 us against 223).
 // (Written out, not with BwdBlock: the compiler kept the struct form's registers
 // in another order, and 8192 x 4096 took 57 us instead of 51.)
 template <int J, int THREADS, bool GBF16>
-__global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(const BwdArgs a)
+__global__ void __launch_bounds__(THREADS, THREADS == 320 ? 2 : 0) rmsnorm_backward_kernel(const BwdArgs a)
 {
     constexpr int kHalfWarps = THREADS / 16;
     __shared__ __align__(16) float tr_all[kHalfWarps][16 * 16 + 16];
@@ -1208,17 +1261,23 @@ inline int cluster_ctas(int64_t K) { return (int)((K + 4095) / 4096); }
 
 // Row groups of the backward's grid (CTAs, or clusters), and with it the
 // partial rows of dgamma: a function of the shape alone, so that the caller's
-// workspace has a fixed size.  A cluster's CTAs share a GPC; eight GPCs of at
-// least 16 SMs are counted on, so that every cluster is resident from the start
-// (with two more than fit, 16384 took twice the time).
+// workspace has a fixed size.  All groups are resident from the start: 16 warps
+// an SM at up to 128 registers, 20 at up to 96 (the registers are dealt out by
+// quarters of an SM; one CTA of 96 threads too many, and 65536 x 1536 took 184
+// us instead of 137).  A cluster's CTAs share a GPC; eight GPCs of at least 16
+// SMs are counted on (with two clusters more than fit, 16384 took twice the
+// time).
 inline int64_t backward_groups(int64_t M, int64_t K)
 {
-    const int64_t most = K <= 512     ? 148 * 4
-                         : K <= 1024  ? 148 * 8
-                         : K <= 2048  ? 148 * 4
-                         : K <= 4096  ? 148 * 2
-                         : K > 16384 && K <= 32768 ? 32 / cluster_ctas(K) * 8
-                                                   : 148;
+    const int64_t nb = K / 256;
+    const int64_t most = nb <= 2    ? 148 * 4
+                         : nb <= 4  ? 148 * 8
+                         : nb <= 6  ? 148 * 5
+                         : nb <= 8  ? 148 * 4
+                         : nb <= 12 ? 148 * 3
+                         : nb <= 20 ? 148 * 2
+                         : nb > 64 && nb <= 128 ? 32 / cluster_ctas(K) * 8
+                                                : 148;
     const int64_t rows = K == 256 ? 8 : K == 512 ? 4 : 1;  // a group's rows at once
     const int64_t need = (M + rows - 1) / rows;
     return need < most ? need : most;
@@ -1250,22 +1309,37 @@ inline cudaError_t launch_bwd_t(const BwdArgs &a, float *dgamma, cudaStream_t st
 {
     const int64_t P = backward_groups(a.M, a.K);
     const dim3 grid((unsigned)P);
+    auto in_one = [&](auto threads) {  // a half-warp per block
+        constexpr int T = decltype(threads)::value;
+        return launch_dependent(rmsnorm_backward_kernel<1, T, GBF16>, grid, T, 0, stream, a);
+    };
     cudaError_t e;
-    if (a.K == 256)
+    const int64_t nb = a.K / 256;
+    if (nb == 1)
         e = launch_dependent(rmsnorm_backward_small_kernel<1, GBF16>, grid, 128, 0, stream, a);
-    else if (a.K == 512)
+    else if (nb == 2)
         e = launch_dependent(rmsnorm_backward_small_kernel<2, GBF16>, grid, 128, 0, stream, a);
-    else if (a.K <= 1024)
-        e = launch_dependent(rmsnorm_backward_kernel<1, 64, GBF16>, grid, 64, 0, stream, a);
-    else if (a.K <= 2048)
-        e = launch_dependent(rmsnorm_backward_kernel<1, 128, GBF16>, grid, 128, 0, stream, a);
-    else if (a.K <= 4096)
-        e = launch_dependent(rmsnorm_backward_kernel<1, 256, GBF16>, grid, 256, 0, stream, a);
-    else if (a.K <= 8192)
-        e = launch_dependent(rmsnorm_backward_kernel<1, 512, GBF16>, grid, 512, 0, stream, a);
-    else if (a.K <= 16384)
+    else if (nb <= 4)
+        e = in_one(std::integral_constant<int, 64>{});
+    else if (nb <= 6)
+        e = in_one(std::integral_constant<int, 96>{});
+    else if (nb <= 8)
+        e = in_one(std::integral_constant<int, 128>{});
+    else if (nb <= 10)
+        e = in_one(std::integral_constant<int, 160>{});
+    else if (nb <= 12)
+        e = in_one(std::integral_constant<int, 192>{});
+    else if (nb <= 16)
+        e = in_one(std::integral_constant<int, 256>{});
+    else if (nb <= 20)
+        e = in_one(std::integral_constant<int, 320>{});
+    else if (nb <= 32)
+        e = in_one(std::integral_constant<int, 512>{});
+    else if (nb <= 40)
+        e = in_one(std::integral_constant<int, 640>{});
+    else if (nb <= 64)
         e = launch_dependent(rmsnorm_backward_kernel<2, 512, GBF16>, grid, 512, 0, stream, a);
-    else if (a.K <= 32768)
+    else if (nb <= 128)
         e = launch_clusters(rmsnorm_backward_cluster_kernel<GBF16>, P, cluster_ctas(a.K), 256, stream, a,
                             cluster_ctas(a.K));
     else
