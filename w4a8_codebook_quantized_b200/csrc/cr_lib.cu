@@ -499,7 +499,7 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
                                                         : pair_tiles >= d.num_sms / 2;
     const int64_t tn = gm::has_exponentials(MODE) && e.narrow ? 128 : gm::BN;
     CUtensorMap ta, tb;
-    if (!map(&ta, A, M, (uint32_t)gm::BM) ||
+    if (!map(&ta, A, M, (uint32_t)(use_pair ? gm::BM : gm::a_box_rows(M))) ||
         !(gm::b_is_kn(MODE) ? make_tmap_bf16(&tb, B, (uint64_t)N, (uint64_t)(e.b_rows ? e.b_rows : K), 64u, 64u)
                             : map(&tb, B, N, use_pair ? 128u : (uint32_t)tn)))
         return CR_ERR_CUDA;

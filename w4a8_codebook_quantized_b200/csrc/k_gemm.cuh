@@ -222,6 +222,11 @@ constexpr size_t smem_bytes()
 
 static_assert(BN == kSlotCols, "tile width of Tiling");
 
+// Rows of the boxes that bring A to a 128-row tile: 128, or where A has fewer
+// rows no more than those (the tile's other rows hold whatever was there; they
+// belong to no row of the output).
+__host__ __device__ constexpr int a_box_rows(int64_t M) { return M < BM ? (int)(M + 7) / 8 * 8 : BM; }
+
 __device__ __forceinline__ void tile_coords(int tile, int tiles_n, int &tm, int &tn)
 {
     tm = tile / tiles_n;
@@ -895,6 +900,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             uint32_t phase = 0;
             uint32_t issued = 0;  // stages filled so far
             bool ok = true;
+            const uint32_t stage_bytes = (uint32_t)(Sh::kStageBytes - kABytes + a_box_rows(max_rows) * BK);
             for (int tile = blockIdx.x; ok && tile < num_tiles; tile += gridDim.x) {
                 int tm, tn, k0, k1, copy;
                 if (!coords(tile, tm, tn, k0, k1, copy))
@@ -904,7 +910,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&sh.full[stage], Sh::kStageBytes);
+                    mbar_arrive_expect_tx(&sh.full[stage], stage_bytes);
                     tma_load_2d(sh.stage[stage], &tmA, kb * BKE, tm * BM, &sh.full[stage]);
                     if constexpr (b_is_kn(MODE)) {
 #pragma unroll
