@@ -121,7 +121,8 @@ def _targets(M, V, seed, ignored=True):
 
 
 CE_SHAPES = [(1, 1, 256, False), (1, 300, 512, True), (3, 4097, 256, False), (8, 2048, 768, True), (9, 257, 256, False),
-             (100, 255, 512, True), (129, 1000, 256, False), (300, 10007, 256, True), (513, 5000, 1024, False)]
+             (100, 255, 512, True), (129, 1000, 256, False), (300, 10007, 256, True), (513, 5000, 1024, False),
+             (9, 1, 2048, False), (12, 3001, 2048, True), (16, 1500, 2304, False), (17, 400, 2048, True)]
 
 
 @pytest.mark.parametrize("M,V,K,bias", CE_SHAPES)

@@ -499,7 +499,7 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
                                                         : pair_tiles >= d.num_sms / 2;
     const int64_t tn = gm::has_exponentials(MODE) && e.narrow ? 128 : gm::BN;
     CUtensorMap ta, tb;
-    if (!map(&ta, A, M, (uint32_t)(use_pair ? gm::BM : gm::a_box_rows(M))) ||
+    if (!map(&ta, A, M, (uint32_t)gm::a_box_rows(M)) ||
         !(gm::b_is_kn(MODE) ? make_tmap_bf16(&tb, B, (uint64_t)N, (uint64_t)(e.b_rows ? e.b_rows : K), 64u, 64u)
                             : map(&tb, B, N, use_pair ? 128u : (uint32_t)tn)))
         return CR_ERR_CUDA;
@@ -1410,6 +1410,15 @@ int64_t ce_piece(int64_t V, int64_t per_entry)
     return round_up((V + n - 1) / n, cr::gm::BN);
 }
 
+// Whether the decode GEMV makes the outputs: up to 8 rows, and up to twice that
+// in two passes over the packed codes for K >= 2048 (16 rows, decode and GEMM
+// against two passes: 131072 x 4096 218 -> 147 us, 50021 x 2048 51 -> 39 us,
+// 32768 x 2048 29.6 -> 29.1; 32768 x 1024 20.0 -> 23.5, so not there).
+bool ce_by_gemv(int64_t M, int64_t K)
+{
+    return M <= CR_GEMV_MAX_M || (M <= 2 * CR_GEMV_MAX_M && K >= 2048);
+}
+
 struct CeFwdWork {
     int64_t rows, piece, slices;
     bool narrow = false;  // of every launch, so that the slices have one width
@@ -1423,7 +1432,7 @@ struct CeFwdWork {
         Parts p(work);
         rows = M < kFwdRows ? M : kFwdRows;
         piece = ce_piece(V, K);
-        if (M <= CR_GEMV_MAX_M) {
+        if (ce_by_gemv(M, K)) {
             slices = 0;
             y = static_cast<float *>(p.take(4 * M * V));
         } else {
@@ -1594,10 +1603,12 @@ cr_status cr_w4a8_cross_entropy(const int8_t *xq, const float *xs, const uint8_t
     if (st != CR_OK)
         return st;
     using namespace cr;
-    if (M <= CR_GEMV_MAX_M) {
+    if (ce_by_gemv(M, K)) {
         // a decode batch: the GEMV streams the packed codes; its outputs are small
-        st = run_gemv(d->num_sms, d->gemv_attr_set, xq, xs, qdata, srel, codebook, s_channel, bias, M, V, K,
-                      CR_OUT_F32, w.y, nullptr, stream, /*pdl=*/true, 0, &d->gemv32_attr_set);
+        for (int64_t m0 = 0; st == CR_OK && m0 < M; m0 += CR_GEMV_MAX_M)
+            st = run_gemv(d->num_sms, d->gemv_attr_set, xq + m0 * K, xs + m0, qdata, srel, codebook, s_channel, bias,
+                          M - m0 < CR_GEMV_MAX_M ? M - m0 : CR_GEMV_MAX_M, V, K, CR_OUT_F32, w.y + m0 * V, nullptr,
+                          stream, /*pdl=*/true, 0, &d->gemv32_attr_set);
         if (st == CR_OK)
             st = launched(ce::launch_row_loss(w.y, M, V, targets, ignore_index, loss, lse, stream));
         return st;

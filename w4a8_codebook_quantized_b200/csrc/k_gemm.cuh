@@ -224,7 +224,9 @@ static_assert(BN == kSlotCols, "tile width of Tiling");
 
 // Rows of the boxes that bring A to a 128-row tile: 128, or where A has fewer
 // rows no more than those (the tile's other rows hold whatever was there; they
-// belong to no row of the output).
+// belong to no row of the output).  Rows that a box fills past the tensor's end
+// are not free: with boxes of 128 rows 9 x 32768 x 4096 takes 36.9 us instead of
+// 29.5, 32 rows the same.
 __host__ __device__ constexpr int a_box_rows(int64_t M) { return M < BM ? (int)(M + 7) / 8 * 8 : BM; }
 
 __device__ __forceinline__ void tile_coords(int tile, int tiles_n, int &tm, int &tn)
@@ -1170,6 +1172,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             prefetch_tmap(&tmA);
             prefetch_tmap(&tmB);
             const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0);  // the leader's
+            const uint32_t pair_bytes = 2u * (uint32_t)(pair::kHalfBytes + a_box_rows(max_rows) * BK);
             int stage = 0;
             uint32_t phase = 0;
             uint32_t issued = 0;  // stages filled so far
@@ -1185,7 +1188,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                     }
                     const uint32_t full_leader = full0 + 8u * (uint32_t)stage;
                     if (leader)
-                        mbar_arrive_expect_tx(&sh.full[stage], 2 * pair::kStageBytes);
+                        mbar_arrive_expect_tx(&sh.full[stage], pair_bytes);
                     tma_load_2d_pair(sh.stage[stage], &tmA, kb * BKE, tm * 256 + (int)rank * 128, full_leader);
                     if constexpr (b_is_kn(MODE)) {
 #pragma unroll
