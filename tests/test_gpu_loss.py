@@ -49,7 +49,7 @@ def _work(name, *shape):
 @pytest.mark.parametrize("M,N,K,bias", [(1, 8, 256, False), (1, 264, 512, True), (8, 520, 256, False),
                                         (37, 1000, 768, True), (128, 256, 256, False), (129, 2824, 1280, True),
                                         (257, 512, 1024, False), (700, 6400, 256, True), (2500, 512, 1024, False),
-                                        (3900, 3200, 1280, False)])
+                                        (3900, 3200, 1280, False), (1, 4096, 512, False), (9, 2824, 768, True)])
 def test_swiglu_backward(M, N, K, bias):
     """One row to several tiles, ragged rows and columns (N / 2 a multiple of
     4 only), both GEMM forms; the reduction split for few tiles, and for the

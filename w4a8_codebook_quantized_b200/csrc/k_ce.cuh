@@ -215,8 +215,9 @@ __global__ void __launch_bounds__(kThreads) split_sum_kernel(const SumArgs a)
     const gm::Tiling t(M, a.K, a.kblocks, a.bm, a.slots, a.max_splits, a.split_tail);
     constexpr int kTileQuads = gm::kSlotCols / 4;  // float4s of a copy's row
     const int per_row = a.K / 4;
+    const int tile_rows = min(a.bm, M);  // fewer than bm only where all tiles have as many
     const int64_t n4 = a.acc != nullptr ? (int64_t)M * per_row
-                                        : (int64_t)(t.units - t.full) / t.splits * a.bm * kTileQuads;
+                                        : (int64_t)(t.units - t.full) / t.splits * tile_rows * kTileQuads;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n4; i += (int64_t)gridDim.x * kThreads) {
         int m, k, tile;
         if (a.acc != nullptr) {
@@ -226,9 +227,9 @@ __global__ void __launch_bounds__(kThreads) split_sum_kernel(const SumArgs a)
         } else {
             int tm, tn;
             const int r = (int)(i / kTileQuads);  // row among the split tiles' rows
-            tile = t.full + r / a.bm;
+            tile = t.full + r / tile_rows;
             gm::tile_place(tile, t.tiles_m, t.tiles_n, tm, tn);
-            m = tm * a.bm + r % a.bm;
+            m = tm * a.bm + r % tile_rows;
             k = tn * gm::kSlotCols + 4 * (int)(i % kTileQuads);
             if (m >= M)
                 continue;
