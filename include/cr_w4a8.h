@@ -655,16 +655,15 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
  *   loss[m] = lse[m] - y[m, targets[m]];  0 where targets[m] == ignore_index;
  *             NaN where the target is any other value outside 0 .. V - 1
  * A bias of -inf takes an entry out of the softmax.  V >= 1 (CR_ERR_INVALID_ARG
- * otherwise), any V.  M <= 8 takes the decode GEMV, M <= 16 with K >= 2048 two
- * passes of it.
+ * otherwise), any V.  M <= 8 takes the decode GEMV.
  *
  * xq [>= M, K] int8, xs [>= M] fp32, the layer as in (3); targets [M] int64.
  * loss [M], lse [M] fp32, written.  work: at least
  * cr_w4a8_cross_entropy_work_bytes(M, V, K) bytes, 16-byte aligned
  * (CR_ERR_INVALID_ARG when smaller): a decoded piece of the weight (64 MB or
  * 256 K bytes, whichever is more) and 8 bytes per row (of at most 32768 at a
- * time) and 256 outputs, 128 for short problems; with the decode GEMV the
- * M V fp32 outputs themselves.  Nothing is allocated.  Results are the same from run to
+ * time) and 256 outputs, 128 for short problems; with the decode GEMV (up to 8
+ * rows, up to 16 of some layers) the M V fp32 outputs themselves.  Nothing is allocated.  Results are the same from run to
  * run; between batch sizes the sums' order, and so the last bits, may differ.
  *
  * (23b) Its gradient with respect to the layer's rotated input:

@@ -183,6 +183,24 @@ __device__ __forceinline__ uint32_t to_bf16x2_bits(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
+// Sixteen decoded weights (four words of int8) times their channel's scale,
+// as bf16, to a 32-byte aligned place.  int8 -> fp32 through the low mantissa
+// byte of 2^23.
+__device__ __forceinline__ void store_bf16_weights(uint16_t *w, const uint32_t (&o)[4], float sc)
+{
+    uint32_t b[8];
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+        const uint32_t x = o[j >> 2] ^ 0x80808080u;
+        const float f0 = __fsub_rn(__uint_as_float(prmt(x, 0x4B000000u, 0x7650u | (uint32_t)(j & 3))), 8388736.0f);
+        const float f1 = __fsub_rn(__uint_as_float(prmt(x, 0x4B000000u, 0x7650u | (uint32_t)((j + 1) & 3))), 8388736.0f);
+        b[j >> 1] = to_bf16x2_bits(__fmul_rn(f0, sc), __fmul_rn(f1, sc));
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(w), "r"(b[0]), "r"(b[1]), "r"(b[2]),
+                 "r"(b[3]), "r"(b[4]), "r"(b[5]), "r"(b[6]), "r"(b[7])
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- fp32 pairs in 64-bit registers
 
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi)

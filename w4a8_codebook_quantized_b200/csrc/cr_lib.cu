@@ -21,6 +21,7 @@
 #include "k_ce.cuh"
 #include "k_elementwise.cuh"
 #include "k_gemm.cuh"
+#include "k_gemm_decode.cuh"
 #include "k_gemv.cuh"
 #include "k_norm.cuh"
 #include "k_peak.cuh"
@@ -41,6 +42,7 @@ struct DeviceState {
     std::atomic<bool> gemm_attr_set[cr::gm::kModes] = {};  // by gm::Mode
     std::atomic<bool> gemm_pair_attr_set[cr::gm::kModes] = {};
     std::atomic<bool> gemm_narrow_attr_set[cr::gm::kModes] = {};
+    std::atomic<bool> gemm_decode_attr_set[cr::gm::kModes] = {};
     std::atomic<bool> gemv_attr_set{false};
     std::atomic<bool> gemv_split_attr_set{false};
     std::atomic<bool> gemv32_attr_set{false};
@@ -549,6 +551,54 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
             return launch_single(gm::gemm_kernel<MODE, 128>, d.gemm_narrow_attr_set[MODE], gm::smem_bytes<MODE, 128>());
     }
     return launch_single(gm::gemm_kernel<MODE>, d.gemm_attr_set[MODE], gm::smem_bytes<MODE, gm::BN>());
+}
+
+// The same for up to 128 rows on a packed weight (k_gemm_decode.cuh); w: the
+// bf16 weight to write, for a gradient.
+template <int MODE>
+cr_status launch_gemm_decode(DeviceState &d, const int8_t *xq, const uint8_t *qdata, const uint8_t *srel,
+                             const float *codebook, const CUtensorMap *to, int64_t M, int64_t N, int64_t K,
+                             const GemmEpilogue &e, uint16_t *w, cudaStream_t stream)
+{
+    using namespace cr;
+    auto packed = [&](CUtensorMap *m, const uint8_t *base, int64_t row_bytes, uint32_t box_bytes) {
+        const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)N};
+        const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+        const cuuint32_t box[2] = {box_bytes, (cuuint32_t)gd::TN};
+        const cuuint32_t estr[2] = {1u, 1u};
+        return g_encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    CUtensorMap ta, tq, ts;
+    if (!make_tmap_i8(&ta, xq, (uint64_t)K, (uint64_t)M, (uint32_t)gm::a_box_rows(M)) || !packed(&tq, qdata, K / 2, 64u) ||
+        !packed(&ts, srel, K / 16, 16u))
+        return CR_ERR_CUDA;
+    if (!d.gemm_decode_attr_set[MODE]) {
+        if (cudaFuncSetAttribute((const void *)gd::gemm_decode_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)gd::smem_bytes<MODE>()) != cudaSuccess) {
+            cudaGetLastError();
+            return CR_ERR_CUDA;
+        }
+        d.gemm_decode_attr_set[MODE] = true;
+    }
+    const int64_t tiles = (N + gd::TN - 1) / gd::TN;
+    return launched(launch_dependent(gd::gemm_decode_kernel<MODE>, dim3((unsigned)(tiles < d.num_sms ? tiles : d.num_sms)),
+                                     gd::kThreads, (int)gd::smem_bytes<MODE>(), stream, ta, tq, ts, to ? *to : ta,
+                                     codebook, e.xs, e.ws, e.bias, (int)M, (int)N, (int)K, w, e.ex));
+}
+
+// Whether an int8 contraction on a packed weight decodes it on the way: for one
+// tile of rows, where there are tiles of columns for close to half of the SMs or
+// a short reduction (a CTA decodes its columns alone).  Weight decoded first
+// against on the way, 64 rows: cross entropy 32768 x 4096 56 -> 36 us, 10007 x
+// 1024 12.7 -> 9.9, 2000 x 1024 10.2 -> 9.2, but 3000 x 8192 24.6 -> 28.2; its
+// gradient 32768 x 4096 178 -> 130, 10007 x 1024 29.7 -> 28.2, but 2000 x 1024
+// 21.1 -> 23.3; gated gradient 12288 x 4096 74 -> 62, 128 x 256 12.6 -> 11.3, but
+// 2048 x 8192 41 -> 80.
+bool decode_on_the_way(int64_t M, int64_t N, int64_t K, bool gradient)
+{
+    return M <= 128 && (N > 63 * 128 || K <= (gradient ? 512 : 1024));
 }
 
 // Whether an int8 contraction whose epilogue has exponentials runs on 128 x
@@ -1411,12 +1461,12 @@ int64_t ce_piece(int64_t V, int64_t per_entry)
 }
 
 // Whether the decode GEMV makes the outputs: up to 8 rows, and up to twice that
-// in two passes over the packed codes for K >= 2048 (16 rows, decode and GEMM
-// against two passes: 131072 x 4096 218 -> 147 us, 50021 x 2048 51 -> 39 us,
-// 32768 x 2048 29.6 -> 29.1; 32768 x 1024 20.0 -> 23.5, so not there).
-bool ce_by_gemv(int64_t M, int64_t K)
+// in two passes over the packed codes where the reduction is long and the
+// contraction does not decode on the way (16 rows, 3000 x 8192: 17.1 us
+// against 24.4 with the weight decoded first).
+bool ce_by_gemv(int64_t M, int64_t V, int64_t K)
 {
-    return M <= CR_GEMV_MAX_M || (M <= 2 * CR_GEMV_MAX_M && K >= 2048);
+    return M <= CR_GEMV_MAX_M || (M <= 2 * CR_GEMV_MAX_M && K >= 2048 && !decode_on_the_way(M, V, K, false));
 }
 
 struct CeFwdWork {
@@ -1432,13 +1482,17 @@ struct CeFwdWork {
         Parts p(work);
         rows = M < kFwdRows ? M : kFwdRows;
         piece = ce_piece(V, K);
-        if (ce_by_gemv(M, K)) {
+        if (ce_by_gemv(M, V, K)) {
             slices = 0;
             y = static_cast<float *>(p.take(4 * M * V));
         } else {
-            narrow = narrow_tiles(rows, piece < V ? piece : V, K);
+            const bool packed = decode_on_the_way(M, V, K, false);
+            narrow = packed || narrow_tiles(rows, piece < V ? piece : V, K);
             slices = (V + (narrow ? 127 : 255)) / (narrow ? 128 : 256);
-            w8 = static_cast<int8_t *>(p.take((piece < V ? piece : V) * K));
+            if (packed)
+                piece = V;
+            else
+                w8 = static_cast<int8_t *>(p.take((piece < V ? piece : V) * K));
             part = static_cast<float2 *>(p.take(8 * slices * rows));
             tlogit = static_cast<float *>(p.take(4 * rows));
         }
@@ -1556,16 +1610,20 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
     if (!make_tmap_out(&tz, dz, M, N, false, /*half=*/true) || !make_tmap_out(&tx, dx, M, K, false) ||
         (w.plan.copies && !make_tmap_out(&tc, w.copies, w.plan.copies * w.plan.bm, gm::BN, true)))
         return CR_ERR_CUDA;
-    st = launched(ew::launch_decode_both(qdata, srel, codebook, s_channel, N, K, w.w8, w.w, d->num_sms, stream));
-    if (st != CR_OK)
-        return st;
     GemmEpilogue e;
     e.xs = xs;
     e.ws = s_channel;
     e.bias = bias;
     e.ex.dout = dout;
-    e.narrow = narrow_tiles(M, N, K);
-    st = launch_gemm<gm::kSwigluGrad>(*d, xq, w.w8, &tz, M, N, K, e, stream);
+    if (decode_on_the_way(M, N, K, true)) {
+        st = launch_gemm_decode<gm::kSwigluGrad>(*d, xq, qdata, srel, codebook, &tz, M, N, K, e, w.w, stream);
+    } else {
+        st = launched(ew::launch_decode_both(qdata, srel, codebook, s_channel, N, K, w.w8, w.w, d->num_sms, stream));
+        if (st != CR_OK)
+            return st;
+        e.narrow = narrow_tiles(M, N, K);
+        st = launch_gemm<gm::kSwigluGrad>(*d, xq, w.w8, &tz, M, N, K, e, stream);
+    }
     if (st != CR_OK)
         return st;
     GemmEpilogue g;
@@ -1603,7 +1661,7 @@ cr_status cr_w4a8_cross_entropy(const int8_t *xq, const float *xs, const uint8_t
     if (st != CR_OK)
         return st;
     using namespace cr;
-    if (ce_by_gemv(M, K)) {
+    if (ce_by_gemv(M, V, K)) {
         // a decode batch: the GEMV streams the packed codes; its outputs are small
         for (int64_t m0 = 0; st == CR_OK && m0 < M; m0 += CR_GEMV_MAX_M)
             st = run_gemv(d->num_sms, d->gemv_attr_set, xq + m0 * K, xs + m0, qdata, srel, codebook, s_channel, bias,
@@ -1617,8 +1675,9 @@ cr_status cr_w4a8_cross_entropy(const int8_t *xq, const float *xs, const uint8_t
         const int64_t rows = M - m0 < w.rows ? M - m0 : w.rows;
         for (int64_t n0 = 0; n0 < V; n0 += w.piece) {
             const int64_t n = V - n0 < w.piece ? V - n0 : w.piece;
-            st = launched(ew::launch_decode(qdata + n0 * (K / 2), srel + n0 * (K / 16), codebook, n, K, w.w8,
-                                            d->num_sms, stream));
+            if (w.w8)
+                st = launched(ew::launch_decode(qdata + n0 * (K / 2), srel + n0 * (K / 16), codebook, n, K, w.w8,
+                                                d->num_sms, stream));
             if (st != CR_OK)
                 return st;
             GemmEpilogue e;
@@ -1633,7 +1692,9 @@ cr_status cr_w4a8_cross_entropy(const int8_t *xq, const float *xs, const uint8_t
             e.ex.slices = (int)w.slices;
             e.narrow = w.narrow;
             e.ex.tlogit = w.tlogit;
-            st = launch_gemm<gm::kCeStats>(*d, xq + m0 * K, w.w8, nullptr, rows, n, K, e, stream);
+            st = w.w8 ? launch_gemm<gm::kCeStats>(*d, xq + m0 * K, w.w8, nullptr, rows, n, K, e, stream)
+                      : launch_gemm_decode<gm::kCeStats>(*d, xq, qdata, srel, codebook, nullptr, rows, n, K, e, nullptr,
+                                                         stream);
             if (st != CR_OK)
                 return st;
         }
@@ -1705,7 +1766,9 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
         for (int64_t n0 = 0; n0 < V; n0 += w.piece) {
             const int64_t n = V - n0 < w.piece ? V - n0 : w.piece, np = round_up(n, 8);
             const uint8_t *q = qdata + n0 * (K / 2), *s = srel + n0 * (K / 16);
-            st = launched(ew::launch_decode_both(q, s, codebook, s_channel + n0, n, K, w.w8, w.w, d->num_sms, stream));
+            const bool packed = decode_on_the_way(M, n, K, true);
+            if (!packed)
+                st = launched(ew::launch_decode_both(q, s, codebook, s_channel + n0, n, K, w.w8, w.w, d->num_sms, stream));
             if (st != CR_OK)
                 return st;
             // dl [rows, np]: the gradient of the piece's outputs
@@ -1719,7 +1782,8 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
             e.ex = ex;
             e.ex.n0 = (int)n0;
             e.narrow = narrow_tiles(rows, n, K);
-            st = launch_gemm<gm::kCeGrad>(*d, bxq, w.w8, &tl, rows, n, K, e, stream);
+            st = packed ? launch_gemm_decode<gm::kCeGrad>(*d, bxq, q, s, codebook, &tl, rows, n, K, e, w.w, stream)
+                        : launch_gemm<gm::kCeGrad>(*d, bxq, w.w8, &tl, rows, n, K, e, stream);
             if (st != CR_OK)
                 return st;
             GemmEpilogue g;

@@ -332,21 +332,7 @@ __global__ void __launch_bounds__(kThreads) decode_both_kernel(const uint8_t *__
                 decode8(c[u].x, T, o[0], o[1]);
                 decode8(c[u].y, T, o[2], o[3]);
                 *reinterpret_cast<uint4 *>(w8 + 16 * i) = make_uint4(o[0], o[1], o[2], o[3]);
-                // int8 -> fp32 through the low mantissa byte of 2^23, as in dequant_t_bf16_kernel
-                const float sc = __bfloat162float(__float2bfloat16_rn(sch[u]));
-                uint32_t b[8];
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const uint32_t x = o[j >> 2] ^ 0x80808080u;
-                    const float f0 = __fsub_rn(
-                        __uint_as_float(prmt(x, 0x4B000000u, 0x7650u | (uint32_t)(j & 3))), 8388736.0f);
-                    const float f1 = __fsub_rn(
-                        __uint_as_float(prmt(x, 0x4B000000u, 0x7650u | (uint32_t)((j + 1) & 3))), 8388736.0f);
-                    b[j >> 1] = to_bf16x2_bits(__fmul_rn(f0, sc), __fmul_rn(f1, sc));
-                }
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(w + 16 * i), "r"(b[0]),
-                             "r"(b[1]), "r"(b[2]), "r"(b[3]), "r"(b[4]), "r"(b[5]), "r"(b[6]), "r"(b[7])
-                             : "memory");
+                store_bf16_weights(w + 16 * i, o, __bfloat162float(__float2bfloat16_rn(sch[u])));
             }
         }
     }
