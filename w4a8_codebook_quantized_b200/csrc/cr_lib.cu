@@ -42,7 +42,7 @@ struct DeviceState {
     std::atomic<bool> gemm_attr_set[cr::gm::kModes] = {};  // by gm::Mode
     std::atomic<bool> gemm_pair_attr_set[cr::gm::kModes] = {};
     std::atomic<bool> gemm_narrow_attr_set[cr::gm::kModes] = {};
-    std::atomic<bool> gemm_decode_attr_set[cr::gm::kModes] = {};
+    std::atomic<bool> gemm_decode_attr_set[2][cr::gm::kModes] = {};
     std::atomic<bool> gemv_attr_set{false};
     std::atomic<bool> gemv_split_attr_set{false};
     std::atomic<bool> gemv32_attr_set{false};
@@ -555,8 +555,8 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
 
 // The same for up to 128 rows on a packed weight (k_gemm_decode.cuh); w: the
 // bf16 weight to write, for a gradient.
-template <int MODE>
-cr_status launch_gemm_decode(DeviceState &d, const int8_t *xq, const uint8_t *qdata, const uint8_t *srel,
+template <int MODE, int TN>
+cr_status launch_gemm_decode_t(DeviceState &d, const int8_t *xq, const uint8_t *qdata, const uint8_t *srel,
                              const float *codebook, const CUtensorMap *to, int64_t M, int64_t N, int64_t K,
                              const GemmEpilogue &e, uint16_t *w, cudaStream_t stream)
 {
@@ -564,7 +564,7 @@ cr_status launch_gemm_decode(DeviceState &d, const int8_t *xq, const uint8_t *qd
     auto packed = [&](CUtensorMap *m, const uint8_t *base, int64_t row_bytes, uint32_t box_bytes) {
         const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)N};
         const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-        const cuuint32_t box[2] = {box_bytes, (cuuint32_t)gd::TN};
+        const cuuint32_t box[2] = {box_bytes, (cuuint32_t)TN};
         const cuuint32_t estr[2] = {1u, 1u};
         return g_encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(base), dims, strides, box, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -574,31 +574,48 @@ cr_status launch_gemm_decode(DeviceState &d, const int8_t *xq, const uint8_t *qd
     if (!make_tmap_i8(&ta, xq, (uint64_t)K, (uint64_t)M, (uint32_t)gm::a_box_rows(M)) || !packed(&tq, qdata, K / 2, 64u) ||
         !packed(&ts, srel, K / 16, 16u))
         return CR_ERR_CUDA;
-    if (!d.gemm_decode_attr_set[MODE]) {
-        if (cudaFuncSetAttribute((const void *)gd::gemm_decode_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)gd::smem_bytes<MODE>()) != cudaSuccess) {
+    auto kern = gd::gemm_decode_kernel<MODE, TN>;
+    constexpr int smem = (int)gd::smem_bytes<MODE, TN>();
+    std::atomic<bool> &set = d.gemm_decode_attr_set[TN == 64][MODE];
+    if (!set) {
+        if (cudaFuncSetAttribute((const void *)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
             cudaGetLastError();
             return CR_ERR_CUDA;
         }
-        d.gemm_decode_attr_set[MODE] = true;
+        set = true;
     }
-    const int64_t tiles = (N + gd::TN - 1) / gd::TN;
-    return launched(launch_dependent(gd::gemm_decode_kernel<MODE>, dim3((unsigned)(tiles < d.num_sms ? tiles : d.num_sms)),
-                                     gd::kThreads, (int)gd::smem_bytes<MODE>(), stream, ta, tq, ts, to ? *to : ta,
-                                     codebook, e.xs, e.ws, e.bias, (int)M, (int)N, (int)K, w, e.ex));
+    const int64_t tiles = (N + TN - 1) / TN;
+    return launched(launch_dependent(kern, dim3((unsigned)(tiles < d.num_sms ? tiles : d.num_sms)),
+                                     gd::Sizes<TN>::kThreads, smem, stream, ta, tq, ts, to ? *to : ta, codebook, e.xs,
+                                     e.ws, e.bias, (int)M, (int)N, (int)K, w, e.ex));
+}
+
+// Columns of a tile there: 64 where tiles of 128 would be for half of the SMs or
+// fewer (64 rows, tiles of 128 against 64: gated gradient 8192 x 1024 27.4 ->
+// 23.6 us, cross entropy 2000 x 1024 9.2 -> 7.7).
+int packed_tile(int64_t N) { return N > 74 * 128 ? 128 : 64; }
+
+template <int MODE>
+cr_status launch_gemm_decode(DeviceState &d, const int8_t *xq, const uint8_t *qdata, const uint8_t *srel,
+                             const float *codebook, const CUtensorMap *to, int64_t M, int64_t N, int64_t K,
+                             const GemmEpilogue &e, uint16_t *w, cudaStream_t stream)
+{
+    return packed_tile(N) == 64
+               ? launch_gemm_decode_t<MODE, 64>(d, xq, qdata, srel, codebook, to, M, N, K, e, w, stream)
+               : launch_gemm_decode_t<MODE, 128>(d, xq, qdata, srel, codebook, to, M, N, K, e, w, stream);
 }
 
 // Whether an int8 contraction on a packed weight decodes it on the way: for one
-// tile of rows, where there are tiles of columns for close to half of the SMs or
-// a short reduction (a CTA decodes its columns alone).  Weight decoded first
-// against on the way, 64 rows: cross entropy 32768 x 4096 56 -> 36 us, 10007 x
-// 1024 12.7 -> 9.9, 2000 x 1024 10.2 -> 9.2, but 3000 x 8192 24.6 -> 28.2; its
-// gradient 32768 x 4096 178 -> 130, 10007 x 1024 29.7 -> 28.2, but 2000 x 1024
-// 21.1 -> 23.3; gated gradient 12288 x 4096 74 -> 62, 128 x 256 12.6 -> 11.3, but
-// 2048 x 8192 41 -> 80.
-bool decode_on_the_way(int64_t M, int64_t N, int64_t K, bool gradient)
+// tile of rows, where the reduction is short or the weight at least as high as
+// it is wide (a CTA decodes its columns alone, one block of terms after another).
+// Weight decoded first against on the way, 64 rows: cross entropy 32768 x 4096
+// 56 -> 36 us, 5000 x 2048 13.7 -> 10.9, 2000 x 1024 10.2 -> 7.7, but 3000 x 8192
+// 24.5 -> 25.8; its gradient 32768 x 4096 178 -> 130, 5000 x 1024 24.9 -> 21.0,
+// but 500 x 4096 24.3 -> 32.6; gated gradient 12288 x 4096 74 -> 62, 512 x 1280
+// 19.0 -> 15.6, 128 x 256 12.4 -> 9.0, but 1024 x 4096 29.4 -> 33.9.
+bool decode_on_the_way(int64_t M, int64_t N, int64_t K)
 {
-    return M <= 128 && (N > 63 * 128 || K <= (gradient ? 512 : 1024));
+    return M <= cr::gm::BM && (K <= 1536 || N >= K);
 }
 
 // Whether an int8 contraction whose epilogue has exponentials runs on 128 x
@@ -1462,11 +1479,12 @@ int64_t ce_piece(int64_t V, int64_t per_entry)
 
 // Whether the decode GEMV makes the outputs: up to 8 rows, and up to twice that
 // in two passes over the packed codes where the reduction is long and the
-// contraction does not decode on the way (16 rows, 3000 x 8192: 17.1 us
-// against 24.4 with the weight decoded first).
+// columns are few (9 rows, two passes against the contraction: 3000 x 8192 16.8
+// against 24.5 us, 4096 x 4096 12.4 against 15.2; 8192 x 8192 28.1 against 26.0).
 bool ce_by_gemv(int64_t M, int64_t V, int64_t K)
 {
-    return M <= CR_GEMV_MAX_M || (M <= 2 * CR_GEMV_MAX_M && K >= 2048 && !decode_on_the_way(M, V, K, false));
+    return M <= CR_GEMV_MAX_M ||
+           (M <= 2 * CR_GEMV_MAX_M && K >= 2048 && (V <= 4096 || !decode_on_the_way(M, V, K)));
 }
 
 struct CeFwdWork {
@@ -1486,9 +1504,10 @@ struct CeFwdWork {
             slices = 0;
             y = static_cast<float *>(p.take(4 * M * V));
         } else {
-            const bool packed = decode_on_the_way(M, V, K, false);
-            narrow = packed || narrow_tiles(rows, piece < V ? piece : V, K);
-            slices = (V + (narrow ? 127 : 255)) / (narrow ? 128 : 256);
+            const bool packed = decode_on_the_way(M, V, K);
+            narrow = narrow_tiles(rows, piece < V ? piece : V, K);
+            const int64_t tile = packed ? packed_tile(V) : narrow ? 128 : 256;
+            slices = (V + tile - 1) / tile;
             if (packed)
                 piece = V;
             else
@@ -1615,7 +1634,7 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
     e.ws = s_channel;
     e.bias = bias;
     e.ex.dout = dout;
-    if (decode_on_the_way(M, N, K, true)) {
+    if (decode_on_the_way(M, N, K)) {
         st = launch_gemm_decode<gm::kSwigluGrad>(*d, xq, qdata, srel, codebook, &tz, M, N, K, e, w.w, stream);
     } else {
         st = launched(ew::launch_decode_both(qdata, srel, codebook, s_channel, N, K, w.w8, w.w, d->num_sms, stream));
@@ -1766,7 +1785,7 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
         for (int64_t n0 = 0; n0 < V; n0 += w.piece) {
             const int64_t n = V - n0 < w.piece ? V - n0 : w.piece, np = round_up(n, 8);
             const uint8_t *q = qdata + n0 * (K / 2), *s = srel + n0 * (K / 16);
-            const bool packed = decode_on_the_way(M, n, K, true);
+            const bool packed = decode_on_the_way(M, n, K);
             if (!packed)
                 st = launched(ew::launch_decode_both(q, s, codebook, s_channel + n0, n, K, w.w8, w.w, d->num_sms, stream));
             if (st != CR_OK)

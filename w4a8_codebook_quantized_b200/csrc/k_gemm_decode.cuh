@@ -6,10 +6,11 @@
 //
 // With one tile of rows every weight is wanted by one CTA only, and decoding it
 // to memory first (0.56 bytes read, 1 written, 1 read again) is most of the
-// work.  Here a CTA owns 128 columns (rows of the weight) at a time:
+// work.  Here a CTA owns TN = 128 columns (rows of the weight) at a time, or 64,
+// with half the decoding warps, where there are few tiles:
 //
 //   warp 0       TMA of A's 128-term blocks into the operand ring
-//   warp 1       tcgen05.mma kind::i8, 128 x 128 tiles, two accumulators
+//   warp 1       tcgen05.mma kind::i8, 128 x TN tiles, two accumulators
 //   warps 2..17  decode: codes, scales -> int8 in the operand ring's swizzled
 //                layout (and, for a gradient, the bf16 weight to memory);
 //                warps 2..9 do the tile's epilogue (k_gemm.cuh) after its last
@@ -20,8 +21,8 @@
 // against 219 with the weight decoded first; 128 rows 116 us; the gated gradient
 // of 17 x 12288 x 4096 60 us against 73.  Bound by the latency of the decoding
 // warps' chain (wait, two dependent shared-memory reads, decode, store, fence)
-// and by shared memory, which operand reads, TMA writes, table reads and stores
-// keep busy for some 750 of a block's 700 to 860 cycles: 17 x 131072 x 4096 took
+// and by shared memory (its pipe 62 % busy with the warps' accesses alone, beside
+// the MMAs' operands and the copies; issue slots 51 %): 17 x 131072 x 4096 took
 // 136 us with eight warps that handed over every block, 116 with two blocks at a
 // time, 100 with sixteen warps.  Eight copies of the table (no bank conflicts,
 // one slot of codes less) made no difference.
@@ -33,28 +34,33 @@
 namespace cr {
 namespace gd {
 
-constexpr int TN = 128;                     // columns of a tile
-constexpr int kStages = 4;                  // operand ring, 128 terms each
-constexpr int kStageBytes = gm::kABytes + TN * gm::BK;
-constexpr int kRaw = 3;                     // ring of packed codes, 256 terms each
-constexpr int kCodeBytes = TN * 64;         // codes of 128 terms
-constexpr int kScaleBytes = TN * 16;        // scales of 256 terms
-constexpr int kRawBytes = 2 * kCodeBytes + kScaleBytes;
+constexpr int kStages = 4;       // operand ring, 128 terms each
+constexpr int kRaw = 3;          // ring of packed codes, 256 terms each
 constexpr int kLutCopies = 4;
-constexpr int kDecoders = 512;              // threads of warps 2..17
-constexpr int kWorkers = 256;               // threads of warps 2..9: the epilogue
-constexpr int kThreads = 64 + kDecoders + 32;
-constexpr int kTmemCols = 2 * TN;
+constexpr int kWorkers = 256;    // threads of warps 2..9: the epilogue
 
-template <int MODE>
+// For tiles of TN columns.
+template <int TN>
+struct Sizes {
+    static constexpr int kStageBytes = gm::kABytes + TN * gm::BK;
+    static constexpr int kCodeBytes = TN * 64;   // codes of 128 terms
+    static constexpr int kScaleBytes = TN * 16;  // scales of 256 terms
+    static constexpr int kRawBytes = 2 * kCodeBytes + kScaleBytes;
+    static constexpr int kDecoders = 4 * TN;     // threads from warp 2 on that decode
+    static constexpr int kRawWarp = 2 + kDecoders / 32;
+    static constexpr int kThreads = 32 * (kRawWarp + 1);
+    static constexpr int kTmemCols = 2 * TN;
+};
+
+template <int MODE, int TN>
 struct __align__(1024) Smem {
-    uint8_t stage[kStages][kStageBytes];
-    uint8_t raw[kRaw][kRawBytes];
-    uint8_t epi[gm::epi_units(MODE)][gm::kEpiBytes];
+    uint8_t stage[kStages][Sizes<TN>::kStageBytes];
+    uint8_t raw[kRaw][Sizes<TN>::kRawBytes];
+    alignas(1024) uint8_t epi[gm::epi_units(MODE)][gm::kEpiBytes];
     uint4 lut[256 * kLutCopies];
     float wsb[2][TN];
     float biasb[2][TN];
-    uint64_t full[kStages];      // A has landed and the eight warps have decoded their parts of B
+    uint64_t full[kStages];      // A has landed and the decoding warps have written their parts of B
     uint64_t empty[kStages];
     uint64_t raw_full[kRaw];
     uint64_t raw_empty[kRaw];
@@ -64,17 +70,17 @@ struct __align__(1024) Smem {
     int abort;
 };
 
-template <int MODE>
+template <int MODE, int TN>
 constexpr size_t smem_bytes()
 {
-    static_assert(sizeof(Smem<MODE>) + 1024 <= gm::kMaxSmem, "shared memory of one CTA");
-    return sizeof(Smem<MODE>) + 1024;
+    static_assert(sizeof(Smem<MODE, TN>) + 1024 <= gm::kMaxSmem, "shared memory of one CTA");
+    return sizeof(Smem<MODE, TN>) + 1024;
 }
 
-// tmQ: qdata [N, K / 2] in boxes of 64 bytes x 128 rows; tmS: srel [N, K / 16]
-// in boxes of 16 bytes x 128 rows; w: bf16 [N, K] to write, or null.
-template <int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+// tmQ: qdata [N, K / 2] in boxes of 64 bytes x TN rows; tmS: srel [N, K / 16]
+// in boxes of 16 bytes x TN rows; w: bf16 [N, K] to write, or null.
+template <int MODE, int TN>
+__global__ void __launch_bounds__(Sizes<TN>::kThreads, 1)
     gemm_decode_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmOut,
                        const float *__restrict__ codebook, const float *__restrict__ xs, const float *__restrict__ ws,
@@ -82,7 +88,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const gm::EpiArgs ex)
 {
     extern __shared__ uint8_t smem_raw[];
-    Smem<MODE> &sh = smem_aligned_1024<Smem<MODE>>(smem_raw);
+    using S = Sizes<TN>;
+    constexpr int kDecoders = S::kDecoders, kCodeBytes = S::kCodeBytes;
+    Smem<MODE, TN> &sh = smem_aligned_1024<Smem<MODE, TN>>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kblocks = K / gm::BK, tiles = (N + TN - 1) / TN;
     if (threadIdx.x == 0) {
@@ -103,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 1) {
-        tmem_alloc(&sh.tmem_base, kTmemCols);
+        tmem_alloc(&sh.tmem_base, S::kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -145,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp == 18) {
+    } else if (warp == S::kRawWarp) {
         // ------------------------------------------------ TMA producer of codes and scales
         if (lane == 0) {
             prefetch_tmap(&tmQ);
@@ -159,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&sh.raw_full[slot], kRawBytes);
+                    mbar_arrive_expect_tx(&sh.raw_full[slot], S::kRawBytes);
                     tma_load_2d(sh.raw[slot], &tmQ, kb * 64, tile * TN, &sh.raw_full[slot]);
                     tma_load_2d(sh.raw[slot] + kCodeBytes, &tmQ, kb * 64 + 64, tile * TN, &sh.raw_full[slot]);
                     tma_load_2d(sh.raw[slot] + 2 * kCodeBytes, &tmS, kb * 8, tile * TN, &sh.raw_full[slot]);
@@ -196,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t st = (uint32_t)stage * (kStageBytes >> 4);
+                const uint32_t st = (uint32_t)stage * (S::kStageBytes >> 4);
                 if (issuer) {
 #pragma unroll
                     for (int kk = 0; kk < gm::BK / 32; ++kk)
@@ -218,8 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         {
             const uint4 e = lut_entry((uint32_t)et & 255u, codebook);
 #pragma unroll
-            for (int c = 0; c < kLutCopies / 2; ++c)
-                sh.lut[(et & 255) * kLutCopies + 2 * c + (et >> 8)] = e;
+            for (int c = et >> 8; c < kLutCopies; c += kDecoders / 256)
+                sh.lut[(et & 255) * kLutCopies + c] = e;
         }
         asm volatile("bar.sync 4, %0;" ::"n"(kDecoders) : "memory");
         const uint4 *lut = sh.lut + (et & (kLutCopies - 1));
@@ -292,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     raw_phase ^= 1u;
                 }
             }
-            if (warp >= 10)
+            if (kDecoders > kWorkers && et >= kWorkers)
                 continue;
             const int buf = local & 1;
             const uint32_t use = (uint32_t)(local >> 1) & 1u;
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, S::kTmemCols);
     }
 }
 
