@@ -50,7 +50,7 @@ def _work(name, *shape):
                                         (37, 1000, 768, True), (128, 256, 256, False), (129, 2824, 1280, True),
                                         (257, 512, 1024, False), (700, 6400, 256, True), (2500, 512, 1024, False),
                                         (3900, 3200, 1280, False), (1, 4096, 512, False), (9, 2824, 768, True), (5, 8200, 1280, True),
-                                        (33, 19208, 256, False), (128, 8320, 768, False), (100, 9600, 256, True)])
+                                        (33, 19208, 256, False), (128, 8320, 768, False), (100, 9600, 256, True), (333, 1416, 1280, True)])
 def test_swiglu_backward(M, N, K, bias):
     """One row to several tiles, ragged rows and columns (N / 2 a multiple of
     4 only), both GEMM forms; the reduction split for few tiles, and for the
@@ -125,7 +125,8 @@ CE_SHAPES = [(1, 1, 256, False), (1, 300, 512, True), (3, 4097, 256, False), (8,
              (100, 255, 512, True), (129, 1000, 256, False), (300, 10007, 256, True), (513, 5000, 1024, False),
              (9, 1, 2048, False), (12, 3001, 2048, True), (16, 1500, 2304, False), (17, 400, 2048, True),
              (10, 8200, 2048, False), (40, 20001, 256, True), (128, 9000, 768, False), (65, 8065, 1280, True),
-             (50, 9600, 512, False), (100, 2049, 2048, True), (128, 63, 1536, False)]
+             (50, 9600, 512, False), (100, 2049, 2048, True), (128, 63, 1536, False),
+             (300, 1100, 1536, True), (8300, 100, 256, False)]
 
 
 @pytest.mark.parametrize("M,V,K,bias", CE_SHAPES)

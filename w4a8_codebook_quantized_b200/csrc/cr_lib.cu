@@ -553,7 +553,7 @@ cr_status launch_gemm(DeviceState &d, const void *A, const void *B, const CUtens
     return launch_single(gm::gemm_kernel<MODE>, d.gemm_attr_set[MODE], gm::smem_bytes<MODE, gm::BN>());
 }
 
-// The same for up to 128 rows on a packed weight (k_gemm_decode.cuh); w: the
+// The same on a packed weight (k_gemm_decode.cuh), for few rows; w: the
 // bf16 weight to write, for a gradient.
 template <int MODE, int TN>
 cr_status launch_gemm_decode_t(DeviceState &d, const int8_t *xq, const uint8_t *qdata, const uint8_t *srel,
@@ -584,7 +584,7 @@ cr_status launch_gemm_decode_t(DeviceState &d, const int8_t *xq, const uint8_t *
         }
         set = true;
     }
-    const int64_t tiles = (N + TN - 1) / TN;
+    const int64_t tiles = (N + TN - 1) / TN * ((M + gm::BM - 1) / gm::BM);
     return launched(launch_dependent(kern, dim3((unsigned)(tiles < d.num_sms ? tiles : d.num_sms)),
                                      gd::Sizes<TN>::kThreads, smem, stream, ta, tq, ts, to ? *to : ta, codebook, e.xs,
                                      e.ws, e.bias, (int)M, (int)N, (int)K, w, e.ex));
@@ -593,29 +593,39 @@ cr_status launch_gemm_decode_t(DeviceState &d, const int8_t *xq, const uint8_t *
 // Columns of a tile there: 64 where tiles of 128 would be for half of the SMs or
 // fewer (64 rows, tiles of 128 against 64: gated gradient 8192 x 1024 27.4 ->
 // 23.6 us, cross entropy 2000 x 1024 9.2 -> 7.7).
-int packed_tile(int64_t N) { return N > 74 * 128 ? 128 : 64; }
+int packed_tile(int64_t M, int64_t N)
+{
+    return (M + 127) / 128 * ((N + 127) / 128) > 74 ? 128 : 64;
+}
 
 template <int MODE>
 cr_status launch_gemm_decode(DeviceState &d, const int8_t *xq, const uint8_t *qdata, const uint8_t *srel,
                              const float *codebook, const CUtensorMap *to, int64_t M, int64_t N, int64_t K,
                              const GemmEpilogue &e, uint16_t *w, cudaStream_t stream)
 {
-    return packed_tile(N) == 64
+    return packed_tile(M, N) == 64
                ? launch_gemm_decode_t<MODE, 64>(d, xq, qdata, srel, codebook, to, M, N, K, e, w, stream)
                : launch_gemm_decode_t<MODE, 128>(d, xq, qdata, srel, codebook, to, M, N, K, e, w, stream);
 }
 
 // Whether an int8 contraction on a packed weight decodes it on the way: for one
 // tile of rows, where the reduction is short or the weight at least as high as
-// it is wide (a CTA decodes its columns alone, one block of terms after another).
-// Weight decoded first against on the way, 64 rows: cross entropy 32768 x 4096
-// 56 -> 36 us, 5000 x 2048 13.7 -> 10.9, 2000 x 1024 10.2 -> 7.7, but 3000 x 8192
-// 24.5 -> 25.8; its gradient 32768 x 4096 178 -> 130, 5000 x 1024 24.9 -> 21.0,
-// but 500 x 4096 24.3 -> 32.6; gated gradient 12288 x 4096 74 -> 62, 512 x 1280
-// 19.0 -> 15.6, 128 x 256 12.4 -> 9.0, but 1024 x 4096 29.4 -> 33.9.
+// it is wide (a CTA decodes its columns alone, one block of terms after
+// another); for more, each of which decodes for itself, where the reduction is
+// short and the tiles of 64 columns are at most one for each SM.  Weight decoded
+// first against on the way, 64 rows: cross entropy 32768 x 4096 56 -> 36 us,
+// 5000 x 2048 13.7 -> 10.9, 2000 x 1024 10.2 -> 7.7, but 3000 x 8192 24.5 ->
+// 25.8; its gradient 32768 x 4096 178 -> 130, 5000 x 1024 24.9 -> 21.0, but 500 x
+// 4096 24.3 -> 32.6; gated gradient 12288 x 4096 74 -> 62, 512 x 1280 19.0 ->
+// 15.6, 128 x 256 12.4 -> 9.0, but 1024 x 4096 29.4 -> 33.9.  More rows: gated
+// gradient 333 x 2824 x 1280 29.8 -> 26.7, 500 x 2048 x 1024 27.0 -> 24.5, but
+// (128 columns a tile) 1000 x 2048 x 1024 27.1 -> 29.3, 500 x 2824 x 1280 30.7 ->
+// 31.3 and (a longer reduction) 500 x 2048 x 2048 29.1 -> 30.0.
 bool decode_on_the_way(int64_t M, int64_t N, int64_t K)
 {
-    return M <= cr::gm::BM && (K <= 1536 || N >= K);
+    if (M > cr::gm::BM)
+        return K <= 1536 && packed_tile(M, N) == 64;
+    return K <= 1536 || N >= K;
 }
 
 // Whether an int8 contraction whose epilogue has exponentials runs on 128 x
@@ -1506,7 +1516,7 @@ struct CeFwdWork {
         } else {
             const bool packed = decode_on_the_way(M, V, K);
             narrow = narrow_tiles(rows, piece < V ? piece : V, K);
-            const int64_t tile = packed ? packed_tile(V) : narrow ? 128 : 256;
+            const int64_t tile = packed ? packed_tile(M, V) : narrow ? 128 : 256;
             slices = (V + tile - 1) / tile;
             if (packed)
                 piece = V;
@@ -1712,7 +1722,7 @@ cr_status cr_w4a8_cross_entropy(const int8_t *xq, const float *xs, const uint8_t
             e.narrow = w.narrow;
             e.ex.tlogit = w.tlogit;
             st = w.w8 ? launch_gemm<gm::kCeStats>(*d, xq + m0 * K, w.w8, nullptr, rows, n, K, e, stream)
-                      : launch_gemm_decode<gm::kCeStats>(*d, xq, qdata, srel, codebook, nullptr, rows, n, K, e, nullptr,
+                      : launch_gemm_decode<gm::kCeStats>(*d, xq + m0 * K, qdata, srel, codebook, nullptr, rows, n, K, e, nullptr,
                                                          stream);
             if (st != CR_OK)
                 return st;
@@ -1785,7 +1795,7 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
         for (int64_t n0 = 0; n0 < V; n0 += w.piece) {
             const int64_t n = V - n0 < w.piece ? V - n0 : w.piece, np = round_up(n, 8);
             const uint8_t *q = qdata + n0 * (K / 2), *s = srel + n0 * (K / 16);
-            const bool packed = decode_on_the_way(M, n, K);
+            const bool packed = !w.compact && decode_on_the_way(M, n, K);
             if (!packed)
                 st = launched(ew::launch_decode_both(q, s, codebook, s_channel + n0, n, K, w.w8, w.w, d->num_sms, stream));
             if (st != CR_OK)

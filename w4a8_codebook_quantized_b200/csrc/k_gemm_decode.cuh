@@ -1,10 +1,10 @@
-// k_gemm_decode.cuh -- the int8 contraction of up to 128 rows on packed
-// weights: the codes are decoded into the tensor core's operand stages, so the
-// int8 weight is never stored.
+// k_gemm_decode.cuh -- the int8 contraction of few rows on packed weights: the
+// codes are decoded into the tensor core's operand stages, so the int8 weight is
+// never stored.
 //
-//   acc[m, n] = sum_k xq[m, k] * w8[n, k],   M <= 128
+//   acc[m, n] = sum_k xq[m, k] * w8[n, k]
 //
-// With one tile of rows every weight is wanted by one CTA only, and decoding it
+// With one tile of 128 rows every weight is wanted by one CTA only, and decoding it
 // to memory first (0.56 bytes read, 1 written, 1 read again) is most of the
 // work.  Here a CTA owns TN = 128 columns (rows of the weight) at a time, or 64,
 // with half the decoding warps, where there are few tiles:
@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(Sizes<TN>::kThreads, 1)
     constexpr int kDecoders = S::kDecoders, kCodeBytes = S::kCodeBytes;
     Smem<MODE, TN> &sh = smem_aligned_1024<Smem<MODE, TN>>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kblocks = K / gm::BK, tiles = (N + TN - 1) / TN;
+    const int kblocks = K / gm::BK, tiles_m = (M + gm::BM - 1) / gm::BM, tiles = (N + TN - 1) / TN * tiles_m;
+    // tile t: rows 128 (t % tiles_m), columns TN (t / tiles_m)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sh.full[s], 1 + kDecoders / 32);
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(Sizes<TN>::kThreads, 1)
                         break;
                     }
                     mbar_arrive_expect_tx(&sh.full[stage], bytes);
-                    tma_load_2d(sh.stage[stage], &tmA, kb * gm::BK, 0, &sh.full[stage]);
+                    tma_load_2d(sh.stage[stage], &tmA, kb * gm::BK, tile % tiles_m * gm::BM, &sh.full[stage]);
                     ++issued;
                     if (++stage == kStages) {
                         stage = 0;
@@ -162,15 +163,15 @@ __global__ void __launch_bounds__(Sizes<TN>::kThreads, 1)
             uint32_t phase = 0, issued = 0;
             bool ok = true;
             for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x)
-                for (int kb = 0; kb < kblocks; kb += 2) {
+                for (int kb = 0, n0 = tile / tiles_m * TN; kb < kblocks; kb += 2) {
                     if (!mbar_wait_bounded(&sh.raw_empty[slot], phase ^ 1u, abort)) {
                         ok = false;
                         break;
                     }
                     mbar_arrive_expect_tx(&sh.raw_full[slot], S::kRawBytes);
-                    tma_load_2d(sh.raw[slot], &tmQ, kb * 64, tile * TN, &sh.raw_full[slot]);
-                    tma_load_2d(sh.raw[slot] + kCodeBytes, &tmQ, kb * 64 + 64, tile * TN, &sh.raw_full[slot]);
-                    tma_load_2d(sh.raw[slot] + 2 * kCodeBytes, &tmS, kb * 8, tile * TN, &sh.raw_full[slot]);
+                    tma_load_2d(sh.raw[slot], &tmQ, kb * 64, n0, &sh.raw_full[slot]);
+                    tma_load_2d(sh.raw[slot] + kCodeBytes, &tmQ, kb * 64 + 64, n0, &sh.raw_full[slot]);
+                    tma_load_2d(sh.raw[slot] + 2 * kCodeBytes, &tmS, kb * 8, n0, &sh.raw_full[slot]);
                     ++issued;
                     if (++slot == kRaw) {
                         slot = 0;
@@ -239,11 +240,12 @@ __global__ void __launch_bounds__(Sizes<TN>::kThreads, 1)
         uint32_t units_issued = 0;
         bool ok = true;
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++local) {
+            const int tn = tile / tiles_m, row_base = tile % tiles_m * gm::BM;
             float sc[kItems];
             if constexpr (MODE != gm::kCeStats) {
 #pragma unroll
                 for (int u = 0; u < kItems; ++u) {
-                    const int n = tile * TN + ((et + kDecoders * u) >> 2);
+                    const int n = tn * TN + ((et + kDecoders * u) >> 2);
                     sc[u] = n < N ? __bfloat162float(__float2bfloat16_rn(ws[n])) : 0.0f;
                 }
             }
@@ -277,8 +279,8 @@ __global__ void __launch_bounds__(Sizes<TN>::kThreads, 1)
                         *reinterpret_cast<uint4 *>(b + 16 * ((2 * part + g) ^ (row & 7))) =
                             make_uint4(o[0], o[1], o[2], o[3]);
                         if constexpr (MODE != gm::kCeStats) {
-                            const int n = tile * TN + row;
-                            if (n < N)
+                            const int n = tn * TN + row;
+                            if (n < N && row_base == 0)  // the first tile of rows writes the weight
                                 store_bf16_weights(w + (int64_t)n * K + (kb + half) * gm::BK + 32 * part + 16 * g, o,
                                                    sc[u % kItems]);
                         }
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(Sizes<TN>::kThreads, 1)
             const int buf = local & 1;
             const uint32_t use = (uint32_t)(local >> 1) & 1u;
             if (et < TN) {
-                const int n = tile * TN + et, at = gm::stage_column<MODE>(et);
+                const int n = tn * TN + et, at = gm::stage_column<MODE>(et);
                 sh.wsb[buf][at] = n < N ? ws[n] : 0.0f;
                 sh.biasb[buf][at] = (bias != nullptr && n < N) ? bias[n] : 0.0f;
             }
@@ -322,8 +324,9 @@ __global__ void __launch_bounds__(Sizes<TN>::kThreads, 1)
                 if (lane == 0)
                     mbar_arrive(&sh.tmem_empty[buf]);
             };
-            if (32 * q < M) {
-                gm::epilogue_any<MODE, TN>(sh, warp - 2, buf, tbase, 32 * q, 32 * q, tile, tile * TN, lane, xs,
+            const int row0 = row_base + 32 * q;
+            if (row0 < M) {
+                gm::epilogue_any<MODE, TN>(sh, warp - 2, buf, tbase, row0, row0, tn, tn * TN, lane, xs,
                                            bias != nullptr, M, N, 0, 0, 1, &tmOut, units_issued, nullptr, nullptr, ws,
                                            bias, ex, wait, release);
             } else {  // none of the warp's rows exists
