@@ -372,6 +372,31 @@ def test_cross_entropy_forward_row_blocks():
     assert np.allclose(f64(lse[:50]), r_lse, rtol=1e-6) and np.allclose(f64(loss[:50]), r_loss, rtol=1e-5, atol=1e-6)
 
 
+@pytest.mark.parametrize("M,V,K", [(5, 1300, 256), (40, 3000, 1024), (12, 1000, 2048), (200, 2000, 512),
+                                   (300, 5000, 512), (200, 70001, 1024), (700, 24700, 1024)])
+def test_cross_entropy_gradient_of_padded_rows(M, V, K):
+    """Ignored rows get zeros whatever their activations' scale, lse, dloss and
+    int8 values are (a padded batch whose padding was never written), and the
+    other rows what they get beside clean ones: with the weight decoded on the
+    way (one tile of rows, and several), decoded first, in one piece and two,
+    and with the rows gathered."""
+    ly = inputs.layer(V, K, 61, with_bias=True)
+    xq, xs, xq_d, xs_d = _quantised(M, K, 62)
+    t = _targets(M, V, 63)
+    gone = t < 0
+    w, b = _layer_dev(ly)
+    _, lse = cr.cr_w4a8_cross_entropy(xq_d, xs_d, *w, dev(t), bias=b)
+    dloss = torch.rand(M, device="cuda") + 0.5
+    clean = cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(t), lse, dloss, bias=b)
+    assert torch.isfinite(clean).all() and (clean[dev(gone)] == 0).all()
+    idx = dev(np.flatnonzero(gone))
+    for bad in (float("nan"), float("inf"), -float("inf"), 3e38):
+        xs_d[idx], lse[idx], dloss[idx], xq_d[idx] = bad, bad, bad, -128
+        dx = Guarded((M, K), torch.bfloat16)
+        cr.cr_w4a8_cross_entropy_backward(xq_d, xs_d, *w, dev(t), lse, dloss, bias=b, dx=dx.tensor)
+        assert dx.intact() and torch.equal(dx.tensor, clean), bad
+
+
 @pytest.mark.parametrize("M", [6, 300])
 def test_work_buffers_aligned_to_16_bytes_only(M):
     """A work buffer of exactly the stated size at any 16-byte boundary."""

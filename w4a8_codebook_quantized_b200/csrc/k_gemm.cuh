@@ -103,14 +103,15 @@ struct EpiArgs {
     int slots = 1, max_splits = 1, split_tail = 0;
     const int *count = nullptr;        // the number of rows where it is known on the device only
 
-    // The factor of a row of the cross entropy's gradient: dloss, 0 in ignored
-    // rows, NaN in rows whose target is outside the vocabulary.
-    __device__ __forceinline__ float row_scale(int row) const
+    // Whether a row of the cross entropy's gradient takes part in the loss, and
+    // its factor then: dloss, NaN where the target is outside the vocabulary.
+    __device__ __forceinline__ bool takes_part(int row, float &factor) const
     {
         const int64_t t = targets[row];
         if (t == ignore)
-            return 0.0f;
-        return t >= 0 && t < V ? dloss[row] : __int_as_float(0x7FC00000);
+            return false;
+        factor = t >= 0 && t < V ? dloss[row] : __int_as_float(0x7FC00000);
+        return true;
     }
 };
 
@@ -295,7 +296,8 @@ __device__ __forceinline__ void store_half_unit(const uint32_t (&p)[16], int uco
 // thread stores its own row.  release() hands the accumulator back once every
 // column is in registers.
 // RAW: the accumulator holds fp32 values that are the outputs themselves
-// (bf16 GEMM; ROWS: times xm); no channel scales, bias or SwiGLU.  ADD: the fp32 outputs are added to
+// (bf16 GEMM; ROWS: times xm, and 0 in rows without row_ok, whose values may be
+// NaN); no channel scales, bias or SwiGLU.  ADD: the fp32 outputs are added to
 // what is there, by the bulk stores' own reduction (tma_out only).
 template <bool RAW, bool ROWS, bool ADD, int COLS, class Release>
 __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_base, int lane, float xm, bool row_ok,
@@ -315,7 +317,9 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tbase, int row0, int col_
             if constexpr (RAW) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    y[e] = ROWS ? __fmul_rn(__uint_as_float(v[j + e]), xm) : __uint_as_float(v[j + e]);
+                    y[e] = !ROWS    ? __uint_as_float(v[j + e])
+                           : row_ok ? __fmul_rn(__uint_as_float(v[j + e]), xm)
+                                    : 0.0f;
             } else {
                 const float4 w4 = *reinterpret_cast<const float4 *>(wsv + c0 + j);
                 const float4 b4 = *reinterpret_cast<const float4 *>(bsv + c0 + j);
@@ -704,8 +708,8 @@ __device__ __forceinline__ float2 epilogue_ce_stats(uint32_t tbase, int row, int
     return make_float2(ref, lo_of(s) + hi_of(s));
 }
 
-// Epilogue of kCeGrad: dl[m, n] = e^(y - lse[m]) - [n = target], zero for
-// ignored rows, to bf16; columns from N to the buffer's width (a multiple of
+// Epilogue of kCeGrad: dl[m, n] = e^(y - lse[m]) - [n = target] to bf16 (an
+// ignored row's values go nowhere: its outputs are not taken from the sum); columns from N to the buffer's width (a multiple of
 // 8) are written as zeros.  The row's factor dloss[m] is applied after the
 // contraction: dl at the target is then -1 rounded by at most the target's
 // probability, where -dloss itself would carry bf16's relative rounding, the
@@ -717,7 +721,7 @@ __device__ __forceinline__ void epilogue_ce_grad(uint32_t tbase, int row0, int c
                                                  uint8_t *stage_buf, uint32_t &units_issued, Release release)
 {
     const int row = row0 + lane;
-    float lse2 = __int_as_float(0x7F800000);  // an ignored row: every exponential 0
+    float lse2 = __int_as_float(0x7F800000);  // an ignored row: every exponential 0, where its outputs are finite
     int tcol = -1;
     if (row_ok) {
         const int64_t t = ex.targets[row];
@@ -783,9 +787,14 @@ __device__ __forceinline__ void epilogue_any(Sh &sh, int ew, int buf, uint32_t t
     if constexpr (!has_exponentials(MODE)) {
         if (!wait())
             return;
-        const float xm = !row_ok ? 0.0f : row_factor(MODE) ? ex.row_scale(row) : is_bf16(MODE) ? 0.0f : xs[row];
+        float xm = 0.0f;
+        bool live = row_ok;
+        if constexpr (row_factor(MODE))
+            live = row_ok && ex.takes_part(row, xm);
+        else if constexpr (!is_bf16(MODE))
+            xm = row_ok ? xs[row] : 0.0f;
         epilogue_tile<is_bf16(MODE), row_factor(MODE), MODE == kBf16RowsAdd, COLS>(
-            tbase + (uint32_t)c_lo, out_row0, out_col + c_lo, lane, xm, row_ok, wsv + c_lo, bsv + c_lo, has_bias, M, N,
+            tbase + (uint32_t)c_lo, out_row0, out_col + c_lo, lane, xm, live, wsv + c_lo, bsv + c_lo, has_bias, M, N,
             out_f32, swiglu, tma_out, tmOut, sh.epi[ew], units_issued, out, acc_out, ws, bias, release);
     } else {
         const int col_base = tile_n * TN;
