@@ -177,6 +177,26 @@ def test_norm_backward(M, K, gdt, dres):
         assert torch.equal(cr.cr_rmsnorm_backward(*args, dres=over, dx=over)[0], dx.tensor)
 
 
+@pytest.mark.parametrize("M,K", [(19, 256), (19, 512), (19, 768), (19, 4352), (19, 12288), (19, 16640), (19, 33024)])
+@pytest.mark.parametrize("dres", [False, True])
+def test_norm_backward_of_large_and_small_rows(M, K, dres):
+    """Rows of every size the norm takes: rs is their inverse, and its square
+    leaves fp32 at both ends (rs * rs * 1e25^2 is not what the formula has)."""
+    dr, h, gamma, _, dd = _grad_inputs(M, K, 71, torch.float32, dres)
+    scale = 10.0 ** np.array([25, 33, -14, 0, 20, 23, 30, 34, -10, 28, 22, 19, 18, 32, 5, -5, 10, 24, 26])[:M]
+    h = to_bf16(f64(h) / 20 * scale[:, None])  # inputs.activations has values up to about 100
+    dr = to_bf16(f64(dr) * np.minimum(scale, 1.0)[:, None])  # dx stays a normal number
+    if dd is not None:
+        dd = to_bf16(f64(dd) / np.maximum(scale, 1.0)[:, None])
+    eps = 1e-30
+    rs = (1 / np.sqrt((f64(h) ** 2).mean(1) + eps)).astype(np.float32)
+    g = gamma.astype(np.float64)
+    dx, dg = cr.cr_rmsnorm_backward(dr.cuda(), h.cuda(), dev(gamma), dev(rs), dres=None if dd is None else dd.cuda())
+    rx, rg, ex, eg = norm_backward(f64(dr), f64(h), g, rs.astype(np.float64), None if dd is None else f64(dd))
+    assert_bf16_near(dx, rx, ex, "dx")
+    assert (np.abs(f64(dg) - rg) <= eg * 2.0 ** -24).all()
+
+
 def test_norm_backward_against_differences():
     """The gradient against central differences of the forward's real-valued
     function: sum(dr * R(norm(h) * gamma)), in float64."""

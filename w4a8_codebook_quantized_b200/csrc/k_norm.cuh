@@ -867,7 +867,9 @@ __device__ __forceinline__ float block_sum(float s, float (*warp_sum)[THREADS / 
 // neighbouring elements.  V = 16 dv comes out of the rotation; the 1/16 (exact)
 // sits in rs16 = rs / 16: with
 //   g' = V * gamma,  xh' = h * rs16:  V * xh' = dv * xh,  g' * xh' = g * xh,
-//   dx = g' * rs16 + (h * (-rs * rs * c) + dres).
+//   dx = (g' - h * (16 c rs)) * rs16 + dres.
+// (No rs * rs, which leaves fp32 for rows above 1e19; where 16 c rs is subnormal
+// its lost bits change dx by less than 2^-140.)
 struct BwdBlock {
     uint32_t d[8], h[8], r[8];  // dr, h and dres of the block's sixteen elements
 
@@ -904,12 +906,12 @@ struct BwdBlock {
     }
     __device__ __forceinline__ void finish(const BwdArgs &a, int64_t at, const uint64_t (&g)[8], float rs, float c) const
     {
-        const uint64_t rs16 = pair_both(rs * 0.0625f), k = pair_both(-(rs * rs) * c);
+        const uint64_t rs16 = pair_both(rs * 0.0625f), k = pair_both(-16.0f * c * rs);
         uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             uint32_t lo, hi;
-            unpack2(fma2(g[i], rs16, fma2(pair_of(h[i]), k, pair_of(r[i]))), lo, hi);
+            unpack2(fma2(fma2(pair_of(h[i]), k, g[i]), rs16, pair_of(r[i])), lo, hi);
             o[i] = to_bf16x2_bits(__uint_as_float(lo), __uint_as_float(hi));
         }
         store16(a.dx + at, a.wide, o);
@@ -1084,12 +1086,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 320 ? 2 : 0) rmsnorm_backw
     };
     auto finish = [&](int64_t at, const uint64_t (&g)[8], const uint32_t (&hp)[8], const uint32_t (&r)[8], float rs,
                       float c) {
-        const uint64_t rs16 = pair_both(rs * 0.0625f), k = pair_both(-(rs * rs) * c);
+        const uint64_t rs16 = pair_both(rs * 0.0625f), k = pair_both(-16.0f * c * rs);
         uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             uint32_t lo, hi;
-            unpack2(fma2(g[i], rs16, fma2(pair_of(hp[i]), k, pair_of(r[i]))), lo, hi);
+            unpack2(fma2(fma2(pair_of(hp[i]), k, g[i]), rs16, pair_of(r[i])), lo, hi);
             o[i] = to_bf16x2_bits(__uint_as_float(lo), __uint_as_float(hi));
         }
         store16(a.dx + at, a.wide, o);
