@@ -2,6 +2,9 @@
 (nothing is launched on these paths), and the restatements the GPU tests use
 against each other and against the oracle."""
 import ctypes
+import glob
+import os
+import re
 
 import numpy as np
 import pytest
@@ -234,3 +237,22 @@ def test_written_buffers_overlap_nothing(L):
                                                 need, None)
 
     pairs(ce_backward, [10, 11], list(range(10)))
+
+
+def test_shared_arrays_written_in_wide_words_say_their_alignment():
+    """A shared array of bytes, words or floats that a kernel accesses in words
+    of 8 or 16 bytes declares the alignment: its element type alone promises 1
+    to 4 bytes, and a misaligned access is a fault."""
+    wide = r"(?:store_partial\(\s*&?|reinterpret_cast<(?:const )?(?:uint4|uint2|float4|float2|ulonglong2|uint64_t) \*>\(\s*&?)"
+    declared = 0
+    for path in sorted(glob.glob(os.path.join(build.CSRC, "*.cuh"))):
+        for kernel in re.split(r"__global__", open(path).read())[1:]:
+            for line, name in re.findall(r"(__shared__[^;]*?\b(\w+)(?:\[[^;]*\])+;)", kernel):
+                if not re.search(r"\b(float|int|uint32_t|int32_t|uint16_t|uint8_t|int8_t)\b", line):
+                    continue
+                declared += 1
+                used = {name} | set(re.findall(r"\*(\w+) = &?%s\b" % name, kernel))
+                for n in used:
+                    if re.search(wide + n + r"\b", kernel):
+                        assert "__align__" in line, f"{os.path.basename(path)}: {line}"
+    assert declared > 20

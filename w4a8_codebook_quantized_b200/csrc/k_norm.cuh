@@ -940,7 +940,7 @@ template <int G, bool GBF16>
 __global__ void __launch_bounds__(128) rmsnorm_backward_small_kernel(const BwdArgs a)
 {
     __shared__ __align__(16) float tr_all[8][16 * 16 + 16];
-    __shared__ float share[8][256];
+    __shared__ __align__(16) float share[8][256];  // written in 16-byte words (store_partial)
     asm volatile("griddepcontrol.launch_dependents;" :::);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int hw = threadIdx.x >> 4, L = threadIdx.x & 15, b = hw % G;
