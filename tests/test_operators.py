@@ -256,3 +256,18 @@ def test_shared_arrays_written_in_wide_words_say_their_alignment():
                     if re.search(wide + n + r"\b", kernel):
                         assert "__align__" in line, f"{os.path.basename(path)}: {line}"
     assert declared > 20
+
+
+def test_gradient_work_holds_no_weight_that_is_decoded_on_the_way(L):
+    """The cross entropy's gradient of few rows keeps the bf16 weight of a piece
+    but not its int8 grid, unless a piece (the short last one too) needs it."""
+    f = L.cr_w4a8_cross_entropy_backward_work_bytes
+    slack = 1 << 20
+    for M, V, K in ((64, 8192, 4096), (1, 16384, 4096), (40, 20001, 1024)):  # one piece: bf16 weight, dl, fp32 sums, copies
+        copies = 20 << 20
+        assert f(M, V, K) <= 2 * V * K + 2 * (V + 8) * M + 4 * M * K + copies + slack
+    assert f(64, 32768, 4096) <= 2 * 16384 * 4096 + 2 * 16384 * 64 + 4 * 64 * 4096 + (20 << 20) + slack  # two pieces
+    assert f(64, 2048, 8192) >= 3 * 2048 * 8192   # fewer columns than terms: decoded first
+    assert f(300, 9000, 2048) >= 3 * 9000 * 2048  # three tiles of rows, long reduction
+    assert f(900, 20011, 1024) >= 3 * 20011 * 1024  # rows gathered
+    assert f(20, 128 * 32768 + 1, 2048) >= 3 * 32768 * 2048  # 129 pieces, the last of one entry

@@ -1534,7 +1534,7 @@ struct CeFwdWork {
 // (4096 x 65536 x 4096, 10 percent ignored: 2671 -> 2385 us with the split
 // last wave; 500 x 10007 x 1024, half ignored: 43.2 -> 44.8 us, so not there).
 struct CeBwdWork {
-    int64_t rows, piece;
+    int64_t all_rows, rows, piece, K;
     int8_t *w8;
     uint16_t *w, *dl;
     float *acc, *copies;  // fp32 sums over the pieces: whole tiles, and the copies of split ones
@@ -1542,13 +1542,17 @@ struct CeBwdWork {
     cr::ce::CompactArgs c = {};
     KnPlan plan;
     int64_t bytes;
-    CeBwdWork(void *work, int64_t M, int64_t V, int64_t K)
-        : rows(M < kBwdRows ? M : kBwdRows), piece(ce_piece(V, rows > K ? rows : K)), compact(M > 256 && (double)M * (double)V * (double)K >= 17179869184.0),
+    // Whether the contraction of a piece of n entries decodes its weight on the way.
+    bool packed(int64_t n) const { return !compact && decode_on_the_way(all_rows, n, K); }
+    CeBwdWork(void *work, int64_t M, int64_t V, int64_t K_)
+        : all_rows(M), rows(M < kBwdRows ? M : kBwdRows), piece(ce_piece(V, rows > K_ ? rows : K_)), K(K_),
+          compact(M > 256 && (double)M * (double)V * (double)K >= 17179869184.0),
           plan(rows, K, piece < V ? piece : V)
     {
         Parts p(work);
-        const int64_t most = piece < V ? piece : round_up(V, 8);
-        w8 = static_cast<int8_t *>(p.take(most * K));
+        const int64_t most = piece < V ? piece : round_up(V, 8), last = (V - 1) % piece + 1;
+        // the int8 grid of a piece: the last piece is the only one of another length
+        w8 = packed(piece < V ? piece : V) && packed(last) ? nullptr : static_cast<int8_t *>(p.take(most * K));
         w = static_cast<uint16_t *>(p.take(2 * most * K));
         dl = static_cast<uint16_t *>(p.take(2 * most * rows));
         acc = static_cast<float *>(p.take(4 * rows * K));
@@ -1795,7 +1799,7 @@ cr_status cr_w4a8_cross_entropy_backward(const int8_t *xq, const float *xs, cons
         for (int64_t n0 = 0; n0 < V; n0 += w.piece) {
             const int64_t n = V - n0 < w.piece ? V - n0 : w.piece, np = round_up(n, 8);
             const uint8_t *q = qdata + n0 * (K / 2), *s = srel + n0 * (K / 16);
-            const bool packed = !w.compact && decode_on_the_way(M, n, K);
+            const bool packed = w.packed(n);
             if (!packed)
                 st = launched(ew::launch_decode_both(q, s, codebook, s_channel + n0, n, K, w.w8, w.w, d->num_sms, stream));
             if (st != CR_OK)
