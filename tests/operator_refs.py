@@ -170,3 +170,55 @@ def cross_entropy_backward(layer, xq, xs, targets, lse, dloss, ignore=-100):
     e_dx = (2.0 ** -8 * np.abs(d) + 2 * e + 2.0 ** -133) @ np.abs(w)
     e_dx = e_dx + y.shape[1] * 2.0 ** -24 * (np.abs(d) @ np.abs(w))
     return d @ w, e_dx
+
+
+def silence_targets(layer, entries):
+    """Zero group scales, so zero weights, in a head's rows `entries`: as targets
+    they leave only the softmax part of the gradient, which the target's -1
+    otherwise outweighs by far."""
+    layer.srel[entries] = 0
+    return layer
+
+
+def softmax_gradient(layer, xq, xs, lse, dloss, device="cpu", drop=None, columns=8192):
+    """The cross entropy's input gradient of rows whose targets have zero
+    weights, and the size of its error: (dx, sigma) float64 tensors, sigma the
+    root of the sum of the squares of its terms, computed `columns` vocabulary
+    entries at a time.  drop = (a, b): without the entries a .. b - 1 (a planted
+    mistake)."""
+    t64 = lambda a: torch.as_tensor(np.asarray(a, dtype=np.float64), device=device)
+    x, scale, base, d = t64(xq), t64(xs)[:, None], t64(lse)[:, None], t64(dloss)[:, None]
+    dx, sq = torch.zeros_like(x), torch.zeros_like(x)
+    for a in range(0, layer.N, columns):
+        s = slice(a, min(a + columns, layer.N))
+        w8 = t64(oracle.decode_w8(layer.qdata[s], layer.srel[s], layer.codebook))
+        ch = torch.as_tensor(layer.s_channel[s], device=device)
+        y = (x @ w8.T) * scale * ch.double()
+        if layer.bias is not None:
+            y += t64(layer.bias[s])
+        p = torch.exp(y - base) * d
+        if drop is not None:
+            p[:, max(0, drop[0] - a):max(0, drop[1] - a)] = 0
+        w = (w8 * ch.to(torch.bfloat16).double()[:, None]).to(torch.bfloat16).double()
+        dx += p @ w
+        sq += (p * p) @ (w * w)
+    return dx, sq.sqrt()
+
+
+def assert_sum_of_random_terms(got, ref, sigma, terms, rel=0.0, what=""):
+    """got (bf16) is ref, a sum of `terms` products of signs that are
+    independent of the errors, each factor rounded to bf16 once at most
+    (2^-8), added up in fp32 in any order, rounded once.
+
+    A sum of terms a_i e_i with |e_i| <= 2^-8 and random signs is beyond 7 *
+    2^-8 * sigma, sigma^2 = sum a_i^2, with a probability of 2 exp(-49 / 2) =
+    5e-11 (Hoeffding).  The sum's own roundings: terms / 16 additions of the
+    tensor core's groups (and some 64 of a split's joining), each cut off by at
+    most 2^-23 of a partial sum, which is below 7 sigma by the same bound (plus
+    the mean's share, below |ref|).  rel: an error all terms have in common."""
+    g = got.double().cpu()
+    r, s = ref.cpu(), sigma.cpu()
+    add = (terms / 16 + 64) * 2.0 ** -23 * (7 * s + r.abs())
+    inner = 7 * 2.0 ** -8 * s + add + rel * r.abs()
+    bad = (g - r).abs() > 2.0 ** -8 * (r.abs() + inner) + inner + 2.0 ** -133
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {g.numel()} off"

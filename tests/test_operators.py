@@ -14,7 +14,8 @@ import oracle
 import w4a8_codebook_quantized_b200 as cr
 from w4a8_codebook_quantized_b200 import build, inputs
 
-from operator_refs import hadamard, norm_backward, norm_quant, rotate32, rotate64
+from operator_refs import (assert_sum_of_random_terms, cross_entropy, gradient_weight, hadamard, norm_backward,
+                           norm_quant, rotate32, rotate64, silence_targets, softmax_gradient)
 
 A, B, C = 0x10000, 0x4000000, 0x8000000  # aligned stand-in addresses far apart; never dereferenced
 MIS = 0x10008
@@ -271,3 +272,34 @@ def test_gradient_work_holds_no_weight_that_is_decoded_on_the_way(L):
     assert f(300, 9000, 2048) >= 3 * 9000 * 2048  # three tiles of rows, long reduction
     assert f(900, 20011, 1024) >= 3 * 20011 * 1024  # rows gathered
     assert f(20, 128 * 32768 + 1, 2048) >= 3 * 32768 * 2048  # 129 pieces, the last of one entry
+
+
+@pytest.mark.parametrize("M,V,K", [(20, 20011, 256), (3, 6000, 512), (300, 5000, 256)])
+def test_gradient_comparison_sees_a_missing_tile(M, V, K):
+    """The comparison that the GPU tests of every tile use: it passes the
+    formula with dl rounded to bf16 and fp32 sums, and fails it without one tile
+    of 64 or 128 entries, or a ragged last one of 13, of the reduction."""
+    ly = inputs.layer(V, K, 5)
+    at = np.array([0, V // 3, V // 2, V - 2])
+    silence_targets(ly, at)
+    rng = np.random.default_rng([M, V, K])
+    z = rng.standard_normal((M, K))
+    xq = np.rint(z * (127 / np.abs(z).max(1, keepdims=True))).astype(np.int8)
+    xs = rng.uniform(0.02, 0.05, M).astype(np.float32)
+    t = at[rng.integers(0, len(at), M)]
+    _, lse, y = cross_entropy(ly, xq, xs, t)
+    lse32, dloss = lse.astype(np.float32), rng.uniform(0.5, 1, M).astype(np.float32)
+    dl = torch.exp(torch.from_numpy(y).float() - torch.from_numpy(lse32)[:, None])
+    dl[torch.arange(M), torch.from_numpy(t)] -= 1
+    w = torch.from_numpy(gradient_weight(ly)).float()
+    got = ((dl.to(torch.bfloat16).float() @ w) * torch.from_numpy(dloss)[:, None]).to(torch.bfloat16)
+    rel = 2.0 ** -24 * (2 * np.abs(lse).max() + 8)
+
+    def check(drop=None):
+        ref, sigma = softmax_gradient(ly, xq, xs, lse32, dloss, drop=drop, columns=4096)
+        assert_sum_of_random_terms(got, ref, sigma, V, rel)
+
+    check()
+    for drop in ((1, 129), (256, 320), (V // 2 // 64 * 64 - 64, V // 2 // 64 * 64), (4096 - 64, 4096), (V - 15, V)):
+        with pytest.raises(AssertionError):
+            check(drop)
