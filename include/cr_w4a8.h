@@ -634,7 +634,8 @@ cr_status cr_rotate(const uint16_t *x, int64_t M, int64_t K, uint16_t *out, cr_s
  * activations of the forward; the interleaved layer as in (9).  dx [M, K] bf16,
  * dz [M, N] bf16, written.  N must be a multiple of 8 (CR_ERR_UNSUPPORTED
  * otherwise); N == 0 writes dx = 0.  work: at least
- * cr_w4a8_swiglu_backward_work_bytes(M, N, K) bytes (the decoded weight, 3 N K,
+ * cr_w4a8_swiglu_backward_work_bytes(M, N, K) bytes (3 N K for the decoded weight
+ * as bf16 and int8, the latter unused where the contraction decodes on the way,
  * and up to 20 MB for a split reduction), 16-byte aligned; CR_ERR_INVALID_ARG
  * when smaller.  Nothing is allocated.
  */
@@ -654,25 +655,32 @@ cr_status cr_w4a8_swiglu_backward(const uint16_t *dout, const int8_t *xq, const 
  *   lse[m]  = log sum_n e^y[m, n]
  *   loss[m] = lse[m] - y[m, targets[m]];  0 where targets[m] == ignore_index;
  *             NaN where the target is any other value outside 0 .. V - 1
- * A bias of -inf takes an entry out of the softmax.  V >= 1 (CR_ERR_INVALID_ARG
- * otherwise), any V.  M <= 8 takes the decode GEMV.
+ * A bias of -inf takes an entry out of the softmax, and so does one below
+ * -2.3e38 (the type's lowest value); outputs above 2^127 are unspecified.
+ * V >= 1 (CR_ERR_INVALID_ARG otherwise), any V.  Up to 8 rows take the decode
+ * GEMV; 9 to 16 rows take two passes of it where K >= 2048 and V <= 4096 or
+ * V < K.
  *
  * xq [>= M, K] int8, xs [>= M] fp32, the layer as in (3); targets [M] int64.
  * loss [M], lse [M] fp32, written.  work: at least
  * cr_w4a8_cross_entropy_work_bytes(M, V, K) bytes, 16-byte aligned
- * (CR_ERR_INVALID_ARG when smaller): a decoded piece of the weight (64 MB or
- * 256 K bytes, whichever is more) and 8 bytes per row (of at most 32768 at a
- * time) and 256 outputs, 128 for short problems; with the decode GEMV (up to 8
- * rows, up to 16 of some layers) the M V fp32 outputs themselves.  Nothing is allocated.  Results are the same from run to
- * run; between batch sizes the sums' order, and so the last bits, may differ.
+ * (CR_ERR_INVALID_ARG when smaller): a decoded piece of the weight (up to 64 MB
+ * or 256 K bytes, whichever is more; none where the contraction decodes on the
+ * way, as for few rows) and 8 bytes per row (of at most 32768 at a time) and
+ * 256 outputs (128 or 64 for short problems and few rows); with the decode GEMV
+ * the M V fp32 outputs themselves instead.  Nothing is allocated.  Results are
+ * the same from run to run; between batch sizes the sums' order, and so the
+ * last bits, may differ.
  *
  * (23b) Its gradient with respect to the layer's rotated input:
  *   dl[m, n] = bf16( e^(y[m, n] - lse[m]) - [n == targets[m]] )
  *   dx[m, k] = bf16( dloss[m] * sum_n dl[m, n] * w[n, k] )   (w as in (13); the sum in fp32);
  *              0 in ignored rows, NaN in rows with an invalid target
  * lse from (23) on the same arguments; dloss [M] fp32, the gradient of loss
- * (1 / count for the mean over count rows).  dx [M, K] bf16, written: (20) or (21) take it back.  Ignored rows cost little: in larger problems the others
- * are gathered first.  work: at least
+ * (1 / count for the mean over count rows).  dx [M, K] bf16, written: (20) or
+ * (21) take it back.  In ignored rows xq, xs, lse and dloss may hold anything,
+ * NaN too.  They cost little: in larger problems the others are gathered first.
+ * work: at least
  * cr_w4a8_cross_entropy_backward_work_bytes(M, V, K) bytes (some 0.5 GB at most
  * for K = 4096).
  */
